@@ -407,6 +407,55 @@ sffn_status sffn_hybrid_check(sffn_handle* h, const sffn_hybrid* hy, hipStream_t
 sffn_status sffn_check(sffn_handle* h, hipStream_t stream);
 
 /*
+ * Microscaled 4-bit floating point (MXFP4). A matrix of R rows and K
+ * columns is kept with one power-of-two scale for every 32 consecutive
+ * elements of a row; an element is the scale times a signed e2m1 value (0,
+ * 0.5, 1, 1.5, 2, 3, 4 or 6). With Kp = K rounded up to 128:
+ *   codes   [R, Kp / 2] bytes: element k of a row is in byte k / 2, the
+ *           even element in the low nibble (bit 3 the sign); the elements
+ *           from K on are 0
+ *   scales  [Kp / 128, R, 4] bytes: byte b of (g, r) is the scale's
+ *           exponent plus 127 for elements 128 g + 32 b .. + 31 of row r;
+ *           255 makes those elements NaN
+ * sffn_mx_bytes gives the two sizes. The calls take no handle: they run on
+ * the current device, on the caller's stream, allocate nothing and keep no
+ * state, so calls on different streams may overlap. Sizes: R up to 2^27
+ * (products: up to 2^21 rows in either operand), K up to 2^22; a size of 0
+ * is valid (nothing is written; a product over K = 0 writes zeros). Codes
+ * must be 16-byte and scales 4-byte aligned; float matrices need only their
+ * elements' alignment (loads and stores are wider where 16-byte alignment
+ * of pointer and row stride allows).
+ */
+sffn_status sffn_mx_bytes(int64_t rows, int64_t cols, size_t* code_bytes, size_t* scale_bytes);
+
+/* Quantise x (dtype SFFN_F32 or SFFN_BF16, [rows, cols], row stride ldx >=
+ * cols elements). transposed = 0: codes and scales describe x, blocks along
+ * its rows (R = rows, K = cols). transposed = 1: they describe x^T (R =
+ * cols, K = rows): the form of a weight stored [F, d] whose product
+ * contracts over F, such as w_down's. A block's exponent is that of its
+ * largest magnitude less 2, at least -127; elements round to the nearest
+ * value (ties to the even code) and saturate at 6. A block that holds an
+ * infinity or a NaN becomes NaN as a whole. */
+sffn_status sffn_mx_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                             int32_t transposed, uint8_t* codes, uint8_t* scales,
+                             hipStream_t stream);
+
+/* The values the codes stand for, [rows, cols] of dtype (SFFN_F32 or
+ * SFFN_BF16) with row stride ldo >= cols elements; exact. */
+sffn_status sffn_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                               int64_t cols, void* out, int32_t dtype, int64_t ldo,
+                               hipStream_t stream);
+
+/* out[m, n] = sum_k a[m, k] b[n, k] of two MXFP4 matrices with the same K:
+ * a [M, K] (tokens), b [N, K] (an nn.Linear weight or any neuron-major
+ * one). Products are exact, sums float32, out float32 or bf16 (out_dtype;
+ * rounded once), [M, N] with row stride ldo >= N elements. Deterministic.
+ * A float32 out with ldo = N = d_ff is what sffn_pack_twell takes as z. */
+sffn_status sffn_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
+                           const uint8_t* b_codes, const uint8_t* b_scales, int64_t N, int64_t K,
+                           void* out, int32_t out_dtype, int64_t ldo, hipStream_t stream);
+
+/*
  * Per-kernel timing. While enabled, every kernel launch of the library is
  * bracketed by two HIP events recorded on the call's stream, so that each
  * interval holds one kernel id's launches alone. sffn_profile_read waits

@@ -41,7 +41,8 @@ EXPORTS = ("sffn_create", "sffn_destroy", "sffn_last_error", "sffn_status_string
            "sffn_kernel_name", "sffn_hybrid_compact", "sffn_forward_train",
            "sffn_hybrid_check", "sffn_backward", "sffn_forward_noalloc",
            "sffn_choose_mode", "sffn_train_dense_act_bytes", "sffn_forward_train_dense",
-           "sffn_backward_dense")
+           "sffn_backward_dense", "sffn_mx_bytes", "sffn_mx_quantize", "sffn_mx_dequantize",
+           "sffn_mx_matmul")
 SFFN_K_COUNT = 24
 
 
@@ -132,6 +133,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sffn_backward.argtypes = [vp, vp, vp, vp, vp, ctypes.POINTER(SffnHybrid), vp, i64,
                                   vp, vp, vp, vp, ctypes.c_float, vp, sz, vp]
     lib.sffn_backward.restype = i32
+    lib.sffn_mx_bytes.argtypes = [i64, i64, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+    lib.sffn_mx_bytes.restype = i32
+    lib.sffn_mx_quantize.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp]
+    lib.sffn_mx_quantize.restype = i32
+    lib.sffn_mx_dequantize.argtypes = [vp, vp, i64, i64, vp, i32, i64, vp]
+    lib.sffn_mx_dequantize.restype = i32
+    lib.sffn_mx_matmul.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, i32, i64, vp]
+    lib.sffn_mx_matmul.restype = i32
     _lib = lib
     return lib
 
@@ -469,7 +478,8 @@ class SparseFFN:
                                                  _ptr(w_down), _ptr(act), _ptr(dy), T, _ptr(dx),
                                                  _ptr(dwg), _ptr(dwu), _ptr(dwd),
                                                  float(l1_coeff), ws, nb, _stream()),
-                    "sffn_backward_dense")
+                    "sffn_backward_dense", "sffn_mx_bytes", "sffn_mx_quantize", "sffn_mx_dequantize",
+           "sffn_mx_matmul")
         return dx, dwg, dwu, dwd
 
     def hybrid_check(self, hy) -> int:

@@ -71,6 +71,8 @@ typedef int32_t sffn_status;
 /* element type of x, the weights and dy */
 #define SFFN_F32  0
 #define SFFN_BF16 1
+/* element type of an expert layer's weights (microscaled 4-bit, below) */
+#define SFFN_MXFP4 2
 
 /* forward modes */
 #define SFFN_SPARSE 0   /* gate GEMM + TwELL, sparse up/down, dense path for flagged rows */
@@ -454,6 +456,83 @@ sffn_status sffn_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int6
 sffn_status sffn_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
                            const uint8_t* b_codes, const uint8_t* b_scales, int64_t N, int64_t K,
                            void* out, int32_t out_dtype, int64_t ldo, hipStream_t stream);
+
+/*
+ * A whole mixture-of-experts layer for few tokens (decoding batches). With
+ * the router l = x W_r^T, the k = top_k experts e(0), e(1), .. of a token in
+ * descending order of l (ties: the lower expert first) and p their softmax
+ * weights,
+ *   y = sum_r p_r (ReLU(x W_g,e(r)) * (x W_u,e(r))) W_d,e(r)     gated
+ *   y = sum_r p_r ReLU(x W_1,e(r)) W_2,e(r)                      non-gated
+ * Only the selected experts' weights are read, the up and down rows only of
+ * neurons that are active (strictly z > 0, as everywhere here) for one of
+ * the tokens. Logits are summed in 64 bits, so that the choice of experts
+ * does not depend on an order of summation; everything else in float32, h
+ * entering the down product with 16 significant bits. Results repeat bit
+ * for bit.
+ *   d          model width; d % 128 == 0, d <= 8192
+ *   d_ff       F, neurons an expert; F % 32 == 0, F <= 65536
+ *   n_experts  E <= 1024, E F <= 2^27
+ *   top_k      k <= min(E, 32)
+ *   gated      1 gated, 0 non-gated
+ *   normalize  1: p is the softmax over the token's k experts; 0: over all
+ *              E (the k weights then sum to less than 1)
+ *   weights    SFFN_BF16 or SFFN_MXFP4 (of the experts; x and the router
+ *              are bf16)
+ * (SFFN_E_ARG for a size below 1 or a bad enum, SFFN_E_UNSUPPORTED outside
+ * these ranges.)
+ */
+typedef struct sffn_moe_desc {
+  int32_t d;
+  int32_t d_ff;
+  int32_t n_experts;
+  int32_t top_k;
+  int32_t gated;
+  int32_t normalize;
+  int32_t weights;
+} sffn_moe_desc;
+
+/*
+ * Weights of an expert layer (device).
+ *   router          [E, d] bf16
+ *   gate, up, down  [E, F, d], row j of an expert belongs to neuron j (as
+ *                   in the layer): bf16, or the codes of the [E F, d]
+ *                   matrix (blocks along d) as sffn_mx_quantize makes them.
+ *                   up is NULL iff non-gated; non-gated layers pass W_1 as
+ *                   gate and W_2 as down.
+ *   *_scales        the scales of those codes (SFFN_MXFP4; else NULL)
+ * All 16-byte aligned (scales 4). Non-finite weights make the results of
+ * every token of their expert unspecified.
+ */
+typedef struct sffn_moe_weights {
+  const void* router;
+  const void* gate;
+  const void* up;
+  const void* down;
+  const uint8_t* gate_scales;
+  const uint8_t* up_scales;
+  const uint8_t* down_scales;
+} sffn_moe_weights;
+
+/* Most tokens of one call. */
+#define SFFN_MOE_MAX_TOKENS 256
+
+/* Bytes of workspace for T tokens (256-byte aligned, contents need no
+ * initialisation, not shared by calls that overlap). */
+sffn_status sffn_moe_workspace_bytes(const sffn_moe_desc* desc, int64_t T, size_t* bytes);
+
+/* The layer's forward: x [T, d] bf16, y [T, d] float32, T <=
+ * SFFN_MOE_MAX_TOKENS (SFFN_E_UNSUPPORTED above). ids [T, k] int32 and
+ * probs [T, k] float32 (each nullable) receive the experts and their
+ * weights by rank. n_tokens (device int32, nullable): only the first
+ * *n_tokens rows (at most T) are tokens; the others are not read and their
+ * rows of y, ids and probs are left as they were, so one captured graph
+ * serves smaller batches. A NaN in a token's x makes its row NaN and no
+ * other. No handle: runs on the current device, on the stream, keeps no
+ * state. */
+sffn_status sffn_moe_forward(const sffn_moe_desc* desc, const void* x, const sffn_moe_weights* w,
+                             int64_t T, const int32_t* n_tokens, float* y, int32_t* ids,
+                             float* probs, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /*
  * Per-kernel timing. While enabled, every kernel launch of the library is

@@ -23,6 +23,7 @@ SFFN_E_CAPACITY = -4
 
 SFFN_F32 = 0
 SFFN_BF16 = 1
+SFFN_MXFP4 = 2
 SFFN_SPARSE = 0
 SFFN_DENSE = 1
 SFFN_OP_PACK = 0
@@ -42,7 +43,7 @@ EXPORTS = ("sffn_create", "sffn_destroy", "sffn_last_error", "sffn_status_string
            "sffn_hybrid_check", "sffn_backward", "sffn_forward_noalloc",
            "sffn_choose_mode", "sffn_train_dense_act_bytes", "sffn_forward_train_dense",
            "sffn_backward_dense", "sffn_mx_bytes", "sffn_mx_quantize", "sffn_mx_dequantize",
-           "sffn_mx_matmul")
+           "sffn_mx_matmul", "sffn_moe_workspace_bytes", "sffn_moe_forward")
 SFFN_K_COUNT = 24
 
 
@@ -68,6 +69,20 @@ class SffnHybrid(ctypes.Structure):
                 ("n_backup", ctypes.c_void_p), ("bk_a", ctypes.c_void_p),
                 ("bk_u", ctypes.c_void_p), ("max_backup", ctypes.c_int64)]
 
+
+class SffnMoeDesc(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int32), ("d_ff", ctypes.c_int32), ("n_experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("gated", ctypes.c_int32),
+                ("normalize", ctypes.c_int32), ("weights", ctypes.c_int32)]
+
+
+class SffnMoeWeights(ctypes.Structure):
+    _fields_ = [("router", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("up", ctypes.c_void_p),
+                ("down", ctypes.c_void_p), ("gate_scales", ctypes.c_void_p),
+                ("up_scales", ctypes.c_void_p), ("down_scales", ctypes.c_void_p)]
+
+
+SFFN_MOE_MAX_TOKENS = 256
 
 _lib = None
 
@@ -141,6 +156,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sffn_mx_dequantize.restype = i32
     lib.sffn_mx_matmul.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, i32, i64, vp]
     lib.sffn_mx_matmul.restype = i32
+    lib.sffn_moe_workspace_bytes.argtypes = [ctypes.POINTER(SffnMoeDesc), i64, ctypes.POINTER(sz)]
+    lib.sffn_moe_workspace_bytes.restype = i32
+    lib.sffn_moe_forward.argtypes = [ctypes.POINTER(SffnMoeDesc), vp,
+                                     ctypes.POINTER(SffnMoeWeights), i64, vp, vp, vp, vp, vp, sz,
+                                     vp]
+    lib.sffn_moe_forward.restype = i32
     _lib = lib
     return lib
 
@@ -479,7 +500,7 @@ class SparseFFN:
                                                  _ptr(dwg), _ptr(dwu), _ptr(dwd),
                                                  float(l1_coeff), ws, nb, _stream()),
                     "sffn_backward_dense", "sffn_mx_bytes", "sffn_mx_quantize", "sffn_mx_dequantize",
-           "sffn_mx_matmul")
+           "sffn_mx_matmul", "sffn_moe_workspace_bytes", "sffn_moe_forward")
         return dx, dwg, dwu, dwd
 
     def hybrid_check(self, hy) -> int:

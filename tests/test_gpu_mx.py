@@ -165,7 +165,11 @@ def test_matmul(M, N, K, dtype):
     assert torch.equal(out, sffn.mx_matmul(a, b, dtype=dtype))
 
 
-@pytest.mark.parametrize("M,N,K", [(4096, 2048, 1024), (2048, 5632, 640)])
+@pytest.mark.parametrize("M,N,K", [
+    # 128 x 256 tiles, whole and cut, K of one group, fewer and more than the ring
+    (4096, 2048, 1024), (2048, 5632, 640), (2047, 2305, 128), (2500, 2000, 300), (4000, 3900, 513),
+    # 256 x 256 tiles
+    (4096, 4096, 2048), (3841, 3700, 1100), (8192, 5632, 1153), (40000, 300, 1280)])
 def test_matmul_large(M, N, K):
     """Sizes of the large tiles; the float64 product on the GPU."""
     a = sffn.mx_quantize(_rand((M, K), 1))

@@ -102,16 +102,13 @@ def test_empty_calls_touch_nothing():
 
 
 def test_python_refusals():
-    x = torch.zeros(4, 64)
     with pytest.raises(ValueError, match="GPU"):
-        sffn.mx_quantize(x)
-    q = sffn.MXTensor(torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(1, 4, 4, dtype=torch.uint8),
-                      4, 100)
-    with pytest.raises(ValueError, match="GPU"):
-        sffn.mx_dequantize(q)
-    with pytest.raises(ValueError, match="do not hold"):
-        sffn.mx_dequantize(q._replace(cols=129))
-    with pytest.raises(ValueError, match="do not hold"):
-        sffn.mx_matmul(q._replace(rows=5), q)
-    with pytest.raises(ValueError, match="uint8"):
-        sffn.mx_matmul(q._replace(codes=q.codes.int()), q)
+        sffn.mx_quantize(torch.zeros(4, 64))
+    codes, scales = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(1, 4, 4, dtype=torch.uint8)
+    for c, s, r, k, why in ((codes, scales, 4, 129, "do not hold"), (codes, scales, 5, 100, "do not hold"),
+                            (codes, scales[0], 4, 100, "do not hold"),
+                            (codes.int(), scales, 4, 100, "uint8"), (codes, scales, 4, 100, "GPU"),
+                            (codes.expand(4, 64)[:, ::1].t().contiguous().t(), scales, 4, 100,
+                             "contiguous")):
+        with pytest.raises(ValueError, match=why):
+            sffn.MXTensor(c, s, r, k)

@@ -7,9 +7,9 @@ from typing import Dict, Optional, Tuple, Union
 
 import torch
 
-from .binding import (SFFN_BF16, SFFN_MOE_MAX_TOKENS, SFFN_MXFP4, SffnMoeDesc,
-                      SffnMoeWeights, load_library)
-from .mxfp4 import MXTensor, _check, _on, check_mx
+from .binding import (SFFN_BF16, SFFN_MOE_MAX_TOKENS, SFFN_MXFP4, SFFN_OK, SffnError,
+                      SffnMoeDesc, SffnMoeWeights, load_library)
+from .mxfp4 import MXTensor, _launch
 
 Weight = Union[torch.Tensor, MXTensor]
 
@@ -41,6 +41,7 @@ class SparseMoE:
         self.gated, self.normalize, self.weights = gated, normalize, weights
         self.desc = SffnMoeDesc(d, d_ff, n_experts, top_k, int(gated), int(normalize),
                                 SFFN_MXFP4 if weights == "mxfp4" else SFFN_BF16)
+        self._desc = ctypes.byref(self.desc)
         self._bytes: Dict[int, int] = {}
         self.workspace_bytes(1)      # the descriptor's validation
 
@@ -48,8 +49,10 @@ class SparseMoE:
         n = self._bytes.get(T)
         if n is None:
             c = ctypes.c_size_t()
-            _check(self.lib.sffn_moe_workspace_bytes(ctypes.byref(self.desc), T, ctypes.byref(c)),
-                   "sffn_moe_workspace_bytes")
+            st = self.lib.sffn_moe_workspace_bytes(ctypes.byref(self.desc), T, ctypes.byref(c))
+            if st != SFFN_OK:
+                raise SffnError(st, "sffn_moe_workspace_bytes: "
+                                    + self.lib.sffn_status_string(st).decode())
             n = self._bytes[T] = c.value
         return n
 
@@ -68,10 +71,9 @@ class SparseMoE:
             return self._plain(w, (E, F, d), torch.bfloat16, device, what), None
         if not isinstance(w, MXTensor):
             raise ValueError(f"{what} must be an MXTensor of {E * F} x {d}")
-        check_mx(w, what)
-        if (w.rows, w.cols) != (E * F, d) or w.codes.device != device:
+        if w.rows != E * F or w.cols != d or w.device != device:
             raise ValueError(f"{what} must be an MXTensor of {E * F} x {d} on {device}")
-        return w.codes.data_ptr(), w.scales.data_ptr()
+        return w._pc, w._ps
 
     def forward(self, x: torch.Tensor, w_router: torch.Tensor, w_gate: Weight,
                 w_up: Optional[Weight], w_down: Weight, y: Optional[torch.Tensor] = None,
@@ -120,12 +122,9 @@ class SparseMoE:
             pi = self._plain(ids, (T, self.top_k), torch.int32, dev, "ids")
             pp = self._plain(probs, (T, self.top_k), torch.float32, dev, "probs")
         if T > 0:
-            with _on(dev):
-                nb = self.workspace_bytes(T)
-                # torch's allocations are 512-byte aligned
-                ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-                _check(self.lib.sffn_moe_forward(
-                    ctypes.byref(self.desc), px, ctypes.byref(w), T, pn, py, pi, pp,
-                    ws.data_ptr(), nb, torch.cuda.current_stream().cuda_stream),
-                    "sffn_moe_forward")
+            nb = self.workspace_bytes(T)
+            # torch's allocations are 512-byte aligned
+            ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+            _launch(dev, "sffn_moe_forward", self.lib.sffn_moe_forward, self._desc, px,
+                    ctypes.byref(w), T, pn, py, pi, pp, ws.data_ptr(), nb)
         return (y, ids, probs) if return_routing else y

@@ -7,37 +7,81 @@ nothing and may be captured into a graph.
 """
 from __future__ import annotations
 
-import contextlib
-from typing import NamedTuple, Optional
+from typing import Optional
 
 import torch
 
 from .binding import SFFN_BF16, SFFN_F32, SFFN_OK, SffnError, load_library
 
 _DTYPES = {torch.float32: SFFN_F32, torch.bfloat16: SFFN_BF16}
-_SAME_DEVICE = contextlib.nullcontext()
+
+# The current stream's handle. A small call's time is the host's, and the
+# public call, which builds a Stream object, takes 3 us of it (this one 0.1).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    def _raw_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
 
 
-class MXTensor(NamedTuple):
+class MXTensor:
     """A matrix of ``rows`` x ``cols`` elements in MXFP4, one scale for 32
     elements along a row. ``codes`` [rows, Kp / 2] and ``scales`` [Kp / 128,
     rows, 4] are uint8 tensors, Kp = cols rounded up to 128; include/sffn.h
-    gives the layout."""
+    gives the layout. Made by :func:`mx_quantize` or :func:`mx_empty`, or
+    from codes and scales kept elsewhere (contiguous, on one GPU)."""
 
-    codes: torch.Tensor
-    scales: torch.Tensor
-    rows: int
-    cols: int
+    __slots__ = ("rows", "cols", "device", "_codes", "_scales", "_buf", "_pc", "_ps")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
+        G = (cols + 127) // 128
+        if rows < 0 or cols < 0 or codes.shape != (rows, G * 64) or scales.shape != (G, rows, 4):
+            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not "
+                             f"hold {rows} x {cols} elements")
+        for t in (codes, scales):
+            if t.dtype != torch.uint8 or not t.is_contiguous():
+                raise ValueError("codes and scales must be contiguous uint8 tensors")
+        if not codes.is_cuda or codes.device != scales.device:
+            raise ValueError("codes and scales must be on one GPU")
+        self.rows, self.cols, self.device = rows, cols, codes.device
+        self._codes, self._scales, self._buf = codes, scales, None
+        self._pc, self._ps = codes.data_ptr(), scales.data_ptr()
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            row = (self.cols + 127) // 128 * 64
+            self._codes = self._buf[:self.rows * row].view(self.rows, row)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            G = (self.cols + 127) // 128
+            self._scales = self._buf[self.rows * G * 64:].view(G, self.rows, 4)
+        return self._scales
 
 
-def _on(device: torch.device):
-    """The library launches on the current device."""
-    if device.index == torch.cuda.current_device():
-        return _SAME_DEVICE
-    return torch.cuda.device(device)
+def mx_empty(rows: int, cols: int, device) -> MXTensor:
+    """An MXTensor with uninitialised memory: one buffer, the codes and then
+    the scales."""
+    g = (cols + 127) // 128
+    q = MXTensor.__new__(MXTensor)
+    q._buf = buf = torch.empty(rows * g * 68, dtype=torch.uint8, device=device)
+    q.rows, q.cols, q.device, q._codes, q._scales = rows, cols, buf.device, None, None
+    q._pc = buf.data_ptr()
+    q._ps = q._pc + rows * g * 64
+    return q
 
 
-def _check(st: int, what: str) -> None:
+def _launch(device: torch.device, what: str, f, *args) -> None:
+    """f(*args, stream) on ``device`` (the library launches on the current
+    device) and its current stream."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        st = f(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            st = f(*args, _raw_stream(i))
     if st != SFFN_OK:
         raise SffnError(st, f"{what}: {load_library().sffn_status_string(st).decode()}")
 
@@ -51,33 +95,27 @@ def _matrix(t: torch.Tensor, what: str) -> int:
     if t.dim() != 2:
         raise ValueError(f"{what} must have 2 dimensions, not {t.dim()}")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{what} must have contiguous rows")
-    ld = t.stride(0) if rows > 1 else cols
+    if rows <= 1:
+        return cols
     if ld < cols:
         raise ValueError(f"{what}'s rows overlap")
     return ld
 
 
-def check_mx(q: MXTensor, what: str) -> None:
-    """Raise ValueError unless ``q`` is whole: uint8, contiguous, on one GPU,
-    of the shapes its rows and columns ask for."""
-    Kp = (q.cols + 127) // 128 * 128
-    if q.codes.shape != (q.rows, Kp // 2) or q.scales.shape != (Kp // 128, q.rows, 4):
-        raise ValueError(f"{what}: codes {tuple(q.codes.shape)} and scales "
-                         f"{tuple(q.scales.shape)} do not hold {q.rows} x {q.cols} elements")
-    for t in (q.codes, q.scales):
-        if t.dtype != torch.uint8 or not t.is_contiguous():
-            raise ValueError(f"{what}: codes and scales must be contiguous uint8 tensors")
-    if not q.codes.is_cuda or q.codes.device != q.scales.device:
-        raise ValueError(f"{what}: codes and scales must be on one GPU")
-
-
-def mx_empty(rows: int, cols: int, device) -> MXTensor:
-    """An MXTensor with uninitialised memory."""
-    g = (cols + 127) // 128
-    return MXTensor(torch.empty((rows, g * 64), dtype=torch.uint8, device=device),
-                    torch.empty((g, rows, 4), dtype=torch.uint8, device=device), rows, cols)
+def _result(out: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtype,
+            device: torch.device):
+    """(out, its row stride, its type's number), made when not given."""
+    if out is None:
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype must be float32 or bfloat16, not {dtype}")
+        return torch.empty((rows, cols), dtype=dtype, device=device), cols, _DTYPES[dtype]
+    ld = _matrix(out, "out")
+    if out.shape != (rows, cols) or out.device != device:
+        raise ValueError(f"out must be {rows} x {cols} on {device}")
+    return out, ld, _DTYPES[out.dtype]
 
 
 def mx_quantize(x: torch.Tensor, transposed: bool = False,
@@ -89,16 +127,13 @@ def mx_quantize(x: torch.Tensor, transposed: bool = False,
     ld = _matrix(x, "x")
     rows, cols = x.shape
     R, K = (cols, rows) if transposed else (rows, cols)
+    device = x.device
     if out is None:
-        out = mx_empty(R, K, x.device)
-    else:
-        check_mx(out, "out")
-        if (out.rows, out.cols) != (R, K) or out.codes.device != x.device:
-            raise ValueError(f"out must be {R} x {K} on {x.device}")
-    with _on(x.device):
-        _check(load_library().sffn_mx_quantize(
-            x.data_ptr(), _DTYPES[x.dtype], rows, cols, ld, int(transposed), out.codes.data_ptr(),
-            out.scales.data_ptr(), torch.cuda.current_stream().cuda_stream), "sffn_mx_quantize")
+        out = mx_empty(R, K, device)
+    elif out.rows != R or out.cols != K or out.device != device:
+        raise ValueError(f"out must be {R} x {K} on {device}")
+    _launch(device, "sffn_mx_quantize", load_library().sffn_mx_quantize, x.data_ptr(),
+            _DTYPES[x.dtype], rows, cols, ld, 1 if transposed else 0, out._pc, out._ps)
     return out
 
 
@@ -106,19 +141,9 @@ def mx_dequantize(q: MXTensor, dtype: torch.dtype = torch.float32,
                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of ``q`` [rows, cols], exact, as float32 or bfloat16 (in
     ``out`` when given: contiguous rows, any row stride)."""
-    check_mx(q, "q")
-    if out is None:
-        if dtype not in _DTYPES:
-            raise ValueError(f"dtype must be float32 or bfloat16, not {dtype}")
-        out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
-    ld = _matrix(out, "out")
-    if out.shape != (q.rows, q.cols) or out.device != q.codes.device:
-        raise ValueError(f"out must be {q.rows} x {q.cols} on {q.codes.device}")
-    with _on(out.device):
-        _check(load_library().sffn_mx_dequantize(
-            q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, out.data_ptr(),
-            _DTYPES[out.dtype], ld, torch.cuda.current_stream().cuda_stream),
-            "sffn_mx_dequantize")
+    out, ld, dt = _result(out, q.rows, q.cols, dtype, q.device)
+    _launch(q.device, "sffn_mx_dequantize", load_library().sffn_mx_dequantize, q._pc, q._ps,
+            q.rows, q.cols, out.data_ptr(), dt, ld)
     return out
 
 
@@ -127,22 +152,11 @@ def mx_matmul(a: MXTensor, b: MXTensor, dtype: torch.dtype = torch.float32,
     """a b^T for ``a`` [M, K] and ``b`` [N, K]: [M, N] float32 or bfloat16
     (in ``out`` when given: contiguous rows, any row stride). Sums are
     float32, rounded once when stored as bfloat16."""
-    check_mx(a, "a")
-    check_mx(b, "b")
     if a.cols != b.cols:
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
-    if a.codes.device != b.codes.device:
+    if a.device != b.device:
         raise ValueError("a and b must be on one GPU")
-    if out is None:
-        if dtype not in _DTYPES:
-            raise ValueError(f"dtype must be float32 or bfloat16, not {dtype}")
-        out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
-    ld = _matrix(out, "out")
-    if out.shape != (a.rows, b.rows) or out.device != a.codes.device:
-        raise ValueError(f"out must be {a.rows} x {b.rows} on {a.codes.device}")
-    with _on(out.device):
-        _check(load_library().sffn_mx_matmul(
-            a.codes.data_ptr(), a.scales.data_ptr(), a.rows, b.codes.data_ptr(),
-            b.scales.data_ptr(), b.rows, a.cols, out.data_ptr(), _DTYPES[out.dtype], ld,
-            torch.cuda.current_stream().cuda_stream), "sffn_mx_matmul")
+    out, ld, dt = _result(out, a.rows, b.rows, dtype, a.device)
+    _launch(a.device, "sffn_mx_matmul", load_library().sffn_mx_matmul, a._pc, a._ps, a.rows, b._pc,
+            b._ps, b.rows, a.cols, out.data_ptr(), dt, ld)
     return out

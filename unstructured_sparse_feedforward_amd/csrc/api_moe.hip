@@ -27,22 +27,39 @@ sffn_status validate(const sffn_moe_desc* D) {
 }
 
 struct Layout {
-  size_t keys, chosen, part, total;
-  int nb, S;
+  size_t keys, chosen, cnt, expert, list, on, h, part, total;
 };
 
-Layout layout(const sffn_moe_desc& D, int64_t T) {
+// the sizes of a call, with what moe_plan derives from them
+MoeArgs sizes(const sffn_moe_desc& D, int64_t T) {
+  MoeArgs a = {};
+  a.T = (int)T;
+  a.d = D.d;
+  a.F = D.d_ff;
+  a.E = D.n_experts;
+  a.k = D.top_k;
+  a.normalize = D.normalize;
+  moe_plan(D.weights == SFFN_MXFP4, &a);
+  return a;
+}
+
+Layout layout(const MoeArgs& a) {
   Layout L;
-  moe_slices((int)T, D.d_ff, D.n_experts, D.top_k, &L.nb, &L.S);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
     o = (o + bytes + kAlign - 1) / kAlign * kAlign;
     return at;
   };
-  L.keys = take((size_t)T * D.n_experts * 8);
-  L.chosen = take((size_t)T * D.top_k * 8);
-  L.part = take((size_t)L.S * T * D.top_k * D.d * 4);
+  const size_t T = a.T, pairs = T * a.k;
+  L.keys = take(T * a.E * 8);
+  L.chosen = take(pairs * 8);
+  L.cnt = take((size_t)a.Y * 4);
+  L.expert = take((size_t)a.Y * 4);
+  L.list = take((size_t)a.Y * T * 4);
+  L.on = take((size_t)a.Y * a.F);
+  L.h = take(pairs * a.F * 4);
+  L.part = take(pairs * a.d * 4);
   L.total = o;
   return L;
 }
@@ -56,7 +73,7 @@ sffn_status sffn_moe_workspace_bytes(const sffn_moe_desc* desc, int64_t T, size_
   if (st != SFFN_OK) return st;
   if (!bytes || T < 0) return SFFN_E_ARG;
   if (T > SFFN_MOE_MAX_TOKENS) return SFFN_E_UNSUPPORTED;
-  *bytes = T == 0 ? 0 : layout(*desc, T).total;
+  *bytes = T == 0 ? 0 : layout(sizes(*desc, T)).total;
   return SFFN_OK;
 }
 
@@ -83,9 +100,10 @@ sffn_status sffn_moe_forward(const sffn_moe_desc* desc, const void* x, const sff
   if ((n_tokens && !aligned(n_tokens, 4)) || (ids && !aligned(ids, 4)) ||
       (probs && !aligned(probs, 4)))
     return SFFN_E_ARG;
-  const Layout L = layout(D, T);
+  MoeArgs a = sizes(D, T);
+  const Layout L = layout(a);
   if (!aligned(ws, kAlign) || ws_bytes < L.total) return SFFN_E_ARG;
-  MoeArgs a = {};
+  char* base = (char*)ws;
   a.x = (const uint16_t*)x;
   a.router = (const uint16_t*)w->router;
   a.wg = w->gate;
@@ -94,18 +112,15 @@ sffn_status sffn_moe_forward(const sffn_moe_desc* desc, const void* x, const sff
   a.sg = w->gate_scales;
   a.su = w->up_scales;
   a.sd = w->down_scales;
-  a.T = (int)T;
-  a.d = D.d;
-  a.F = D.d_ff;
-  a.E = D.n_experts;
-  a.k = D.top_k;
-  a.normalize = D.normalize;
   a.t_dev = n_tokens;
-  a.nb = L.nb;
-  a.S = L.S;
-  a.keys = (long long*)((char*)ws + L.keys);
-  a.chosen = (long long*)((char*)ws + L.chosen);
-  a.part = (float*)((char*)ws + L.part);
+  a.keys = (long long*)(base + L.keys);
+  a.chosen = (long long*)(base + L.chosen);
+  a.cnt = (int32_t*)(base + L.cnt);
+  a.expert = (int32_t*)(base + L.expert);
+  a.list = (int32_t*)(base + L.list);
+  a.on = (uint8_t*)(base + L.on);
+  a.h = (float*)(base + L.h);
+  a.part = (float*)(base + L.part);
   a.y = y;
   a.ids = ids;
   a.probs = probs;

@@ -5,17 +5,17 @@
 //   y = sum_r p_r (ReLU(x W_g,e(r)) * (x W_u,e(r))) W_d,e(r)
 //
 // With few tokens the time is that of reading the selected experts'
-// weights, so every weight is read once, by one workgroup: a workgroup has
-// an expert and a slice of its neurons, and computes those neurons' gate,
-// up and down products for all of the expert's tokens. The layout is the
-// layer's (row j of each matrix belongs to neuron j), so the three products
-// of a slice read three runs of rows. Gate comes first; up and down are
-// read only for neurons that are active (z > 0) for one of the tokens, as
-// in the rest of the library.
-//
-// Three launches: the logits; the experts, which leave each (token, rank)'s
-// partial output of each slice; the weighted sum over ranks and slices, in
-// a fixed order (no atomics: results repeat bit for bit).
+// weights, so every weight is read once (per 16 or 32 of its expert's
+// tokens). Four launches:
+//   logits  64-bit sums;
+//   hidden  a workgroup has an expert and a slice of its neurons: it finds
+//           the expert's tokens from the logits, computes z for all of them,
+//           and u only for the neurons that are active (z > 0) for one of
+//           them, as in the rest of the library;
+//   down    a workgroup has an expert and a chunk of y's columns, and reads
+//           those of the active neurons' rows;
+//   sum     the token's k outputs, weighted, in the order of their ranks (no
+//           float atomics: results repeat bit for bit).
 #include "moe.hpp"
 
 namespace sffn {
@@ -42,34 +42,37 @@ __device__ __forceinline__ double key_value(long long k) {
 
 // ---------------------------------------------------------------- logits
 
-// One wave an expert and kLogitT tokens. The sums are 64-bit: two experts'
+// One wave an expert and TT tokens. The sums are 64-bit: two experts'
 // logits then compare as their exact values do (the product of two bf16
 // values has 16 bits), whatever the order of summation.
-constexpr int kLogitT = 4;
-
+template <int TT>
 __global__ __launch_bounds__(NT) void moe_logits_kernel(MoeArgs a) {
   const int lane = threadIdx.x & 63;
   const int e = blockIdx.x * kWaves + (threadIdx.x >> 6);
   const int T = tokens(a);
-  const int t0 = blockIdx.y * kLogitT;
+  const int t0 = blockIdx.y * TT;
   if (e >= a.E || t0 >= T) return;
   const uint16_t* w = a.router + (int64_t)e * a.d;
-  double s[kLogitT] = {};
-#pragma unroll 2
+  double s[TT] = {};
+#pragma unroll 4
   for (int c = lane * 8; c < a.d; c += 512) {
-    float wv[8];
-    Vec<uint16_t, 8>::cvt(*(const u32x4_t*)(w + c), wv);
+    const u32x4_t wr = *(const u32x4_t*)(w + c);
+    u32x4_t xr[TT];
 #pragma unroll
-    for (int i = 0; i < kLogitT; ++i) {
+    for (int i = 0; i < TT; ++i)
+      xr[i] = *(const u32x4_t*)(a.x + (int64_t)min(t0 + i, T - 1) * a.d + c);
+    float wv[8];
+    Vec<uint16_t, 8>::cvt(wr, wv);
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
       float xv[8];
-      const int t = min(t0 + i, T - 1);
-      Vec<uint16_t, 8>::cvt(*(const u32x4_t*)(a.x + (int64_t)t * a.d + c), xv);
+      Vec<uint16_t, 8>::cvt(xr[i], xv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[i] = fma((double)wv[j], (double)xv[j], s[i]);
     }
   }
 #pragma unroll
-  for (int i = 0; i < kLogitT; ++i) {
+  for (int i = 0; i < TT; ++i) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) s[i] += __shfl_xor(s[i], o);
     if (lane == 0 && t0 + i < T) a.keys[(int64_t)(t0 + i) * a.E + e] = order_key(s[i]);
@@ -85,21 +88,15 @@ struct Rows {            // one of an expert's matrices
   int64_t gpitch;        // scale bytes a 128-column group (all experts' rows)
 };
 
-// the scale 2^(b - 127) of a scale byte
-__device__ __forceinline__ float scale_of(uint32_t b) {
-  return __uint_as_float(b ? b << 23 : 0x00400000u);
-}
-
-// 8 elements of a row as bf16 pairs: bf16 values as they are, or 8 codes
-// times their scale (exact: two significant bits).
+// 8 codes times their scale as bf16 pairs: exact (two significant bits). The
+// conversion takes the scale's exponent byte as it is (255: NaN).
 __device__ __forceinline__ u32x4_t from_codes(uint32_t q, uint32_t sb) {
-  const float s = scale_of(sb);
+  const float s = __uint_as_float(sb << 23);
   u32x4_t o;
   o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0));
   o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1));
   o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 2));
   o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 3));
-  if (__builtin_expect(sb == 255u, 0)) o = u32x4_t{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
   return o;
 }
 
@@ -111,25 +108,25 @@ __device__ __forceinline__ f32x4_t mfma(const u32x4_t& w, const u32x4_t& v, cons
 // ---------------------------------------------------------------- products with x
 
 // acc[i][n] += rows r[i] (16 of them, one a lane's row) . x of 16 tokens,
-// over this wave's share of d. The instruction's k order is free as long as
-// both operands agree: lane l takes 32 (bf16) or 16 (codes) contiguous bytes
-// of row l % 16, so that the four lanes of a row cover 128 or 64 bytes.
+// over steps part, part + parts, .. of d. The instruction's k order is free
+// as long as both operands agree: lane l takes 16 contiguous bytes of row
+// l % 16, so that the four lanes of a row cover 64 bytes: 32 bf16 values, the
+// instruction's own order, or 128 codes, four instructions' worth.
 template <bool MX, int MT, int NTK>
 __device__ __forceinline__ void dots(const MoeArgs& a, const Rows& w, const int (&r)[MT],
-                                     const uint16_t* const (&xt)[NTK], int lane, int wave,
-                                     f32x4_t (&acc)[MT][NTK]) {
+                                     const uint16_t* const (&xt)[NTK], int lane, int part,
+                                     int parts, f32x4_t (&acc)[MT][NTK]) {
   const int kq = lane >> 4;
+  const uint8_t* p[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) p[i] = w.p + (int64_t)r[i] * w.pitch + kq * 16;
   if constexpr (MX) {
-    const uint8_t* p[MT];
     const uint8_t* ps[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      p[i] = w.p + (int64_t)r[i] * w.pitch + kq * 16;
-      ps[i] = w.sc + (int64_t)r[i] * 4 + kq;
-    }
+    for (int i = 0; i < MT; ++i) ps[i] = w.sc + (int64_t)r[i] * 4 + kq;
     const int G = a.d / 128;
 #pragma unroll 2
-    for (int g = wave; g < G; g += kWaves) {
+    for (int g = part; g < G; g += parts) {
       u32x4_t q[MT];
       uint32_t sb[MT];
       u32x4_t xv[NTK][4];
@@ -153,20 +150,17 @@ __device__ __forceinline__ void dots(const MoeArgs& a, const Rows& w, const int 
         }
     }
   } else {
-    const uint8_t* p[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) p[i] = w.p + (int64_t)r[i] * w.pitch + kq * 32;
     const int G = a.d / 64;
 #pragma unroll 4
-    for (int g = wave; g < G; g += kWaves) {
+    for (int g = part; g < G; g += parts) {
       u32x4_t wv[MT][2], xv[NTK][2];
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) wv[i][f] = *(const u32x4_t*)(p[i] + (int64_t)g * 128 + f * 16);
+        for (int i = 0; i < MT; ++i) wv[i][f] = *(const u32x4_t*)(p[i] + (int64_t)g * 128 + f * 64);
 #pragma unroll
         for (int n = 0; n < NTK; ++n)
-          xv[n][f] = *(const u32x4_t*)(xt[n] + g * 64 + kq * 16 + f * 8);
+          xv[n][f] = *(const u32x4_t*)(xt[n] + g * 64 + f * 32 + kq * 8);
       }
 #pragma unroll
       for (int f = 0; f < 2; ++f)
@@ -178,36 +172,79 @@ __device__ __forceinline__ void dots(const MoeArgs& a, const Rows& w, const int 
   }
 }
 
-// ---------------------------------------------------------------- experts
+// ---------------------------------------------------------------- hidden
 
-// LDS of a workgroup for passes of 16 NTK tokens.
-template <int NTK>
+// Rows of a product with x that a wave takes at a time, in blocks of 16:
+// codes are a quarter of the bytes, and two blocks halve the loads of x.
+template <bool MX>
+constexpr int kBlocks = MX ? 2 : 1;
+// most neurons of a workgroup: every wave one tile
+template <bool MX>
+constexpr int kSlice = kWaves * 16 * kBlocks<MX>;
+
+// LDS of a pass of 16 NTK tokens
+template <bool MX, int NTK>
 struct Shared {
-  static constexpr int kTok = 16 * NTK;
-  static constexpr int kZ = kMoeSlice + 4;    // padded rows: no bank conflicts
-  static constexpr int kH = kMoeSlice + 8;
-  f32x4_t red[kWaves][2][NTK][64];     // the waves' shares of a 32-neuron product
-  float z[kTok][kZ];                   // gate pre-activations of the pass
-  __align__(16) uint16_t hi[kTok][kH]; // h of the active neurons, bf16 high ...
-  __align__(16) uint16_t lo[kTok][kH]; // ... and low parts
-  int act[kMoeSlice];                  // active neurons of the slice, ascending
-  uint8_t on[kMoeSlice];
+  static constexpr int MT = kBlocks<MX>, SL = kSlice<MX>;
+  f32x4_t red[kWaves][MT][NTK][64];    // the waves' shares of a product with x
+  float z[16 * NTK][SL + 4];           // gate pre-activations (padded rows)
+  int act[SL];                         // active neurons of the slice, ascending
+  uint8_t on[SL];
   int na;
 };
 
+// The products of tiles of 16 MT rows with the pass's tokens: the waves share
+// out the tiles, and d where the tiles are fewer than the waves. row(i) is
+// the row of position i. Leaves the shares in sh.red, joined by share_sum.
+template <bool MX, int NTK, typename F>
+__device__ __forceinline__ int share_products(const MoeArgs& a, Shared<MX, NTK>& sh,
+                                              const Rows& w, const uint16_t* const (&xt)[NTK],
+                                              int tiles, F&& row) {
+  constexpr int MT = kBlocks<MX>;
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int lg = tiles <= 1 ? 0 : tiles <= 2 ? 1 : 2;
+  const int parts = kWaves >> lg, tile = wave >> (2 - lg), part = wave & (parts - 1);
+  if (tile < tiles) {
+    f32x4_t acc[MT][NTK] = {};
+    int r[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) r[i] = row((tile * MT + i) * 16 + (lane & 15));
+    dots<MX, MT, NTK>(a, w, r, xt, lane, part, parts, acc);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int t = 0; t < NTK; ++t) sh.red[wave][i][t][lane] = acc[i][t];
+  }
+  return parts;
+}
+template <bool MX, int NTK>
+__device__ __forceinline__ f32x4_t share_sum(const Shared<MX, NTK>& sh, int parts, int block,
+                                             int t, int l) {
+  constexpr int MT = kBlocks<MX>;
+  const int w0 = block / MT * parts;
+  f32x4_t s = sh.red[w0][block % MT][t][l];
+  for (int p = 1; p < parts; ++p) s += sh.red[w0 + p][block % MT][t][l];
+  return s;
+}
+
 struct Lists {
-  int tok[kMoeMaxT];                   // the expert's tokens, ascending
+  int tok[kMoeMaxT];                   // the unit's tokens, ascending
   int pair[kMoeMaxT];                  // token * k + rank
-  int rank[kMoeMaxT];                  // of each token (k: not selected)
+  int rank[kMoeMaxT];                  // of each token (k and above: not selected)
   int wsum[kWaves];
+  int expert;
 };
 
-// 16 NTK of the expert's tokens (list positions p0 ..) through the slice's
-// neurons j0 .. j0 + nbe.
+__device__ __forceinline__ uint64_t below(int lane) { return lane ? ~0ull >> (64 - lane) : 0ull; }
+
+// 16 NTK of the unit's tokens (list positions p0 ..) through the slice's
+// neurons j0 .. j0 + nbe: their h, and in `any` the neurons active for one.
 template <bool MX, bool GATED, int NTK>
-__device__ __forceinline__ void pass(const MoeArgs& a, Shared<NTK>& sh, const Lists& ls,
-                                     const Rows& wg, const Rows& wu, const Rows& wd, int j0,
-                                     int nbe, int n, int p0, int slice) {
+__device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, const Lists& ls,
+                                     const Rows& wg, const Rows& wu, int j0, int nbe, int n,
+                                     int p0, uint8_t* any) {
+  constexpr int MT = kBlocks<MX>;
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
   const int tid = threadIdx.x;
@@ -217,203 +254,171 @@ __device__ __forceinline__ void pass(const MoeArgs& a, Shared<NTK>& sh, const Li
   for (int i = 0; i < NTK; ++i)
     xt[i] = a.x + (int64_t)ls.tok[p0 + min(i * 16 + (lane & 15), nt - 1)] * a.d;
 
-  if (tid < kMoeSlice) sh.on[tid] = 0;
-  // gate: 32 neurons at a time, the waves' shares of d joined in LDS
-  for (int c = 0; c < nbe; c += 32) {
-    f32x4_t acc[2][NTK] = {};
-    const int r[2] = {j0 + c + (lane & 15), j0 + c + 16 + (lane & 15)};
-    dots<MX, 2, NTK>(a, wg, r, xt, lane, wave, acc);
-    __syncthreads();
+  if (tid < kSlice<MX>) sh.on[tid] = 0;
+  const int blocks = nbe / 16;
+  int parts = share_products<MX, NTK>(a, sh, wg, xt, (blocks + MT - 1) / MT,
+                                      [&](int i) { return j0 + min(i, nbe - 1); });
+  __syncthreads();
+  for (int e = tid; e < blocks * NTK * 64; e += NT) {
+    const int block = e / (NTK * 64), t = (e >> 6) % NTK, l = e & 63;
+    const f32x4_t s = share_sum<MX, NTK>(sh, parts, block, t, l);
+    const int tk = t * 16 + (l & 15), j = block * 16 + 4 * (l >> 4);
+    *(f32x4_t*)&sh.z[tk][j] = s;
+    if (tk < nt) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int q = 0; q < 4; ++q)
+        if (s[q] > 0.0f) sh.on[j + q] = any[j + q] = 1;   // every writer stores the same
+      // non-gated: h is z itself; gated: a neuron that only another pass
+      // finds active has h = 0 here
+      f32x4_t h = {};
 #pragma unroll
-      for (int t = 0; t < NTK; ++t) sh.red[wave][i][t][lane] = acc[i][t];
-    __syncthreads();
-    for (int e = tid; e < 2 * NTK * 64; e += NT) {
-      const int i = e / (NTK * 64), t = (e >> 6) % NTK, l = e & 63;
-      f32x4_t s = sh.red[0][i][t][l];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) s += sh.red[w][i][t][l];
-      const int tk = t * 16 + (l & 15), j = c + i * 16 + 4 * (l >> 4);
-      *(f32x4_t*)&sh.z[tk][j] = s;
-      if (tk < nt) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (s[q] > 0.0f) sh.on[j + q] = 1;   // every writer stores the same
-      }
+      for (int q = 0; q < 4; ++q) h[q] = !GATED && s[q] > 0.0f ? s[q] : 0.0f;
+      if (!GATED || n > 16 * NTK || p0 > 0)
+        *(f32x4_t*)(a.h + (int64_t)ls.pair[p0 + tk] * a.F + j0 + j) = h;
     }
   }
   __syncthreads();
+  if (!GATED) return;
   // the neurons active for some token of the pass, ascending
   if (wave == 0) {
     int base = 0;
     for (int c = 0; c < nbe; c += 64) {
       const bool p = c + lane < nbe && sh.on[c + lane];
       const uint64_t b = __ballot(p);
-      if (p) sh.act[base + __popcll(b & (lane ? ~0ull >> (64 - lane) : 0ull))] = c + lane;
+      if (p) sh.act[base + __popcll(b & below(lane))] = c + lane;
       base += __popcll(b);
     }
     if (lane == 0) sh.na = base;
   }
   __syncthreads();
   const int na = sh.na;
-  const int nap = (na + 31) / 32 * 32;
-
-  // h = z u of the active neurons, as bf16 high and low parts: their sum
-  // has 16 significant bits, so the down product sees h to 2^-17
-  for (int c = 0; c < nap; c += 32) {
-    f32x4_t acc[2][NTK] = {};
-    if constexpr (GATED) {
-      const int r[2] = {j0 + sh.act[min(c + (lane & 15), na - 1)],
-                        j0 + sh.act[min(c + 16 + (lane & 15), na - 1)]};
-      dots<MX, 2, NTK>(a, wu, r, xt, lane, wave, acc);
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int t = 0; t < NTK; ++t) sh.red[wave][i][t][lane] = acc[i][t];
-      __syncthreads();
-    }
-    for (int e = tid; e < 2 * NTK * 64; e += NT) {
-      const int i = e / (NTK * 64), t = (e >> 6) % NTK, l = e & 63;
-      f32x4_t u = {1.0f, 1.0f, 1.0f, 1.0f};
-      if constexpr (GATED) {
-        u = sh.red[0][i][t][l];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) u += sh.red[w][i][t][l];
-      }
-      const int tk = t * 16 + (l & 15), j = c + i * 16 + 4 * (l >> 4);
+  if (na == 0) return;
+  parts = share_products<MX, NTK>(a, sh, wu, xt, (na + 16 * MT - 1) / (16 * MT),
+                                  [&](int i) { return j0 + sh.act[min(i, na - 1)]; });
+  __syncthreads();
+  // h of the active neurons; the others' is not read
+  for (int e = tid; e < (na + 15) / 16 * NTK * 64; e += NT) {
+    const int block = e / (NTK * 64), t = (e >> 6) % NTK, l = e & 63;
+    const f32x4_t u = share_sum<MX, NTK>(sh, parts, block, t, l);
+    const int tk = t * 16 + (l & 15);
+    if (tk < nt) {
+      float* o = a.h + (int64_t)ls.pair[p0 + tk] * a.F + j0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        float h = 0.0f;
-        if (j + q < na) {
-          const float z = sh.z[tk][sh.act[j + q]];
-          h = z > 0.0f ? z * u[q] : 0.0f;
+        const int i = block * 16 + 4 * (l >> 4) + q;
+        if (i < na) {
+          const int j = sh.act[i];
+          const float z = sh.z[tk][j];
+          o[j] = z > 0.0f ? z * u[q] : 0.0f;
         }
-        const __bf16 hh = (__bf16)h;
-        const float hf = (float)hh;
-        // an infinite or NaN h is all in its high part
-        const __bf16 hl = (__bf16)(fabsf(hf) < INFINITY ? h - hf : 0.0f);
-        sh.hi[tk][j + q] = __builtin_bit_cast(uint16_t, hh);
-        sh.lo[tk][j + q] = __builtin_bit_cast(uint16_t, hl);
-      }
-    }
-  }
-  __syncthreads();
-
-  // down: a wave has 128 columns at a time. A lane loads 8 columns of 8
-  // neurons and turns them into 8 operands, one a column: operand q of lane
-  // l holds column 8 (l % 16) + q at k = neurons 8 (l / 16) .. + 7, and the
-  // results of a lane are 32 consecutive columns of token l % 16.
-  const int kq = lane >> 4;
-  for (int c0 = wave * 128; c0 < a.d; c0 += kWaves * 128) {
-    f32x4_t acc[8][NTK] = {};
-    const int col = c0 + 8 * (lane & 15);
-    for (int ks = 0; ks < nap; ks += 32) {
-      u32x4_t v[8];
-      if constexpr (MX) {
-        uint32_t q[8], sb[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = j0 + sh.act[min(ks + kq * 8 + j, na - 1)];
-          q[j] = *(const uint32_t*)(wd.p + (int64_t)r * wd.pitch + col / 2);
-          sb[j] = wd.sc[(c0 / 128) * wd.gpitch + (int64_t)r * 4 + ((lane & 15) >> 2)];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = from_codes(q[j], sb[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = j0 + sh.act[min(ks + kq * 8 + j, na - 1)];
-          v[j] = *(const u32x4_t*)(wd.p + (int64_t)r * wd.pitch + col * 2);
-        }
-      }
-      u32x4_t hh[NTK], hl[NTK];
-#pragma unroll
-      for (int t = 0; t < NTK; ++t) {
-        hh[t] = *(const u32x4_t*)&sh.hi[t * 16 + (lane & 15)][ks + kq * 8];
-        hl[t] = *(const u32x4_t*)&sh.lo[t * 16 + (lane & 15)][ks + kq * 8];
-      }
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        // low (q even) or high halves of neurons 2 i and 2 i + 1
-        const uint32_t sel = (q & 1) ? 0x07060302u : 0x05040100u;
-        u32x4_t o;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o[i] = __builtin_amdgcn_perm(v[2 * i + 1][q >> 1], v[2 * i][q >> 1], sel);
-#pragma unroll
-        for (int t = 0; t < NTK; ++t) {
-          acc[q][t] = mfma(o, hh[t], acc[q][t]);
-          acc[q][t] = mfma(o, hl[t], acc[q][t]);
-        }
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < NTK; ++t) {
-      const int tk = t * 16 + (lane & 15);
-      if (tk >= nt) continue;
-      float* o = a.part + ((int64_t)slice * a.T * a.k + ls.pair[p0 + tk]) * a.d + c0 + 32 * kq;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        *(f32x4_t*)(o + 8 * i) = f32x4_t{acc[0][t][i], acc[1][t][i], acc[2][t][i], acc[3][t][i]};
-        *(f32x4_t*)(o + 8 * i + 4) =
-            f32x4_t{acc[4][t][i], acc[5][t][i], acc[6][t][i], acc[7][t][i]};
       }
     }
   }
 }
 
-template <bool MX, bool GATED, int NTK>
-__global__ __launch_bounds__(NT) void moe_experts_kernel(MoeArgs a) {
+template <bool MX, bool GATED, bool PAIRS, int NTK>
+__global__ __launch_bounds__(NT, NTK == 1 ? 4 : 2) void moe_hidden_kernel(MoeArgs a) {
   __shared__ Lists ls;
-  __shared__ Shared<NTK> sh;
-  const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const int e = blockIdx.y;
-  const int slice = blockIdx.x;
+  __shared__ uint8_t any[kSlice<MX>];
+  __shared__ union {
+    struct {
+      long long keys[kMoeMaxE];
+      int before[kMoeMaxE];
+    } r;
+    Shared<MX, 1> s1;
+    Shared<MX, NTK> s;
+  } sh;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = tid >> 6;
+  const int slice = blockIdx.x, unit = blockIdx.y;
   const int T = tokens(a);
-  // the expert's rank for each token: the experts that come before it
-  for (int t = wave; t < T; t += kWaves) {
-    const long long* keys = a.keys + (int64_t)t * a.E;
-    const long long mine = keys[e];
-    int before = 0;
-    for (int o = 0; o < a.E; o += 64) {
-      const int f = o + lane;
-      bool b = false;
-      if (f < a.E) {
-        const long long other = keys[f];
-        b = other > mine || (other == mine && f < e);
+  const long long* __restrict__ keys = a.keys;
+  int e = unit, first = 0;
+  if (PAIRS) {
+    first = unit / a.k;
+    // every expert's rank for the pair's token: the experts before it, the
+    // comparisons shared out over all threads
+    const int rank = unit % a.k;
+    for (int f = tid; f < a.E; f += NT) {
+      sh.r.keys[f] = first < T ? keys[(int64_t)first * a.E + f] : 0;
+      sh.r.before[f] = 0;
+    }
+    __syncthreads();
+    const int parts = max(NT / a.E, 1);
+    for (int i = tid; i < a.E * parts; i += NT) {
+      const int f = i % a.E;
+      const long long mine = sh.r.keys[f];
+      int before = 0;
+      for (int o = i / a.E; o < a.E; o += parts) {
+        const long long other = sh.r.keys[o];
+        before += other > mine || (other == mine && o < f);
       }
-      before += __popcll(__ballot(b));
+      atomicAdd(&sh.r.before[f], before);   // whole numbers: any order
+    }
+    __syncthreads();
+    for (int f = tid; f < a.E; f += NT)
+      if (sh.r.before[f] == rank) ls.expert = f;
+    __syncthreads();
+    e = ls.expert;
+  }
+  // the expert's rank for each token: kAt tokens a wave at a time, so that
+  // their loads are in flight together
+  constexpr int kAt = 8;
+  for (int t0 = wave * kAt; t0 < T; t0 += kWaves * kAt) {
+    long long mine[kAt];
+    int before[kAt] = {};
+#pragma unroll
+    for (int i = 0; i < kAt; ++i) mine[i] = keys[(int64_t)min(t0 + i, T - 1) * a.E + e];
+    for (int o = 0; o < a.E; o += 64) {
+      const int f = min(o + lane, a.E - 1);
+      long long other[kAt];
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) other[i] = keys[(int64_t)min(t0 + i, T - 1) * a.E + f];
+#pragma unroll
+      for (int i = 0; i < kAt; ++i)
+        before[i] += __popcll(__ballot(o + lane < a.E &&
+                                       (other[i] > mine[i] || (other[i] == mine[i] && f < e))));
     }
     if (lane == 0) {
-      ls.rank[t] = before;
-      if (slice == 0 && before < a.k) {
-        a.chosen[t * a.k + before] = mine;
-        if (a.ids) a.ids[t * a.k + before] = e;
-      }
+#pragma unroll
+      for (int i = 0; i < kAt; ++i)
+        if (t0 + i < T) ls.rank[t0 + i] = before[i];
     }
   }
+  if (tid < kSlice<MX>) any[tid] = 0;
   __syncthreads();
   // list its tokens, one a thread, in ascending order
-  const int t = threadIdx.x;
-  const bool mine = t < T && ls.rank[t] < a.k;
+  const bool mine = tid < T && ls.rank[tid] < a.k;
   const uint64_t b = __ballot(mine);
   if (lane == 0) ls.wsum[wave] = __popcll(b);
   __syncthreads();
-  int at = __popcll(b & (lane ? ~0ull >> (64 - lane) : 0ull)), n = 0;
+  int at = __popcll(b & below(lane)), n = 0;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
     if (w < wave) at += ls.wsum[w];
     n += ls.wsum[w];
   }
   if (mine) {
-    ls.tok[at] = t;
-    ls.pair[at] = t * a.k + ls.rank[t];
+    ls.tok[at] = tid;
+    ls.pair[at] = tid * a.k + ls.rank[tid];
+  }
+  __syncthreads();
+  if (PAIRS && (first >= T || ls.tok[0] != first)) n = 0;   // its first token's pair works for it
+  if (slice == 0) {
+    // what the down kernel needs of the routing
+    if (tid == 0) {
+      a.cnt[unit] = n;
+      a.expert[unit] = e;
+    }
+    if (mine && n > 0) {
+      const int pair = tid * a.k + ls.rank[tid];
+      a.list[(int64_t)unit * a.T + at] = pair;
+      a.chosen[pair] = keys[(int64_t)tid * a.E + e];
+      if (a.ids) a.ids[pair] = e;
+    }
   }
   if (n == 0) return;
-  __syncthreads();
 
   const int j0 = slice * a.nb;
   const int nbe = min(a.nb, a.F - j0);
@@ -423,91 +428,233 @@ __global__ __launch_bounds__(NT) void moe_experts_kernel(MoeArgs a) {
   const Rows wg = {(const uint8_t*)a.wg + row0 * pitch, MX ? a.sg + row0 * 4 : nullptr, pitch, gp};
   const Rows wu = {GATED ? (const uint8_t*)a.wu + row0 * pitch : nullptr,
                    MX && GATED ? a.su + row0 * 4 : nullptr, pitch, gp};
-  const Rows wd = {(const uint8_t*)a.wd + row0 * pitch, MX ? a.sd + row0 * 4 : nullptr, pitch, gp};
   for (int p0 = 0; p0 < n; p0 += 16 * NTK) {
-    pass<MX, GATED, NTK>(a, sh, ls, wg, wu, wd, j0, nbe, n, p0, slice);
+    if (n - p0 <= 16) pass<MX, GATED, 1>(a, sh.s1, ls, wg, wu, j0, nbe, n, p0, any);
+    else pass<MX, GATED, NTK>(a, sh.s, ls, wg, wu, j0, nbe, n, p0, any);
+    __syncthreads();
+  }
+  if (tid < nbe) a.on[(int64_t)unit * a.F + j0 + tid] = any[tid];
+}
+
+// ---------------------------------------------------------------- down
+
+constexpr int kSeg = 8 * NT;    // neurons whose active ones are listed at a time
+
+// A lane loads CPL columns of 8 neurons (16 bytes of bf16, 8 of codes) and
+// turns them into CPL operands, one a column: operand q of lane l holds
+// column CPL (l % 16) + q at k = neurons 8 (l / 16) .. + 7, and the results
+// of a lane are 4 CPL consecutive columns of token l % 16.
+template <bool MX>
+constexpr int kCpl = MX ? 16 : 8;
+
+template <bool MX>
+__global__ __launch_bounds__(NT, 3) void moe_down_kernel(MoeArgs a) {
+  constexpr int CPL = kCpl<MX>, COLS = 16 * CPL;
+  __shared__ uint16_t act[kSeg];
+  __shared__ int wsum[kWaves];
+  __shared__ f32x4_t red[kWaves][CPL][64];
+  __shared__ int pair[kMoeMaxT];
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = tid >> 6;
+  const int kq = lane >> 4, l15 = lane & 15;
+  const int chunk = blockIdx.x, unit = blockIdx.y;
+  const int n = a.cnt[unit];
+  if (n == 0) return;
+  const int e = a.expert[unit];
+  if (tid < n) pair[tid] = a.list[(int64_t)unit * a.T + tid];
+  const int c0 = chunk * COLS;
+  const int ncol = min(COLS, a.d - c0);            // (the last chunk of codes may be half)
+  const int col = c0 + min(CPL * l15, ncol - CPL);
+  const int64_t pitch = MX ? a.d / 2 : (int64_t)a.d * 2;
+  const int64_t gp = (int64_t)a.E * a.F * 4;
+  const uint8_t* wp = (const uint8_t*)a.wd + (int64_t)e * a.F * pitch + (MX ? col / 2 : col * 2);
+  const uint8_t* sp = MX ? a.sd + (int64_t)e * a.F * 4 + (col >> 7) * gp + ((col >> 5) & 3) : nullptr;
+  const uint8_t* on = a.on + (int64_t)unit * a.F;
+
+  for (int p0 = 0; p0 < n; p0 += 16) {
+    const int nt = min(n - p0, 16);
+    f32x4_t acc[CPL] = {};
+    for (int s0 = 0; s0 < a.F; s0 += kSeg) {
+      // list the segment's active neurons: 8 flags a thread
+      const int f0 = s0 + tid * 8;
+      uint64_t fl = f0 < a.F ? *(const uint64_t*)(on + f0) : 0;   // F is a multiple of 32
+      const int mine = __popcll(fl);
+      int pre = mine;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(pre, o);
+        if (lane >= o) pre += v;
+      }
+      __syncthreads();                 // the last segment's list is done with
+      if (lane == 63) wsum[wave] = pre;
+      __syncthreads();
+      int at = pre - mine, na = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) at += wsum[w];
+        na += wsum[w];
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if ((fl >> (8 * q)) & 1) act[at++] = (uint16_t)(f0 + q);
+      __syncthreads();
+      // 32 neurons a step, the steps shared out over the waves
+      const float* h = a.h + (int64_t)pair[p0 + min(l15, nt - 1)] * a.F;
+#pragma unroll 2
+      for (int ks = wave * 32; ks < na; ks += kWaves * 32) {
+        u32x4_t v[8][CPL / 8];
+        float hv[8];
+        int r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = act[min(ks + kq * 8 + j, na - 1)];
+        if constexpr (MX) {
+          u32x2_t q[8];
+          uint32_t sb[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            q[j] = *(const u32x2_t*)(wp + (int64_t)r[j] * pitch);
+            sb[j] = sp[(int64_t)r[j] * 4];
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) hv[j] = h[r[j]];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < CPL / 8; ++i) v[j][i] = from_codes(q[j][i], sb[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j][0] = *(const u32x4_t*)(wp + (int64_t)r[j] * pitch);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) hv[j] = h[r[j]];
+        }
+        // h in three bf16 parts, whose sum has the 24 bits of a float32: the
+        // matrix instructions take bf16, and one rounding of h to it would
+        // be the layer's largest error by far
+        u32x4_t hp[3];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float x = ks + kq * 8 + j < na ? hv[j] : 0.0f;
+#pragma unroll
+          for (int p = 0; p < 3; ++p) {
+            const __bf16 b = (__bf16)x;
+            const uint32_t bits = __builtin_bit_cast(uint16_t, b);
+            hp[p][j / 2] = j & 1 ? hp[p][j / 2] | bits << 16 : bits;
+            // an infinite or NaN h is all in its first part
+            x = fabsf((float)b) < INFINITY ? x - (float)b : 0.0f;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < CPL; ++q) {
+          // low (q even) or high halves of neurons 2 i and 2 i + 1
+          const uint32_t sel = (q & 1) ? 0x07060302u : 0x05040100u;
+          u32x4_t o;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o[i] = __builtin_amdgcn_perm(v[2 * i + 1][q / 8][(q % 8) >> 1],
+                                         v[2 * i][q / 8][(q % 8) >> 1], sel);
+#pragma unroll
+          for (int p = 2; p >= 0; --p) acc[q] = mfma(o, hp[p], acc[q]);
+        }
+      }
+    }
+    // the waves' sums; thread (token, part of the columns)
+#pragma unroll
+    for (int q = 0; q < CPL; ++q) red[wave][q][lane] = acc[q];
+    __syncthreads();
+    for (int i = tid; i < CPL * 64; i += NT) {
+      const int l = i & 63, q0 = (i >> 6) / 4 * 4, r = (i >> 6) % 4;
+      // row r of operands q0 .. q0 + 3: four consecutive columns
+      const int tk = l & 15, c = 4 * CPL * (l >> 4) + CPL * r + q0;
+      f32x4_t s;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        s[q] = red[0][q0 + q][l][r];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) s[q] += red[w][q0 + q][l][r];
+      }
+      if (tk < nt && c < ncol) *(f32x4_t*)(a.part + (int64_t)pair[p0 + tk] * a.d + c0 + c) = s;
+    }
     __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------- sum
 
-// y of a token's 64 columns: 16 groups of 16 lanes share out the k S
-// partial outputs and are added in LDS.
-__global__ __launch_bounds__(NT) void moe_sum_kernel(MoeArgs a) {
-  __shared__ float p[kMoeMaxK];
-  __shared__ f32x4_t red[16][16];
-  __shared__ float wsum[kWaves];
-  const int t = blockIdx.y;
+// y of a token: a wave 256 columns, the k outputs in the order of their ranks
+__global__ __launch_bounds__(64) void moe_sum_kernel(MoeArgs a) {
+  const int t = blockIdx.y, lane = threadIdx.x;
   if (t >= tokens(a)) return;
-  const int tid = threadIdx.x;
-  const double top = key_value(a.chosen[(int64_t)t * a.k]);
-  if (tid < a.k) p[tid] = expf((float)(key_value(a.chosen[(int64_t)t * a.k + tid]) - top));
-  float total = 0.0f;
+  const long long* chosen = a.chosen + (int64_t)t * a.k;
+  const int c = blockIdx.x * 256 + lane * 4;
+  const float* q = a.part + (int64_t)t * a.k * a.d + min(c, a.d - 4);
+  const long long key = chosen[min(lane, a.k - 1)];
+  f32x4_t v[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    if (r < a.k) v[r] = *(const f32x4_t*)(q + (int64_t)r * a.d);
+  const double top = key_value(__shfl(key, 0));
+  const float p = lane < a.k ? expf((float)(key_value(key) - top)) : 0.0f;
+  float total = p;
   if (!a.normalize) {
-    for (int e = tid; e < a.E; e += NT)
-      total += expf((float)(key_value(a.keys[(int64_t)t * a.E + e]) - top));
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) total += __shfl_xor(total, o);
-    if ((tid & 63) == 0) wsum[tid >> 6] = total;
+    total = 0.0f;
+    for (int f = lane; f < a.E; f += 64)
+      total += expf((float)(key_value(a.keys[(int64_t)t * a.E + f]) - top));
   }
-  __syncthreads();
-  total = 0.0f;
-  if (a.normalize) {
-    for (int r = 0; r < a.k; ++r) total += p[r];
-  } else {
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) total += wsum[w];
-  }
-  if (blockIdx.x == 0 && a.probs && tid < a.k) a.probs[t * a.k + tid] = p[tid] / total;
-  const int g = tid >> 4, c = blockIdx.x * 64 + (tid & 15) * 4;
+  for (int o = 1; o < 64; o <<= 1) total += __shfl_xor(total, o);
+  if (blockIdx.x == 0 && a.probs && lane < a.k) a.probs[t * a.k + lane] = p / total;
   f32x4_t s = {};
-  const int64_t stride = (int64_t)a.T * a.k * a.d;
-  const float* base = a.part + (int64_t)t * a.k * a.d + c;
-#pragma unroll 4
-  for (int i = g; i < a.k * a.S; i += 16) {
-    const int r = i % a.k, sl = i / a.k;
-    s += *(const f32x4_t*)(base + sl * stride + (int64_t)r * a.d) * p[r];
-  }
-  red[g][tid & 15] = s;
-  __syncthreads();
-  if (tid < 16) {
-    f32x4_t v = red[0][tid];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) v += red[i][tid];
-    *(f32x4_t*)(a.y + (int64_t)t * a.d + c) = v / total;
-  }
+  for (int r = 0; r < 8; ++r)
+    if (r < a.k) s += v[r] * __shfl(p, r);
+  for (int r = 8; r < a.k; ++r) s += *(const f32x4_t*)(q + (int64_t)r * a.d) * __shfl(p, r);
+  if (c < a.d) *(f32x4_t*)(a.y + (int64_t)t * a.d + c) = s / total;
 }
 
 template <bool MX, bool GATED>
-hipError_t launch_experts(const MoeArgs& a, hipStream_t s) {
-  const dim3 grid(a.S, a.E);
-  if (a.T <= 16) moe_experts_kernel<MX, GATED, 1><<<grid, NT, 0, s>>>(a);
-  else moe_experts_kernel<MX, GATED, 2><<<grid, NT, 0, s>>>(a);
+hipError_t launch_hidden(const MoeArgs& a, hipStream_t s) {
+  const bool pairs = a.Y != a.E;
+  const dim3 grid((a.F + a.nb - 1) / a.nb, a.Y);
+  if (a.T * a.k <= 12 * a.E) {
+    if (pairs) moe_hidden_kernel<MX, GATED, true, 1><<<grid, NT, 0, s>>>(a);
+    else moe_hidden_kernel<MX, GATED, false, 1><<<grid, NT, 0, s>>>(a);
+  } else {
+    moe_hidden_kernel<MX, GATED, false, 2><<<grid, NT, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
-void moe_slices(int T, int F, int E, int k, int* nb, int* S) {
-  // as many neurons a workgroup as leave two workgroups a CU over the
-  // experts that T tokens can reach: fewer partial outputs to write and add
-  const int64_t reach = (int64_t)T * k < E ? (int64_t)T * k : E;
-  int b = kMoeSlice;
-  while (b > 32 && reach * ((F + b - 1) / b) < 512) b /= 2;
-  *nb = b;
-  *S = (F + b - 1) / b;
+void moe_plan(bool mx, MoeArgs* a) {
+  const int pairs = a->T * a->k;
+  a->Y = pairs < a->E ? pairs : a->E;
+  // as many neurons a workgroup as leave four workgroups a CU
+  const int least = mx ? 32 : 16;
+  int nb = mx ? kSlice<true> : kSlice<false>;
+  while (nb > least && (int64_t)a->Y * ((a->F + nb - 1) / nb) < 1024) nb /= 2;
+  a->nb = nb;
+  const int cols = 16 * (mx ? kCpl<true> : kCpl<false>);
+  a->chunks = (a->d + cols - 1) / cols;
 }
 
 hipError_t launch_moe(bool mx, const MoeArgs& a, hipStream_t s) {
-  moe_logits_kernel<<<dim3((a.E + kWaves - 1) / kWaves, (a.T + kLogitT - 1) / kLogitT), NT, 0, s>>>(a);
+  const unsigned eb = (a.E + kWaves - 1) / kWaves;
+  if (a.T < 4) moe_logits_kernel<1><<<dim3(eb, a.T), NT, 0, s>>>(a);
+  else moe_logits_kernel<4><<<dim3(eb, (a.T + 3) / 4), NT, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const bool gated = a.wu != nullptr;
-  e = mx ? (gated ? launch_experts<true, true>(a, s) : launch_experts<true, false>(a, s))
-         : (gated ? launch_experts<false, true>(a, s) : launch_experts<false, false>(a, s));
+  e = mx ? (gated ? launch_hidden<true, true>(a, s) : launch_hidden<true, false>(a, s))
+         : (gated ? launch_hidden<false, true>(a, s) : launch_hidden<false, false>(a, s));
   if (e != hipSuccess) return e;
-  moe_sum_kernel<<<dim3(a.d / 64, a.T), NT, 0, s>>>(a);
+  const dim3 grid(a.chunks, a.Y);
+  if (mx) moe_down_kernel<true><<<grid, NT, 0, s>>>(a);
+  else moe_down_kernel<false><<<grid, NT, 0, s>>>(a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  moe_sum_kernel<<<dim3((a.d + 255) / 256, a.T), 64, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -9,7 +9,6 @@ namespace sffn {
 constexpr int kMoeMaxT = 256;      // tokens a call
 constexpr int kMoeMaxE = 1024;     // experts
 constexpr int kMoeMaxK = 32;       // experts a token
-constexpr int kMoeSlice = 128;     // most neurons of an expert a workgroup
 
 struct MoeArgs {
   const uint16_t* x;         // [T, d] bf16
@@ -23,18 +22,28 @@ struct MoeArgs {
   int T, d, F, E, k;
   int normalize;
   const int32_t* t_dev;      // nullable: the number of valid tokens
-  int nb;                    // neurons a workgroup (a multiple of 32)
-  int S;                     // workgroups an expert: ceil(F / nb)
+  // A unit is an expert, or, when the (token, rank) pairs are fewer than the
+  // experts, a pair (the pair of an expert's first token works for all of
+  // the expert's tokens, the others have no tokens): Y of them.
+  int Y;
+  int nb;                    // neurons a workgroup of the hidden kernel
+  int chunks;                // column chunks of the down kernel
+  // workspace
   long long* keys;           // [T, E] the logits as ordered integers
   long long* chosen;         // [T, k] the selected experts' keys, by rank
-  float* part;               // [S, T k, d] partial outputs of each (token, rank)
+  int32_t* cnt;              // [Y] tokens of the unit
+  int32_t* expert;           // [Y]
+  int32_t* list;             // [Y, T] its (token, rank) pairs
+  uint8_t* on;               // [Y, F] neuron active for one of its tokens
+  float* h;                  // [T k, F] hidden activations of each pair
+  float* part;               // [T k, d] output of each pair
   float* y;                  // [T, d]
   int32_t* ids;              // [T, k] (nullable)
   float* probs;              // [T, k] (nullable)
 };
 
-// neurons a workgroup and workgroups an expert for T tokens
-void moe_slices(int T, int F, int E, int k, int* nb, int* S);
+// fills Y, nb and chunks from the sizes
+void moe_plan(bool mx, MoeArgs* a);
 hipError_t launch_moe(bool mx, const MoeArgs& a, hipStream_t s);
 
 }  // namespace sffn

@@ -4,12 +4,11 @@
 // block's largest magnitude less that of the largest element, 6 = 1.5 * 4);
 // an element is the e2m1 value nearest to x 2^-e (ties to the even code,
 // saturated at 6). e comes from the exponent bits of the largest magnitude,
-// so no logarithm is taken and the result is exact; the rounding itself is
-// one conversion instruction for two elements, at scale 1 after an exact
-// ldexp (whose operands may be subnormal).
+// so no logarithm is taken and the result is exact; the division and the
+// rounding are one conversion instruction for two elements.
 //
 // Both directions are bound by memory: 2 or 4 bytes read and 17/32 byte
-// written per element, against about five vector instructions.
+// written per element, against about three vector instructions.
 #include "mx.hpp"
 
 namespace sffn {
@@ -25,19 +24,17 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
   return b == 255 ? 255u : (uint32_t)max(b - 2, 0);
 }
 
-// the code byte of two elements of a block (a in the low nibble)
-template <int SEL>
-__device__ __forceinline__ uint32_t pack2(uint32_t old, float a, float b, int k) {
-  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, ldexpf(a, k), ldexpf(b, k), 1.0f, SEL);
-}
+// The conversions take a scale's exponent byte as it is (0 is 2^-127, 255
+// NaN). 8 elements of a block as codes, the first in the lowest nibble.
+__device__ __forceinline__ float scale_of(uint32_t sb) { return __uint_as_float(sb << 23); }
 __device__ __forceinline__ uint32_t pack8(const float* v, uint32_t sb) {
   if (sb == 255u) return 0u;
-  const int k = 127 - (int)sb;
+  const float s = scale_of(sb);
   uint32_t q = 0;
-  q = pack2<0>(q, v[0], v[1], k);
-  q = pack2<1>(q, v[2], v[3], k);
-  q = pack2<2>(q, v[4], v[5], k);
-  q = pack2<3>(q, v[6], v[7], k);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], s, 0);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], s, 1);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4], v[5], s, 2);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6], v[7], s, 3);
   return q;
 }
 
@@ -163,16 +160,17 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
   *(f32x4_t*)p = f32x4_t{v[0], v[1], v[2], v[3]};
   *(f32x4_t*)(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
 }
+__device__ __forceinline__ uint32_t bf16_bits(float v) {
+  return __builtin_bit_cast(uint16_t, (__bf16)v);   // NaN stays NaN
+}
 __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
   u32x4_t o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = f32_to_bf16(v[2 * i]) | (f32_to_bf16(v[2 * i + 1]) << 16);
+  for (int i = 0; i < 4; ++i) o[i] = bf16_bits(v[2 * i]) | (bf16_bits(v[2 * i + 1]) << 16);
   *(u32x4_t*)p = o;
 }
 __device__ __forceinline__ void st(float* p, float v) { *p = v; }
-__device__ __forceinline__ void st(uint16_t* p, float v) {
-  *p = v == v ? (uint16_t)f32_to_bf16(v) : (uint16_t)0x7FC0;
-}
+__device__ __forceinline__ void st(uint16_t* p, float v) { *p = (uint16_t)bf16_bits(v); }
 
 // The values the codes stand for; the lanes' columns as in
 // mx_quantize_kernel. A bf16 value is exact too (two significant bits)
@@ -198,19 +196,14 @@ __global__ __launch_bounds__(NT) void mx_dequantize_kernel(const uint8_t* __rest
 #pragma unroll
   for (int i = 0; i < kQRows; ++i) {
     if (r0 + i >= R) break;
-    float v[8];
-    const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 0);
-    const f32x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 1);
-    const f32x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 2);
-    const f32x2_t e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 3);
-    v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1];
-    v[4] = d[0]; v[5] = d[1]; v[6] = e[0]; v[7] = e[1];
-    const int k = (int)sb[i] - 127;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      v[j] = sb[i] == 255u ? __uint_as_float(0x7FC00000u) : ldexpf(v[j], k);
+    const float s = scale_of(sb[i]);
+    const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], s, 0);
+    const f32x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], s, 1);
+    const f32x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], s, 2);
+    const f32x2_t e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], s, 3);
+    const float v[8] = {a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
     E* o = out + (r0 + i) * ldo + c;
-    if (vec && c + 8 <= K && sb[i] != 255u) {
+    if (vec && c + 8 <= K) {
       store8(o, v);
     } else {
 #pragma unroll

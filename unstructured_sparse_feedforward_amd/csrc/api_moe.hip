@@ -27,7 +27,7 @@ sffn_status validate(const sffn_moe_desc* D) {
 }
 
 struct Layout {
-  size_t keys, chosen, cnt, expert, list, on, h, part, total;
+  size_t keys, expert, weight, on, h, part, total;
 };
 
 // the sizes of a call, with what moe_plan derives from them
@@ -53,10 +53,8 @@ Layout layout(const MoeArgs& a) {
   };
   const size_t T = a.T, pairs = T * a.k;
   L.keys = take(T * a.E * 8);
-  L.chosen = take(pairs * 8);
-  L.cnt = take((size_t)a.Y * 4);
-  L.expert = take((size_t)a.Y * 4);
-  L.list = take((size_t)a.Y * T * 4);
+  L.expert = take(pairs * 4);
+  L.weight = take(pairs * 4);
   L.on = take((size_t)a.Y * a.F);
   L.h = take(pairs * a.F * 4);
   L.part = take(pairs * a.d * 4);
@@ -114,10 +112,8 @@ sffn_status sffn_moe_forward(const sffn_moe_desc* desc, const void* x, const sff
   a.sd = w->down_scales;
   a.t_dev = n_tokens;
   a.keys = (long long*)(base + L.keys);
-  a.chosen = (long long*)(base + L.chosen);
-  a.cnt = (int32_t*)(base + L.cnt);
   a.expert = (int32_t*)(base + L.expert);
-  a.list = (int32_t*)(base + L.list);
+  a.weight = (float*)(base + L.weight);
   a.on = (uint8_t*)(base + L.on);
   a.h = (float*)(base + L.h);
   a.part = (float*)(base + L.part);

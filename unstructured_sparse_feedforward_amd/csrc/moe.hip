@@ -7,10 +7,9 @@
 // With few tokens the time is that of reading the selected experts'
 // weights, so every weight is read once (per 16 or 32 of its expert's
 // tokens). Four launches:
-//   logits  64-bit sums;
-//   hidden  a workgroup has an expert and a slice of its neurons: it finds
-//           the expert's tokens from the logits, computes z for all of them,
-//           and u only for the neurons that are active (z > 0) for one of
+//   route   logits, top k and weights, a workgroup a token;
+//   hidden  a workgroup has an expert and a slice of its neurons: it computes
+//           z for all of the expert's tokens, and u only for the neurons that are active (z > 0) for one of
 //           them, as in the rest of the library;
 //   down    a workgroup has an expert and a chunk of y's columns, and reads
 //           those of the active neurons' rows;
@@ -23,6 +22,22 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int kWaves = NT / 64;
+
+// Compile-time loop: f(Int<0>), .., f(Int<N - 1>).
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+template <int N, int K = 0, typename F>
+__device__ __forceinline__ void unroll(F&& f) {
+  if constexpr (K < N) {
+    f(Int<K>{});
+    unroll<N, K + 1>(f);
+  }
+}
+
+// the wave's index, known to be the same in all its lanes
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 __device__ __forceinline__ int tokens(const MoeArgs& a) {
   return a.t_dev ? min(max(*a.t_dev, 0), a.T) : a.T;
@@ -40,42 +55,133 @@ __device__ __forceinline__ double key_value(long long k) {
   return __longlong_as_double(k < 0 ? k ^ 0x7FFFFFFFFFFFFFFFll : k);
 }
 
-// ---------------------------------------------------------------- logits
+// ---------------------------------------------------------------- router
 
-// One wave an expert and TT tokens. The sums are 64-bit: two experts'
-// logits then compare as their exact values do (the product of two bf16
-// values has 16 bits), whatever the order of summation.
-template <int TT>
-__global__ __launch_bounds__(NT) void moe_logits_kernel(MoeArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int e = blockIdx.x * kWaves + (threadIdx.x >> 6);
-  const int T = tokens(a);
-  const int t0 = blockIdx.y * TT;
-  if (e >= a.E || t0 >= T) return;
-  const uint16_t* w = a.router + (int64_t)e * a.d;
-  double s[TT] = {};
+// The logits are summed in 64 bits: two experts' then compare as their exact
+// values do (the product of two bf16 values has 16 bits), whatever the order
+// of summation.
+constexpr int kRouteWaves = 16;
+constexpr int64_t kRouteOne = 1 << 18;   // most elements of a router that one workgroup reads
+
+// EE experts' logits of a token (the same in every lane)
+template <int EE>
+__device__ __forceinline__ void logits(const MoeArgs& a, const uint16_t* x, const uint16_t* w,
+                                       const int (&e)[EE], int lane, double (&s)[EE]) {
+#pragma unroll
+  for (int i = 0; i < EE; ++i) s[i] = 0.0;
 #pragma unroll 4
   for (int c = lane * 8; c < a.d; c += 512) {
-    const u32x4_t wr = *(const u32x4_t*)(w + c);
-    u32x4_t xr[TT];
+    const u32x4_t xr = *(const u32x4_t*)(x + c);
+    u32x4_t wr[EE];
 #pragma unroll
-    for (int i = 0; i < TT; ++i)
-      xr[i] = *(const u32x4_t*)(a.x + (int64_t)min(t0 + i, T - 1) * a.d + c);
-    float wv[8];
-    Vec<uint16_t, 8>::cvt(wr, wv);
+    for (int i = 0; i < EE; ++i) wr[i] = *(const u32x4_t*)(w + (int64_t)e[i] * a.d + c);
+    float xv[8];
+    Vec<uint16_t, 8>::cvt(xr, xv);
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      float xv[8];
-      Vec<uint16_t, 8>::cvt(xr[i], xv);
+    for (int i = 0; i < EE; ++i) {
+      float wv[8];
+      Vec<uint16_t, 8>::cvt(wr[i], wv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[i] = fma((double)wv[j], (double)xv[j], s[i]);
     }
   }
 #pragma unroll
-  for (int i = 0; i < TT; ++i) {
+  for (int i = 0; i < EE; ++i)
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) s[i] += __shfl_xor(s[i], o);
-    if (lane == 0 && t0 + i < T) a.keys[(int64_t)(t0 + i) * a.E + e] = order_key(s[i]);
+}
+
+// A wave an expert and token, for routers that one workgroup a token would
+// read too slowly.
+__global__ __launch_bounds__(NT) void moe_logits_kernel(MoeArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int e = blockIdx.x * kWaves + wave_id();
+  const int t = blockIdx.y;
+  if (e >= a.E || t >= tokens(a)) return;
+  const int es[1] = {e};
+  double s[1];
+  logits<1>(a, a.x + (int64_t)t * a.d, a.router, es, lane, s);
+  if (lane == 0) a.keys[(int64_t)t * a.E + e] = order_key(s[0]);
+}
+
+// A workgroup a token: its logits (or the keys of moe_logits_kernel), every
+// expert's rank (the number of experts before it), and by rank the k
+// experts and their weights.
+template <bool LOGITS>
+__global__ __launch_bounds__(kRouteWaves * 64) void moe_route_kernel(MoeArgs a) {
+  __shared__ long long keys[kMoeMaxE];
+  __shared__ int before[kMoeMaxE];
+  __shared__ long long top;
+  __shared__ float ex[kMoeMaxK];
+  __shared__ float wsum[kRouteWaves];
+  constexpr int N = kRouteWaves * 64;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = wave_id();
+  const int t = blockIdx.x;
+  if (t >= tokens(a)) return;
+  if (LOGITS) {
+    // four experts of a wave at a time, so that their loads are in flight together
+    for (int e0 = wave * 4; e0 < a.E; e0 += kRouteWaves * 4) {
+      int es[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) es[i] = min(e0 + i, a.E - 1);
+      double s[4];
+      logits<4>(a, a.x + (int64_t)t * a.d, a.router, es, lane, s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lane == 0 && e0 + i < a.E) keys[e0 + i] = order_key(s[i]);
+    }
+  } else {
+    for (int e = tid; e < a.E; e += N) keys[e] = a.keys[(int64_t)t * a.E + e];
+  }
+  for (int e = tid; e < a.E; e += N) before[e] = 0;
+  __syncthreads();
+  // the comparisons shared out over all threads
+  const int parts = max(N / a.E, 1);
+  for (int i = tid; i < a.E * parts; i += N) {
+    const int e = i % a.E;
+    const long long mine = keys[e];
+    int n = 0;
+    for (int o = i / a.E; o < a.E; o += parts) {
+      const long long other = keys[o];
+      n += other > mine || (other == mine && o < e);
+    }
+    if (n) atomicAdd(&before[e], n);   // whole numbers: any order
+  }
+  __syncthreads();
+  // exponentials below that of the largest logit
+  for (int e = tid; e < a.E; e += N)
+    if (before[e] == 0) top = keys[e];
+  __syncthreads();
+  const double l0 = key_value(top);
+  float sum = 0.0f;
+  for (int e = tid; e < a.E; e += N) {
+    const int r = before[e];
+    if (r < a.k || !a.normalize) {
+      const float v = expf((float)(key_value(keys[e]) - l0));
+      if (!a.normalize) sum += v;
+      if (r < a.k) {
+        ex[r] = v;
+        a.expert[t * a.k + r] = e;
+        if (a.ids) a.ids[t * a.k + r] = e;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
+  if (lane == 0) wsum[wave] = sum;
+  __syncthreads();
+  if (tid < a.k) {
+    float total = 0.0f;
+    if (a.normalize) {
+      for (int r = 0; r < a.k; ++r) total += ex[r];
+    } else {
+      for (int w = 0; w < kRouteWaves; ++w) total += wsum[w];
+    }
+    const float p = ex[tid] / total;
+    a.weight[t * a.k + tid] = p;
+    if (a.probs) a.probs[t * a.k + tid] = p;
   }
 }
 
@@ -107,68 +213,69 @@ __device__ __forceinline__ f32x4_t mfma(const u32x4_t& w, const u32x4_t& v, cons
 
 // ---------------------------------------------------------------- products with x
 
-// acc[i][n] += rows r[i] (16 of them, one a lane's row) . x of 16 tokens,
-// over steps part, part + parts, .. of d. The instruction's k order is free
-// as long as both operands agree: lane l takes 16 contiguous bytes of row
-// l % 16, so that the four lanes of a row cover 64 bytes: 32 bf16 values, the
-// instruction's own order, or 128 codes, four instructions' worth.
+// acc[i][n] += rows r[i] (16 of them, one a lane's row) . x of 16 tokens
+// (xo[n]: the offset of a lane's token), over steps part, part + parts, .. of
+// d. The instruction's k order is free as long as both operands agree: lane l
+// takes 16 contiguous bytes of row l % 16, so that the four lanes of a row
+// cover 64 bytes: 32 bf16 values, the instruction's own order, or 128 codes,
+// four instructions' worth. D steps' loads are always in flight: a step's
+// registers are loaded again as soon as it is multiplied. Addresses are 32-bit
+// offsets from one that all lanes share: a register a row, no arithmetic.
 template <bool MX, int MT, int NTK>
 __device__ __forceinline__ void dots(const MoeArgs& a, const Rows& w, const int (&r)[MT],
-                                     const uint16_t* const (&xt)[NTK], int lane, int part,
-                                     int parts, f32x4_t (&acc)[MT][NTK]) {
+                                     const uint32_t (&xo)[NTK], int lane, int part, int parts,
+                                     f32x4_t (&acc)[MT][NTK]) {
   const int kq = lane >> 4;
-  const uint8_t* p[MT];
+  constexpr int D = MX ? 2 : 4, NF = MX ? 4 : 2;   // MFMAs a step and block
+  constexpr int SC = MX ? 128 : 64;                // columns a step
+  uint32_t po[MT], so[MT], xp[NTK];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) p[i] = w.p + (int64_t)r[i] * w.pitch + kq * 16;
-  if constexpr (MX) {
-    const uint8_t* ps[MT];
+  for (int i = 0; i < MT; ++i) {
+    po[i] = (uint32_t)r[i] * (uint32_t)w.pitch + kq * 16;
+    so[i] = (uint32_t)r[i] * 4 + kq;
+  }
 #pragma unroll
-    for (int i = 0; i < MT; ++i) ps[i] = w.sc + (int64_t)r[i] * 4 + kq;
-    const int G = a.d / 128;
-#pragma unroll 2
-    for (int g = part; g < G; g += parts) {
-      u32x4_t q[MT];
-      uint32_t sb[MT];
-      u32x4_t xv[NTK][4];
+  for (int n = 0; n < NTK; ++n) xp[n] = xo[n] + kq * (MX ? 64 : 16);
+  const uint8_t* xb = (const uint8_t*)a.x;
+  u32x4_t q[D][MT][MX ? 1 : 2], xv[D][NTK][NF];
+  uint32_t sb[D][MT];
+  auto load = [&](auto ss, int g) {
+    constexpr int s = decltype(ss)::value;
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        q[i] = *(const u32x4_t*)(p[i] + (int64_t)g * 64);
-        sb[i] = ps[i][g * w.gpitch];
+    for (int i = 0; i < MT; ++i) {
+      if constexpr (MX) {
+        q[s][i][0] = *(const u32x4_t*)(w.p + (int64_t)g * 64 + po[i]);
+        sb[s][i] = *(w.sc + g * w.gpitch + so[i]);
+      } else {
+        q[s][i][0] = *(const u32x4_t*)(w.p + (int64_t)g * 128 + po[i]);
+        q[s][i][1] = *(const u32x4_t*)(w.p + (int64_t)g * 128 + 64 + po[i]);
       }
+    }
 #pragma unroll
-      for (int n = 0; n < NTK; ++n)
+    for (int n = 0; n < NTK; ++n)
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
-          xv[n][f] = *(const u32x4_t*)(xt[n] + g * 128 + kq * 32 + f * 8);
+      for (int f = 0; f < NF; ++f)
+        xv[s][n][f] = *(const u32x4_t*)(xb + (int64_t)g * (SC * 2) + f * (MX ? 16 : 64) + xp[n]);
+  };
+  const int G = a.d / SC;
+  unroll<D>([&](auto s) {
+    if (part + decltype(s)::value * parts < G) load(s, part + decltype(s)::value * parts);
+  });
+  for (int g0 = part; g0 < G; g0 += D * parts) {
+    unroll<D>([&](auto ss) {
+      constexpr int s = decltype(ss)::value;
+      const int g = g0 + s * parts;
+      if (g >= G) return;
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int f = 0; f < NF; ++f)
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          const u32x4_t wv = from_codes(q[i][f], sb[i]);
+        for (int i = 0; i < MT; ++i) {
+          const u32x4_t wv = MX ? from_codes(q[s][i][0][f], sb[s][i]) : q[s][i][MX ? 0 : f];
 #pragma unroll
-          for (int n = 0; n < NTK; ++n) acc[i][n] = mfma(wv, xv[n][f], acc[i][n]);
+          for (int n = 0; n < NTK; ++n) acc[i][n] = mfma(wv, xv[s][n][f], acc[i][n]);
         }
-    }
-  } else {
-    const int G = a.d / 64;
-#pragma unroll 4
-    for (int g = part; g < G; g += parts) {
-      u32x4_t wv[MT][2], xv[NTK][2];
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) wv[i][f] = *(const u32x4_t*)(p[i] + (int64_t)g * 128 + f * 64);
-#pragma unroll
-        for (int n = 0; n < NTK; ++n)
-          xv[n][f] = *(const u32x4_t*)(xt[n] + g * 64 + f * 32 + kq * 8);
-      }
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int n = 0; n < NTK; ++n) acc[i][n] = mfma(wv[i][f], xv[n][f], acc[i][n]);
-    }
+      if (g + D * parts < G) load(ss, g + D * parts);
+    });
   }
 }
 
@@ -198,11 +305,11 @@ struct Shared {
 // the row of position i. Leaves the shares in sh.red, joined by share_sum.
 template <bool MX, int NTK, typename F>
 __device__ __forceinline__ int share_products(const MoeArgs& a, Shared<MX, NTK>& sh,
-                                              const Rows& w, const uint16_t* const (&xt)[NTK],
-                                              int tiles, F&& row) {
+                                              const Rows& w, const uint32_t (&xo)[NTK], int tiles,
+                                              F&& row) {
   constexpr int MT = kBlocks<MX>;
   const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
+  const int wave = wave_id();
   const int lg = tiles <= 1 ? 0 : tiles <= 2 ? 1 : 2;
   const int parts = kWaves >> lg, tile = wave >> (2 - lg), part = wave & (parts - 1);
   if (tile < tiles) {
@@ -210,7 +317,7 @@ __device__ __forceinline__ int share_products(const MoeArgs& a, Shared<MX, NTK>&
     int r[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) r[i] = row((tile * MT + i) * 16 + (lane & 15));
-    dots<MX, MT, NTK>(a, w, r, xt, lane, part, parts, acc);
+    dots<MX, MT, NTK>(a, w, r, xo, lane, part, parts, acc);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -228,15 +335,43 @@ __device__ __forceinline__ f32x4_t share_sum(const Shared<MX, NTK>& sh, int part
   return s;
 }
 
-struct Lists {
-  int tok[kMoeMaxT];                   // the unit's tokens, ascending
-  int pair[kMoeMaxT];                  // token * k + rank
-  int rank[kMoeMaxT];                  // of each token (k and above: not selected)
-  int wsum[kWaves];
-  int expert;
-};
-
 __device__ __forceinline__ uint64_t below(int lane) { return lane ? ~0ull >> (64 - lane) : 0ull; }
+
+// A unit's (token, rank) pairs in ascending order; returns their number. A
+// unit is an expert, or a pair, whose expert's pairs it has if it is the
+// first of them (else none). Called by all NT threads.
+struct Lists {
+  int pair[kMoeMaxT];
+  int wsum[kWaves];
+};
+__device__ __forceinline__ int unit_pairs(const MoeArgs& a, int unit, Lists& ls, int* expert) {
+  const int lane = threadIdx.x & 63;
+  const int wave = wave_id();
+  const int np = tokens(a) * a.k;
+  const bool pairs = a.Y != a.E;
+  if (pairs && unit >= np) return 0;
+  const int e = pairs ? a.expert[unit] : unit;
+  *expert = e;
+  int n = 0;
+  for (int i0 = 0; i0 < np; i0 += NT) {
+    const int i = i0 + threadIdx.x;
+    const bool mine = i < np && a.expert[i] == e;
+    const uint64_t b = __ballot(mine);
+    if (i0) __syncthreads();
+    if (lane == 0) ls.wsum[wave] = __popcll(b);
+    __syncthreads();
+    int at = n + __popcll(b & below(lane));
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) at += ls.wsum[w];
+      n += ls.wsum[w];
+    }
+    if (mine) ls.pair[at] = i;
+  }
+  __syncthreads();
+  if (pairs && n > 0 && ls.pair[0] != unit) n = 0;
+  return n;
+}
 
 // 16 NTK of the unit's tokens (list positions p0 ..) through the slice's
 // neurons j0 .. j0 + nbe: their h, and in `any` the neurons active for one.
@@ -246,17 +381,17 @@ __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, cons
                                      int p0, uint8_t* any) {
   constexpr int MT = kBlocks<MX>;
   const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
+  const int wave = wave_id();
   const int tid = threadIdx.x;
   const int nt = min(n - p0, 16 * NTK);   // tokens of this pass
-  const uint16_t* xt[NTK];
+  uint32_t xo[NTK];
 #pragma unroll
   for (int i = 0; i < NTK; ++i)
-    xt[i] = a.x + (int64_t)ls.tok[p0 + min(i * 16 + (lane & 15), nt - 1)] * a.d;
+    xo[i] = (uint32_t)(ls.pair[p0 + min(i * 16 + (lane & 15), nt - 1)] / a.k) * (uint32_t)(a.d * 2);
 
   if (tid < kSlice<MX>) sh.on[tid] = 0;
   const int blocks = nbe / 16;
-  int parts = share_products<MX, NTK>(a, sh, wg, xt, (blocks + MT - 1) / MT,
+  int parts = share_products<MX, NTK>(a, sh, wg, xo, (blocks + MT - 1) / MT,
                                       [&](int i) { return j0 + min(i, nbe - 1); });
   __syncthreads();
   for (int e = tid; e < blocks * NTK * 64; e += NT) {
@@ -293,7 +428,7 @@ __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, cons
   __syncthreads();
   const int na = sh.na;
   if (na == 0) return;
-  parts = share_products<MX, NTK>(a, sh, wu, xt, (na + 16 * MT - 1) / (16 * MT),
+  parts = share_products<MX, NTK>(a, sh, wu, xo, (na + 16 * MT - 1) / (16 * MT),
                                   [&](int i) { return j0 + sh.act[min(i, na - 1)]; });
   __syncthreads();
   // h of the active neurons; the others' is not read
@@ -316,108 +451,19 @@ __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, cons
   }
 }
 
-template <bool MX, bool GATED, bool PAIRS, int NTK>
+template <bool MX, bool GATED, int NTK>
 __global__ __launch_bounds__(NT, NTK == 1 ? 4 : 2) void moe_hidden_kernel(MoeArgs a) {
   __shared__ Lists ls;
   __shared__ uint8_t any[kSlice<MX>];
   __shared__ union {
-    struct {
-      long long keys[kMoeMaxE];
-      int before[kMoeMaxE];
-    } r;
     Shared<MX, 1> s1;
     Shared<MX, NTK> s;
   } sh;
   const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int wave = tid >> 6;
   const int slice = blockIdx.x, unit = blockIdx.y;
-  const int T = tokens(a);
-  const long long* __restrict__ keys = a.keys;
-  int e = unit, first = 0;
-  if (PAIRS) {
-    first = unit / a.k;
-    // every expert's rank for the pair's token: the experts before it, the
-    // comparisons shared out over all threads
-    const int rank = unit % a.k;
-    for (int f = tid; f < a.E; f += NT) {
-      sh.r.keys[f] = first < T ? keys[(int64_t)first * a.E + f] : 0;
-      sh.r.before[f] = 0;
-    }
-    __syncthreads();
-    const int parts = max(NT / a.E, 1);
-    for (int i = tid; i < a.E * parts; i += NT) {
-      const int f = i % a.E;
-      const long long mine = sh.r.keys[f];
-      int before = 0;
-      for (int o = i / a.E; o < a.E; o += parts) {
-        const long long other = sh.r.keys[o];
-        before += other > mine || (other == mine && o < f);
-      }
-      atomicAdd(&sh.r.before[f], before);   // whole numbers: any order
-    }
-    __syncthreads();
-    for (int f = tid; f < a.E; f += NT)
-      if (sh.r.before[f] == rank) ls.expert = f;
-    __syncthreads();
-    e = ls.expert;
-  }
-  // the expert's rank for each token: kAt tokens a wave at a time, so that
-  // their loads are in flight together
-  constexpr int kAt = 8;
-  for (int t0 = wave * kAt; t0 < T; t0 += kWaves * kAt) {
-    long long mine[kAt];
-    int before[kAt] = {};
-#pragma unroll
-    for (int i = 0; i < kAt; ++i) mine[i] = keys[(int64_t)min(t0 + i, T - 1) * a.E + e];
-    for (int o = 0; o < a.E; o += 64) {
-      const int f = min(o + lane, a.E - 1);
-      long long other[kAt];
-#pragma unroll
-      for (int i = 0; i < kAt; ++i) other[i] = keys[(int64_t)min(t0 + i, T - 1) * a.E + f];
-#pragma unroll
-      for (int i = 0; i < kAt; ++i)
-        before[i] += __popcll(__ballot(o + lane < a.E &&
-                                       (other[i] > mine[i] || (other[i] == mine[i] && f < e))));
-    }
-    if (lane == 0) {
-#pragma unroll
-      for (int i = 0; i < kAt; ++i)
-        if (t0 + i < T) ls.rank[t0 + i] = before[i];
-    }
-  }
+  int e;
   if (tid < kSlice<MX>) any[tid] = 0;
-  __syncthreads();
-  // list its tokens, one a thread, in ascending order
-  const bool mine = tid < T && ls.rank[tid] < a.k;
-  const uint64_t b = __ballot(mine);
-  if (lane == 0) ls.wsum[wave] = __popcll(b);
-  __syncthreads();
-  int at = __popcll(b & below(lane)), n = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) at += ls.wsum[w];
-    n += ls.wsum[w];
-  }
-  if (mine) {
-    ls.tok[at] = tid;
-    ls.pair[at] = tid * a.k + ls.rank[tid];
-  }
-  __syncthreads();
-  if (PAIRS && (first >= T || ls.tok[0] != first)) n = 0;   // its first token's pair works for it
-  if (slice == 0) {
-    // what the down kernel needs of the routing
-    if (tid == 0) {
-      a.cnt[unit] = n;
-      a.expert[unit] = e;
-    }
-    if (mine && n > 0) {
-      const int pair = tid * a.k + ls.rank[tid];
-      a.list[(int64_t)unit * a.T + at] = pair;
-      a.chosen[pair] = keys[(int64_t)tid * a.E + e];
-      if (a.ids) a.ids[pair] = e;
-    }
-  }
+  const int n = unit_pairs(a, unit, ls, &e);
   if (n == 0) return;
 
   const int j0 = slice * a.nb;
@@ -453,23 +499,25 @@ __global__ __launch_bounds__(NT, 3) void moe_down_kernel(MoeArgs a) {
   __shared__ uint16_t act[kSeg];
   __shared__ int wsum[kWaves];
   __shared__ f32x4_t red[kWaves][CPL][64];
-  __shared__ int pair[kMoeMaxT];
+  __shared__ Lists ls;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
-  const int wave = tid >> 6;
+  const int wave = wave_id();
   const int kq = lane >> 4, l15 = lane & 15;
   const int chunk = blockIdx.x, unit = blockIdx.y;
-  const int n = a.cnt[unit];
+  int e;
+  const int n = unit_pairs(a, unit, ls, &e);
   if (n == 0) return;
-  const int e = a.expert[unit];
-  if (tid < n) pair[tid] = a.list[(int64_t)unit * a.T + tid];
   const int c0 = chunk * COLS;
   const int ncol = min(COLS, a.d - c0);            // (the last chunk of codes may be half)
   const int col = c0 + min(CPL * l15, ncol - CPL);
   const int64_t pitch = MX ? a.d / 2 : (int64_t)a.d * 2;
   const int64_t gp = (int64_t)a.E * a.F * 4;
-  const uint8_t* wp = (const uint8_t*)a.wd + (int64_t)e * a.F * pitch + (MX ? col / 2 : col * 2);
-  const uint8_t* sp = MX ? a.sd + (int64_t)e * a.F * 4 + (col >> 7) * gp + ((col >> 5) & 3) : nullptr;
+  // a row's place as a 32-bit offset from an address that all lanes share
+  const uint8_t* wp = (const uint8_t*)a.wd + (int64_t)e * a.F * pitch;
+  const uint32_t cb = MX ? col / 2 : col * 2, rp = (uint32_t)pitch;
+  const uint8_t* sp = MX ? a.sd + (int64_t)e * a.F * 4 : nullptr;
+  const uint32_t so = (uint32_t)((col >> 7) * gp + ((col >> 5) & 3));
   const uint8_t* on = a.on + (int64_t)unit * a.F;
 
   for (int p0 = 0; p0 < n; p0 += 16) {
@@ -499,62 +547,74 @@ __global__ __launch_bounds__(NT, 3) void moe_down_kernel(MoeArgs a) {
       for (int q = 0; q < 8; ++q)
         if ((fl >> (8 * q)) & 1) act[at++] = (uint16_t)(f0 + q);
       __syncthreads();
-      // 32 neurons a step, the steps shared out over the waves
-      const float* h = a.h + (int64_t)pair[p0 + min(l15, nt - 1)] * a.F;
-#pragma unroll 2
-      for (int ks = wave * 32; ks < na; ks += kWaves * 32) {
-        u32x4_t v[8][CPL / 8];
-        float hv[8];
-        int r[8];
+      // 32 neurons a step, the steps shared out over the waves, the next
+      // step's loads in flight
+      const uint32_t ho = (uint32_t)ls.pair[p0 + min(l15, nt - 1)] * (uint32_t)a.F * 4;
+      u32x2_t q[2][8];
+      uint32_t sb[2][8];
+      u32x4_t raw[2][8];
+      float hv[2][8];
+      auto load = [&](auto bb, int ks) {
+        constexpr int b = decltype(bb)::value;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = act[min(ks + kq * 8 + j, na - 1)];
-        if constexpr (MX) {
-          u32x2_t q[8];
-          uint32_t sb[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            q[j] = *(const u32x2_t*)(wp + (int64_t)r[j] * pitch);
-            sb[j] = sp[(int64_t)r[j] * 4];
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t r = act[min(ks + kq * 8 + j, na - 1)];
+          if constexpr (MX) {
+            q[b][j] = *(const u32x2_t*)(wp + (r * rp + cb));
+            sb[b][j] = *(sp + (r * 4 + so));
+          } else {
+            raw[b][j] = *(const u32x4_t*)(wp + (r * rp + cb));
           }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) hv[j] = h[r[j]];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < CPL / 8; ++i) v[j][i] = from_codes(q[j][i], sb[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j][0] = *(const u32x4_t*)(wp + (int64_t)r[j] * pitch);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) hv[j] = h[r[j]];
+          hv[b][j] = *(const float*)((const uint8_t*)a.h + (r * 4 + ho));
         }
+      };
+      auto step = [&](auto bb, int ks) {
+        constexpr int b = decltype(bb)::value;
+        u32x4_t v[8][CPL / 8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < CPL / 8; ++i) {
+            if constexpr (MX) v[j][i] = from_codes(q[b][j][i], sb[b][j]);
+            else v[j][i] = raw[b][j];
+          }
         // h in three bf16 parts, whose sum has the 24 bits of a float32: the
         // matrix instructions take bf16, and one rounding of h to it would
         // be the layer's largest error by far
         u32x4_t hp[3];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float x = ks + kq * 8 + j < na ? hv[j] : 0.0f;
+          float x = ks + kq * 8 + j < na ? hv[b][j] : 0.0f;
 #pragma unroll
           for (int p = 0; p < 3; ++p) {
-            const __bf16 b = (__bf16)x;
-            const uint32_t bits = __builtin_bit_cast(uint16_t, b);
+            const __bf16 xb = (__bf16)x;
+            const uint32_t bits = __builtin_bit_cast(uint16_t, xb);
             hp[p][j / 2] = j & 1 ? hp[p][j / 2] | bits << 16 : bits;
             // an infinite or NaN h is all in its first part
-            x = fabsf((float)b) < INFINITY ? x - (float)b : 0.0f;
+            x = fabsf((float)xb) < INFINITY ? x - (float)xb : 0.0f;
           }
         }
 #pragma unroll
-        for (int q = 0; q < CPL; ++q) {
-          // low (q even) or high halves of neurons 2 i and 2 i + 1
-          const uint32_t sel = (q & 1) ? 0x07060302u : 0x05040100u;
+        for (int c = 0; c < CPL; ++c) {
+          // low (c even) or high halves of neurons 2 i and 2 i + 1
+          const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
           u32x4_t o;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            o[i] = __builtin_amdgcn_perm(v[2 * i + 1][q / 8][(q % 8) >> 1],
-                                         v[2 * i][q / 8][(q % 8) >> 1], sel);
+            o[i] = __builtin_amdgcn_perm(v[2 * i + 1][c / 8][(c % 8) >> 1],
+                                         v[2 * i][c / 8][(c % 8) >> 1], sel);
 #pragma unroll
-          for (int p = 2; p >= 0; --p) acc[q] = mfma(o, hp[p], acc[q]);
+          for (int p = 2; p >= 0; --p) acc[c] = mfma(o, hp[p], acc[c]);
+        }
+      };
+      constexpr int S = kWaves * 32;
+      if (wave * 32 < na) load(Int<0>{}, wave * 32);
+      for (int ks = wave * 32; ks < na; ks += 2 * S) {
+        if (ks + S < na) load(Int<1>{}, ks + S);
+        step(Int<0>{}, ks);
+        if (ks + S < na) {
+          if (ks + 2 * S < na) load(Int<0>{}, ks + 2 * S);
+          step(Int<1>{}, ks + S);
         }
       }
     }
@@ -573,7 +633,7 @@ __global__ __launch_bounds__(NT, 3) void moe_down_kernel(MoeArgs a) {
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) s[q] += red[w][q0 + q][l][r];
       }
-      if (tk < nt && c < ncol) *(f32x4_t*)(a.part + (int64_t)pair[p0 + tk] * a.d + c0 + c) = s;
+      if (tk < nt && c < ncol) *(f32x4_t*)(a.part + (int64_t)ls.pair[p0 + tk] * a.d + c0 + c) = s;
     }
     __syncthreads();
   }
@@ -585,43 +645,21 @@ __global__ __launch_bounds__(NT, 3) void moe_down_kernel(MoeArgs a) {
 __global__ __launch_bounds__(64) void moe_sum_kernel(MoeArgs a) {
   const int t = blockIdx.y, lane = threadIdx.x;
   if (t >= tokens(a)) return;
-  const long long* chosen = a.chosen + (int64_t)t * a.k;
   const int c = blockIdx.x * 256 + lane * 4;
-  const float* q = a.part + (int64_t)t * a.k * a.d + min(c, a.d - 4);
-  const long long key = chosen[min(lane, a.k - 1)];
-  f32x4_t v[8];
-#pragma unroll
-  for (int r = 0; r < 8; ++r)
-    if (r < a.k) v[r] = *(const f32x4_t*)(q + (int64_t)r * a.d);
-  const double top = key_value(__shfl(key, 0));
-  const float p = lane < a.k ? expf((float)(key_value(key) - top)) : 0.0f;
-  float total = p;
-  if (!a.normalize) {
-    total = 0.0f;
-    for (int f = lane; f < a.E; f += 64)
-      total += expf((float)(key_value(a.keys[(int64_t)t * a.E + f]) - top));
-  }
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) total += __shfl_xor(total, o);
-  if (blockIdx.x == 0 && a.probs && lane < a.k) a.probs[t * a.k + lane] = p / total;
+  if (c >= a.d) return;
+  const float* p = a.weight + (int64_t)t * a.k;
+  const float* q = a.part + (int64_t)t * a.k * a.d + c;
   f32x4_t s = {};
-#pragma unroll
-  for (int r = 0; r < 8; ++r)
-    if (r < a.k) s += v[r] * __shfl(p, r);
-  for (int r = 8; r < a.k; ++r) s += *(const f32x4_t*)(q + (int64_t)r * a.d) * __shfl(p, r);
-  if (c < a.d) *(f32x4_t*)(a.y + (int64_t)t * a.d + c) = s / total;
+#pragma unroll 8
+  for (int r = 0; r < a.k; ++r) s += *(const f32x4_t*)(q + (int64_t)r * a.d) * p[r];
+  *(f32x4_t*)(a.y + (int64_t)t * a.d + c) = s;
 }
 
 template <bool MX, bool GATED>
 hipError_t launch_hidden(const MoeArgs& a, hipStream_t s) {
-  const bool pairs = a.Y != a.E;
   const dim3 grid((a.F + a.nb - 1) / a.nb, a.Y);
-  if (a.T * a.k <= 12 * a.E) {
-    if (pairs) moe_hidden_kernel<MX, GATED, true, 1><<<grid, NT, 0, s>>>(a);
-    else moe_hidden_kernel<MX, GATED, false, 1><<<grid, NT, 0, s>>>(a);
-  } else {
-    moe_hidden_kernel<MX, GATED, false, 2><<<grid, NT, 0, s>>>(a);
-  }
+  if (a.ntk == 1) moe_hidden_kernel<MX, GATED, 1><<<grid, NT, 0, s>>>(a);
+  else moe_hidden_kernel<MX, GATED, 2><<<grid, NT, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -635,14 +673,19 @@ void moe_plan(bool mx, MoeArgs* a) {
   int nb = mx ? kSlice<true> : kSlice<false>;
   while (nb > least && (int64_t)a->Y * ((a->F + nb - 1) / nb) < 1024) nb /= 2;
   a->nb = nb;
+  // two blocks of 16 tokens a pass where the experts have more than that
+  a->ntk = pairs <= 12 * a->E ? 1 : 2;
   const int cols = 16 * (mx ? kCpl<true> : kCpl<false>);
   a->chunks = (a->d + cols - 1) / cols;
 }
 
 hipError_t launch_moe(bool mx, const MoeArgs& a, hipStream_t s) {
-  const unsigned eb = (a.E + kWaves - 1) / kWaves;
-  if (a.T < 4) moe_logits_kernel<1><<<dim3(eb, a.T), NT, 0, s>>>(a);
-  else moe_logits_kernel<4><<<dim3(eb, (a.T + 3) / 4), NT, 0, s>>>(a);
+  if ((int64_t)a.E * a.d <= kRouteOne) {
+    moe_route_kernel<true><<<a.T, kRouteWaves * 64, 0, s>>>(a);
+  } else {
+    moe_logits_kernel<<<dim3((a.E + kWaves - 1) / kWaves, a.T), NT, 0, s>>>(a);
+    moe_route_kernel<false><<<a.T, kRouteWaves * 64, 0, s>>>(a);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const bool gated = a.wu != nullptr;

@@ -28,12 +28,11 @@ struct MoeArgs {
   int Y;
   int nb;                    // neurons a workgroup of the hidden kernel
   int chunks;                // column chunks of the down kernel
+  int ntk;                   // blocks of 16 tokens a pass of the hidden kernel
   // workspace
   long long* keys;           // [T, E] the logits as ordered integers
-  long long* chosen;         // [T, k] the selected experts' keys, by rank
-  int32_t* cnt;              // [Y] tokens of the unit
-  int32_t* expert;           // [Y]
-  int32_t* list;             // [Y, T] its (token, rank) pairs
+  int32_t* expert;           // [T k] the experts of each token by rank
+  float* weight;             // [T k] their softmax weights
   uint8_t* on;               // [Y, F] neuron active for one of its tokens
   float* h;                  // [T k, F] hidden activations of each pair
   float* part;               // [T k, d] output of each pair
@@ -42,7 +41,7 @@ struct MoeArgs {
   float* probs;              // [T, k] (nullable)
 };
 
-// fills Y, nb and chunks from the sizes
+// fills Y .. ntk from the sizes
 void moe_plan(bool mx, MoeArgs* a);
 hipError_t launch_moe(bool mx, const MoeArgs& a, hipStream_t s);
 

@@ -57,131 +57,106 @@ __device__ __forceinline__ double key_value(long long k) {
 
 // ---------------------------------------------------------------- router
 
-// The logits are summed in 64 bits: two experts' then compare as their exact
-// values do (the product of two bf16 values has 16 bits), whatever the order
-// of summation.
-constexpr int kRouteWaves = 16;
-constexpr int64_t kRouteOne = 1 << 18;   // most elements of a router that one workgroup reads
-
-// EE experts' logits of a token (the same in every lane)
-template <int EE>
-__device__ __forceinline__ void logits(const MoeArgs& a, const uint16_t* x, const uint16_t* w,
-                                       const int (&e)[EE], int lane, double (&s)[EE]) {
-#pragma unroll
-  for (int i = 0; i < EE; ++i) s[i] = 0.0;
-#pragma unroll 4
-  for (int c = lane * 8; c < a.d; c += 512) {
-    const u32x4_t xr = *(const u32x4_t*)(x + c);
-    u32x4_t wr[EE];
-#pragma unroll
-    for (int i = 0; i < EE; ++i) wr[i] = *(const u32x4_t*)(w + (int64_t)e[i] * a.d + c);
-    float xv[8];
-    Vec<uint16_t, 8>::cvt(xr, xv);
-#pragma unroll
-    for (int i = 0; i < EE; ++i) {
-      float wv[8];
-      Vec<uint16_t, 8>::cvt(wr[i], wv);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[i] = fma((double)wv[j], (double)xv[j], s[i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < EE; ++i)
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) s[i] += __shfl_xor(s[i], o);
-}
-
-// A wave an expert and token, for routers that one workgroup a token would
-// read too slowly.
+// The logits, a wave an expert and token. They are summed in 64 bits: two
+// experts' then compare as their exact values do (the product of two bf16
+// values has 16 bits), whatever the order of summation.
 __global__ __launch_bounds__(NT) void moe_logits_kernel(MoeArgs a) {
   const int lane = threadIdx.x & 63;
   const int e = blockIdx.x * kWaves + wave_id();
   const int t = blockIdx.y;
   if (e >= a.E || t >= tokens(a)) return;
-  const int es[1] = {e};
-  double s[1];
-  logits<1>(a, a.x + (int64_t)t * a.d, a.router, es, lane, s);
-  if (lane == 0) a.keys[(int64_t)t * a.E + e] = order_key(s[0]);
+  const uint16_t* x = a.x + (int64_t)t * a.d;
+  const uint16_t* w = a.router + (int64_t)e * a.d;
+  double s = 0.0;
+#pragma unroll 4
+  for (int c = lane * 8; c < a.d; c += 512) {
+    float wv[8], xv[8];
+    Vec<uint16_t, 8>::cvt(*(const u32x4_t*)(w + c), wv);
+    Vec<uint16_t, 8>::cvt(*(const u32x4_t*)(x + c), xv);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = fma((double)wv[j], (double)xv[j], s);
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
+  if (lane == 0) a.keys[(int64_t)t * a.E + e] = order_key(s);
 }
 
-// A workgroup a token: its logits (or the keys of moe_logits_kernel), every
-// expert's rank (the number of experts before it), and by rank the k
-// experts and their weights.
-template <bool LOGITS>
-__global__ __launch_bounds__(kRouteWaves * 64) void moe_route_kernel(MoeArgs a) {
-  __shared__ long long keys[kMoeMaxE];
-  __shared__ int before[kMoeMaxE];
-  __shared__ long long top;
-  __shared__ float ex[kMoeMaxK];
-  __shared__ float wsum[kRouteWaves];
-  constexpr int N = kRouteWaves * 64;
+// A token's k experts and their weights by rank (an expert's rank is the
+// number of experts before it), from the keys in memory. Called by all N
+// threads of a workgroup; ends with a barrier.
+struct Route {
+  long long keys[kMoeMaxE];
+  int before[kMoeMaxE];
+  long long top;
+  float wsum[16];
+  int expert[kMoeMaxK];
+  float p[kMoeMaxK];
+};
+template <int N>
+__device__ __forceinline__ void route(const MoeArgs& a, int t, Route& r) {
   const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int wave = wave_id();
-  const int t = blockIdx.x;
-  if (t >= tokens(a)) return;
-  if (LOGITS) {
-    // four experts of a wave at a time, so that their loads are in flight together
-    for (int e0 = wave * 4; e0 < a.E; e0 += kRouteWaves * 4) {
-      int es[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) es[i] = min(e0 + i, a.E - 1);
-      double s[4];
-      logits<4>(a, a.x + (int64_t)t * a.d, a.router, es, lane, s);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lane == 0 && e0 + i < a.E) keys[e0 + i] = order_key(s[i]);
-    }
-  } else {
-    for (int e = tid; e < a.E; e += N) keys[e] = a.keys[(int64_t)t * a.E + e];
+  for (int e = tid; e < a.E; e += N) {
+    r.keys[e] = a.keys[(int64_t)t * a.E + e];
+    r.before[e] = 0;
   }
-  for (int e = tid; e < a.E; e += N) before[e] = 0;
   __syncthreads();
   // the comparisons shared out over all threads
   const int parts = max(N / a.E, 1);
   for (int i = tid; i < a.E * parts; i += N) {
     const int e = i % a.E;
-    const long long mine = keys[e];
+    const long long mine = r.keys[e];
     int n = 0;
     for (int o = i / a.E; o < a.E; o += parts) {
-      const long long other = keys[o];
+      const long long other = r.keys[o];
       n += other > mine || (other == mine && o < e);
     }
-    if (n) atomicAdd(&before[e], n);   // whole numbers: any order
+    if (n) atomicAdd(&r.before[e], n);   // whole numbers: any order
   }
   __syncthreads();
-  // exponentials below that of the largest logit
-  for (int e = tid; e < a.E; e += N)
-    if (before[e] == 0) top = keys[e];
-  __syncthreads();
-  const double l0 = key_value(top);
-  float sum = 0.0f;
   for (int e = tid; e < a.E; e += N) {
-    const int r = before[e];
-    if (r < a.k || !a.normalize) {
-      const float v = expf((float)(key_value(keys[e]) - l0));
-      if (!a.normalize) sum += v;
-      if (r < a.k) {
-        ex[r] = v;
-        a.expert[t * a.k + r] = e;
-        if (a.ids) a.ids[t * a.k + r] = e;
-      }
-    }
+    const int rank = r.before[e];
+    if (rank == 0) r.top = r.keys[e];
+    if (rank < a.k) r.expert[rank] = e;
+  }
+  __syncthreads();
+  // exponentials below that of the largest logit; softmax over the k
+  // experts or over all
+  const double l0 = key_value(r.top);
+  float sum = 0.0f;
+  for (int i = tid; i < (a.normalize ? a.k : a.E); i += N) {
+    const int e = a.normalize ? r.expert[i] : i;
+    sum += expf((float)(key_value(r.keys[e]) - l0));
   }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
-  if (lane == 0) wsum[wave] = sum;
+  if ((tid & 63) == 0) r.wsum[tid >> 6] = sum;
   __syncthreads();
   if (tid < a.k) {
     float total = 0.0f;
-    if (a.normalize) {
-      for (int r = 0; r < a.k; ++r) total += ex[r];
-    } else {
-      for (int w = 0; w < kRouteWaves; ++w) total += wsum[w];
-    }
-    const float p = ex[tid] / total;
-    a.weight[t * a.k + tid] = p;
-    if (a.probs) a.probs[t * a.k + tid] = p;
+#pragma unroll
+    for (int w = 0; w < N / 64; ++w) total += r.wsum[w];
+    r.p[tid] = expf((float)(key_value(r.keys[r.expert[tid]]) - l0)) / total;
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ void give_routing(const MoeArgs& a, int t, const Route& r) {
+  const int i = t * a.k + threadIdx.x;
+  if (threadIdx.x < a.k) {
+    if (a.ids) a.ids[i] = r.expert[threadIdx.x];
+    if (a.probs) a.probs[i] = r.p[threadIdx.x];
+  }
+}
+
+// A workgroup a token.
+__global__ __launch_bounds__(NT) void moe_route_kernel(MoeArgs a) {
+  __shared__ Route r;
+  const int t = blockIdx.x;
+  if (t >= tokens(a)) return;
+  route<NT>(a, t, r);
+  give_routing(a, t, r);
+  if (threadIdx.x < a.k) {
+    a.expert[t * a.k + threadIdx.x] = r.expert[threadIdx.x];
+    a.weight[t * a.k + threadIdx.x] = r.p[threadIdx.x];
   }
 }
 
@@ -348,7 +323,7 @@ __device__ __forceinline__ int unit_pairs(const MoeArgs& a, int unit, Lists& ls,
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
   const int np = tokens(a) * a.k;
-  const bool pairs = a.Y != a.E;
+  const bool pairs = a.by_pair;
   if (pairs && unit >= np) return 0;
   const int e = pairs ? a.expert[unit] : unit;
   *expert = e;
@@ -451,20 +426,97 @@ __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, cons
   }
 }
 
-template <bool MX, bool GATED, int NTK>
+// The routing of a single token, for at most kOneE experts: lane l has the
+// keys of experts l and 64 + l, each wave compares them with its share of the
+// experts, and the shares are added. Returns the expert of rank `rank`;
+// `give`: hand the routing on. Called by all threads; holds a barrier.
+constexpr int kOneE = 128;
+__device__ __forceinline__ int route_one(const MoeArgs& a, int rank, bool give,
+                                         int (&share)[kWaves][kOneE]) {
+  const int lane = threadIdx.x & 63;
+  const int wave = wave_id();
+  long long key[2];
+  int before[2] = {};
+  // (below every logit's key, infinities included)
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    key[i] = 64 * i + lane < a.E ? a.keys[64 * i + lane] : (long long)0x8000000000000000ull;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int m = min(a.E - 64 * i, 64);
+    for (int o = wave; o < m; o += kWaves) {
+      const uint32_t lo = __builtin_amdgcn_readlane((int)key[i], o);
+      const uint32_t hi = __builtin_amdgcn_readlane((int)(key[i] >> 32), o);
+      const long long other = (long long)((uint64_t)hi << 32 | lo);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        before[j] += other > key[j] || (other == key[j] && 64 * i + o < 64 * j + lane);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) share[wave][64 * j + lane] = before[j];
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    before[j] = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) before[j] += share[w][64 * j + lane];
+  }
+  int e = 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint64_t b = __ballot(before[j] == rank && 64 * j + lane < a.E);
+    if (b) e = 64 * j + __ffsll((unsigned long long)b) - 1;
+  }
+  if (give && wave == 0) {
+    long long top = max(key[0], key[1]);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) top = max(top, __shfl_xor(top, o));
+    const double l0 = key_value(top);
+    float ex[2], sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const bool counts = 64 * j + lane < a.E && (before[j] < a.k || !a.normalize);
+      ex[j] = counts ? expf((float)(key_value(key[j]) - l0)) : 0.0f;
+      sum += ex[j];
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (64 * j + lane < a.E && before[j] < a.k) {
+        a.expert[before[j]] = 64 * j + lane;
+        a.weight[before[j]] = ex[j] / sum;
+        if (a.ids) a.ids[before[j]] = 64 * j + lane;
+        if (a.probs) a.probs[before[j]] = ex[j] / sum;
+      }
+  }
+  return __builtin_amdgcn_readfirstlane(e);
+}
+
+// ONE: a single token, whose routing every workgroup finds for itself.
+template <bool MX, bool GATED, bool ONE, int NTK>
 __global__ __launch_bounds__(NT, NTK == 1 ? 4 : 2) void moe_hidden_kernel(MoeArgs a) {
   __shared__ Lists ls;
   __shared__ uint8_t any[kSlice<MX>];
   __shared__ union {
+    int share[kWaves][kOneE];
     Shared<MX, 1> s1;
     Shared<MX, NTK> s;
   } sh;
   const int tid = threadIdx.x;
   const int slice = blockIdx.x, unit = blockIdx.y;
-  int e;
+  int e, n = 1;
   if (tid < kSlice<MX>) any[tid] = 0;
-  const int n = unit_pairs(a, unit, ls, &e);
-  if (n == 0) return;
+  if (ONE) {
+    if (tokens(a) == 0) return;
+    e = route_one(a, unit, slice == 0 && unit == 0, sh.share);
+    if (tid == 0) ls.pair[0] = unit;
+    __syncthreads();
+  } else {
+    n = unit_pairs(a, unit, ls, &e);
+    if (n == 0) return;
+  }
 
   const int j0 = slice * a.nb;
   const int nbe = min(a.nb, a.F - j0);
@@ -484,7 +536,8 @@ __global__ __launch_bounds__(NT, NTK == 1 ? 4 : 2) void moe_hidden_kernel(MoeArg
 
 // ---------------------------------------------------------------- down
 
-constexpr int kSeg = 8 * NT;    // neurons whose active ones are listed at a time
+constexpr int kFl = 4;           // times 8 flags a thread
+constexpr int kSeg = kFl * 8 * NT;   // neurons whose active ones are listed at a time (8192)
 
 // A lane loads CPL columns of 8 neurons (16 bytes of bf16, 8 of codes) and
 // turns them into CPL operands, one a column: operand q of lane l holds
@@ -494,40 +547,50 @@ template <bool MX>
 constexpr int kCpl = MX ? 16 : 8;
 
 template <bool MX>
-__global__ __launch_bounds__(NT, 3) void moe_down_kernel(MoeArgs a) {
+__global__ __launch_bounds__(NT, MX ? 2 : 3) void moe_down_kernel(MoeArgs a) {
   constexpr int CPL = kCpl<MX>, COLS = 16 * CPL;
   __shared__ uint16_t act[kSeg];
   __shared__ int wsum[kWaves];
-  __shared__ f32x4_t red[kWaves][CPL][64];
+  __shared__ f32x4_t red[kWaves / 2][CPL][64];
   __shared__ Lists ls;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = wave_id();
   const int kq = lane >> 4, l15 = lane & 15;
   const int chunk = blockIdx.x, unit = blockIdx.y;
+  const uint8_t* on = a.on + (int64_t)unit * a.F;
+  // the active flags of the neurons from s0 on, 8 x kFl a thread (F is a
+  // multiple of 32)
+  uint64_t fl[kFl];
+  auto flags = [&](int s0) {
+    const int f0 = s0 + tid * (8 * kFl);
+#pragma unroll
+    for (int v = 0; v < kFl; ++v) fl[v] = f0 < a.F ? *(const uint64_t*)(on + f0 + 8 * v) : 0;
+  };
+  flags(0);   // (a unit without tokens has none that mean anything)
   int e;
   const int n = unit_pairs(a, unit, ls, &e);
   if (n == 0) return;
-  const int c0 = chunk * COLS;
-  const int ncol = min(COLS, a.d - c0);            // (the last chunk of codes may be half)
-  const int col = c0 + min(CPL * l15, ncol - CPL);
+  const int ncol = min(COLS, a.d - chunk * COLS);   // (the last chunk of codes may be half)
+  const int col = chunk * COLS + min(CPL * l15, ncol - CPL);
   const int64_t pitch = MX ? a.d / 2 : (int64_t)a.d * 2;
   const int64_t gp = (int64_t)a.E * a.F * 4;
   // a row's place as a 32-bit offset from an address that all lanes share
   const uint8_t* wp = (const uint8_t*)a.wd + (int64_t)e * a.F * pitch;
   const uint32_t cb = MX ? col / 2 : col * 2, rp = (uint32_t)pitch;
-  const uint8_t* sp = MX ? a.sd + (int64_t)e * a.F * 4 : nullptr;
-  const uint32_t so = (uint32_t)((col >> 7) * gp + ((col >> 5) & 3));
-  const uint8_t* on = a.on + (int64_t)unit * a.F;
+  // (its scales: one or two 128-column groups)
+  const uint8_t* sp = MX ? a.sd + (int64_t)e * a.F * 4 + (col >> 7) * gp + ((col >> 5) & 3) : nullptr;
 
   for (int p0 = 0; p0 < n; p0 += 16) {
     const int nt = min(n - p0, 16);
     f32x4_t acc[CPL] = {};
     for (int s0 = 0; s0 < a.F; s0 += kSeg) {
-      // list the segment's active neurons: 8 flags a thread
-      const int f0 = s0 + tid * 8;
-      uint64_t fl = f0 < a.F ? *(const uint64_t*)(on + f0) : 0;   // F is a multiple of 32
-      const int mine = __popcll(fl);
+      // list the segment's active neurons
+      if (s0 || p0) flags(s0);
+      const int f0 = s0 + tid * (8 * kFl);
+      int mine = 0;
+#pragma unroll
+      for (int v = 0; v < kFl; ++v) mine += __popcll(fl[v]);
       int pre = mine;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
@@ -544,8 +607,12 @@ __global__ __launch_bounds__(NT, 3) void moe_down_kernel(MoeArgs a) {
         na += wsum[w];
       }
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if ((fl >> (8 * q)) & 1) act[at++] = (uint16_t)(f0 + q);
+      for (int v = 0; v < kFl; ++v) {
+        if (!fl[v]) continue;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if ((fl[v] >> (8 * q)) & 1) act[at++] = (uint16_t)(f0 + 8 * v + q);
+      }
       __syncthreads();
       // 32 neurons a step, the steps shared out over the waves, the next
       // step's loads in flight
@@ -561,7 +628,7 @@ __global__ __launch_bounds__(NT, 3) void moe_down_kernel(MoeArgs a) {
           const uint32_t r = act[min(ks + kq * 8 + j, na - 1)];
           if constexpr (MX) {
             q[b][j] = *(const u32x2_t*)(wp + (r * rp + cb));
-            sb[b][j] = *(sp + (r * 4 + so));
+            sb[b][j] = sp[r * 4];
           } else {
             raw[b][j] = *(const u32x4_t*)(wp + (r * rp + cb));
           }
@@ -618,10 +685,19 @@ __global__ __launch_bounds__(NT, 3) void moe_down_kernel(MoeArgs a) {
         }
       }
     }
-    // the waves' sums; thread (token, part of the columns)
+    // the waves' sums: the upper half's through LDS into the lower half's,
+    // theirs through LDS into the result
 #pragma unroll
-    for (int q = 0; q < CPL; ++q) red[wave][q][lane] = acc[q];
-    __syncthreads();
+    for (int half = 1; half >= 0; --half) {
+      if (wave / (kWaves / 2) == half) {
+#pragma unroll
+        for (int q = 0; q < CPL; ++q) {
+          f32x4_t& m = red[wave % (kWaves / 2)][q][lane];
+          m = half ? acc[q] : acc[q] + m;
+        }
+      }
+      __syncthreads();
+    }
     for (int i = tid; i < CPL * 64; i += NT) {
       const int l = i & 63, q0 = (i >> 6) / 4 * 4, r = (i >> 6) % 4;
       // row r of operands q0 .. q0 + 3: four consecutive columns
@@ -631,9 +707,10 @@ __global__ __launch_bounds__(NT, 3) void moe_down_kernel(MoeArgs a) {
       for (int q = 0; q < 4; ++q) {
         s[q] = red[0][q0 + q][l][r];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) s[q] += red[w][q0 + q][l][r];
+        for (int w = 1; w < kWaves / 2; ++w) s[q] += red[w][q0 + q][l][r];
       }
-      if (tk < nt && c < ncol) *(f32x4_t*)(a.part + (int64_t)ls.pair[p0 + tk] * a.d + c0 + c) = s;
+      if (tk < nt && c < ncol)
+        *(f32x4_t*)(a.part + (int64_t)ls.pair[p0 + tk] * a.d + chunk * COLS + c) = s;
     }
     __syncthreads();
   }
@@ -658,8 +735,9 @@ __global__ __launch_bounds__(64) void moe_sum_kernel(MoeArgs a) {
 template <bool MX, bool GATED>
 hipError_t launch_hidden(const MoeArgs& a, hipStream_t s) {
   const dim3 grid((a.F + a.nb - 1) / a.nb, a.Y);
-  if (a.ntk == 1) moe_hidden_kernel<MX, GATED, 1><<<grid, NT, 0, s>>>(a);
-  else moe_hidden_kernel<MX, GATED, 2><<<grid, NT, 0, s>>>(a);
+  if (a.one) moe_hidden_kernel<MX, GATED, true, 1><<<grid, NT, 0, s>>>(a);
+  else if (a.ntk == 1) moe_hidden_kernel<MX, GATED, false, 1><<<grid, NT, 0, s>>>(a);
+  else moe_hidden_kernel<MX, GATED, false, 2><<<grid, NT, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -667,11 +745,14 @@ hipError_t launch_hidden(const MoeArgs& a, hipStream_t s) {
 
 void moe_plan(bool mx, MoeArgs* a) {
   const int pairs = a->T * a->k;
-  a->Y = pairs < a->E ? pairs : a->E;
-  // as many neurons a workgroup as leave four workgroups a CU
+  a->one = a->T == 1 && a->E <= kOneE;
+  a->by_pair = pairs < a->E || a->one;
+  a->Y = a->by_pair ? pairs : a->E;
+  // as many neurons a workgroup as leave eight workgroups a CU, two for the
+  // few experts of one token
   const int least = mx ? 32 : 16;
   int nb = mx ? kSlice<true> : kSlice<false>;
-  while (nb > least && (int64_t)a->Y * ((a->F + nb - 1) / nb) < 1024) nb /= 2;
+  while (nb > least && (int64_t)a->Y * ((a->F + nb - 1) / nb) < (a->T == 1 ? 512 : 2048)) nb /= 2;
   a->nb = nb;
   // two blocks of 16 tokens a pass where the experts have more than that
   a->ntk = pairs <= 12 * a->E ? 1 : 2;
@@ -680,12 +761,8 @@ void moe_plan(bool mx, MoeArgs* a) {
 }
 
 hipError_t launch_moe(bool mx, const MoeArgs& a, hipStream_t s) {
-  if ((int64_t)a.E * a.d <= kRouteOne) {
-    moe_route_kernel<true><<<a.T, kRouteWaves * 64, 0, s>>>(a);
-  } else {
-    moe_logits_kernel<<<dim3((a.E + kWaves - 1) / kWaves, a.T), NT, 0, s>>>(a);
-    moe_route_kernel<false><<<a.T, kRouteWaves * 64, 0, s>>>(a);
-  }
+  moe_logits_kernel<<<dim3((a.E + kWaves - 1) / kWaves, a.T), NT, 0, s>>>(a);
+  if (!a.one) moe_route_kernel<<<a.T, NT, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const bool gated = a.wu != nullptr;

@@ -26,6 +26,8 @@ struct MoeArgs {
   // experts, a pair (the pair of an expert's first token works for all of
   // the expert's tokens, the others have no tokens): Y of them.
   int Y;
+  int by_pair;
+  int one;                   // a single token, routed by the hidden kernel
   int nb;                    // neurons a workgroup of the hidden kernel
   int chunks;                // column chunks of the down kernel
   int ntk;                   // blocks of 16 tokens a pass of the hidden kernel

@@ -314,12 +314,15 @@ __device__ __forceinline__ uint64_t below(int lane) { return lane ? ~0ull >> (64
 
 // A unit's (token, rank) pairs in ascending order; returns their number. A
 // unit is an expert, or a pair, whose expert's pairs it has if it is the
-// first of them (else none). Called by all NT threads.
+// first of them (else none). *before: the pairs of the experts before it.
+// Called by all NT threads.
 struct Lists {
   int pair[kMoeMaxT];
   int wsum[kWaves];
+  int wless[kWaves];
 };
-__device__ __forceinline__ int unit_pairs(const MoeArgs& a, int unit, Lists& ls, int* expert) {
+__device__ __forceinline__ int unit_pairs(const MoeArgs& a, int unit, Lists& ls, int* expert,
+                                          int* before) {
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
   const int np = tokens(a) * a.k;
@@ -327,22 +330,28 @@ __device__ __forceinline__ int unit_pairs(const MoeArgs& a, int unit, Lists& ls,
   if (pairs && unit >= np) return 0;
   const int e = pairs ? a.expert[unit] : unit;
   *expert = e;
-  int n = 0;
+  int n = 0, less = 0;
   for (int i0 = 0; i0 < np; i0 += NT) {
     const int i = i0 + threadIdx.x;
-    const bool mine = i < np && a.expert[i] == e;
-    const uint64_t b = __ballot(mine);
+    const int f = i < np ? a.expert[i] : a.E;
+    const bool mine = f == e;
+    const uint64_t b = __ballot(mine), l = __ballot(f < e);
     if (i0) __syncthreads();
-    if (lane == 0) ls.wsum[wave] = __popcll(b);
+    if (lane == 0) {
+      ls.wsum[wave] = __popcll(b);
+      ls.wless[wave] = __popcll(l);
+    }
     __syncthreads();
     int at = n + __popcll(b & below(lane));
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       if (w < wave) at += ls.wsum[w];
       n += ls.wsum[w];
+      less += ls.wless[w];
     }
     if (mine) ls.pair[at] = i;
   }
+  *before = less;
   __syncthreads();
   if (pairs && n > 0 && ls.pair[0] != unit) n = 0;
   return n;
@@ -353,12 +362,13 @@ __device__ __forceinline__ int unit_pairs(const MoeArgs& a, int unit, Lists& ls,
 template <bool MX, bool GATED, int NTK>
 __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, const Lists& ls,
                                      const Rows& wg, const Rows& wu, int j0, int nbe, int n,
-                                     int p0, uint8_t* any) {
+                                     int p0, int place, uint8_t* any) {
   constexpr int MT = kBlocks<MX>;
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
   const int tid = threadIdx.x;
   const int nt = min(n - p0, 16 * NTK);   // tokens of this pass
+  const int P = a.T * a.k;
   uint32_t xo[NTK];
 #pragma unroll
   for (int i = 0; i < NTK; ++i)
@@ -380,11 +390,11 @@ __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, cons
         if (s[q] > 0.0f) sh.on[j + q] = any[j + q] = 1;   // every writer stores the same
       // non-gated: h is z itself; gated: a neuron that only another pass
       // finds active has h = 0 here
-      f32x4_t h = {};
+      if (!GATED || n > 16 * NTK || p0 > 0) {
+        float* o = a.h + (int64_t)(j0 + j) * P + place + p0 + tk;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) h[q] = !GATED && s[q] > 0.0f ? s[q] : 0.0f;
-      if (!GATED || n > 16 * NTK || p0 > 0)
-        *(f32x4_t*)(a.h + (int64_t)ls.pair[p0 + tk] * a.F + j0 + j) = h;
+        for (int q = 0; q < 4; ++q) o[q * P] = !GATED && s[q] > 0.0f ? s[q] : 0.0f;
+      }
     }
   }
   __syncthreads();
@@ -412,14 +422,14 @@ __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, cons
     const f32x4_t u = share_sum<MX, NTK>(sh, parts, block, t, l);
     const int tk = t * 16 + (l & 15);
     if (tk < nt) {
-      float* o = a.h + (int64_t)ls.pair[p0 + tk] * a.F + j0;
+      float* o = a.h + (int64_t)j0 * P + place + p0 + tk;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int i = block * 16 + 4 * (l >> 4) + q;
         if (i < na) {
           const int j = sh.act[i];
           const float z = sh.z[tk][j];
-          o[j] = z > 0.0f ? z * u[q] : 0.0f;
+          o[(int64_t)j * P] = z > 0.0f ? z * u[q] : 0.0f;
         }
       }
     }
@@ -429,10 +439,10 @@ __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, cons
 // The routing of a single token, for at most kOneE experts: lane l has the
 // keys of experts l and 64 + l, each wave compares them with its share of the
 // experts, and the shares are added. Returns the expert of rank `rank`;
-// `give`: hand the routing on. Called by all threads; holds a barrier.
+// *place: the chosen experts before it; `give`: hand the routing on. Called by all threads; holds a barrier.
 constexpr int kOneE = 128;
 __device__ __forceinline__ int route_one(const MoeArgs& a, int rank, bool give,
-                                         int (&share)[kWaves][kOneE]) {
+                                         int (&share)[kWaves][kOneE], int* place) {
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
   long long key[2];
@@ -468,6 +478,9 @@ __device__ __forceinline__ int route_one(const MoeArgs& a, int rank, bool give,
     const uint64_t b = __ballot(before[j] == rank && 64 * j + lane < a.E);
     if (b) e = 64 * j + __ffsll((unsigned long long)b) - 1;
   }
+  const uint64_t c0 = __ballot(before[0] < a.k && lane < a.E);
+  const uint64_t c1 = __ballot(before[1] < a.k && 64 + lane < a.E);
+  *place = __popcll(c0 & (e < 64 ? below(e) : ~0ull)) + __popcll(e < 64 ? 0ull : c1 & below(e - 64));
   if (give && wave == 0) {
     long long top = max(key[0], key[1]);
 #pragma unroll
@@ -506,15 +519,15 @@ __global__ __launch_bounds__(NT, NTK == 1 ? 4 : 2) void moe_hidden_kernel(MoeArg
   } sh;
   const int tid = threadIdx.x;
   const int slice = blockIdx.x, unit = blockIdx.y;
-  int e, n = 1;
+  int e, n = 1, place;
   if (tid < kSlice<MX>) any[tid] = 0;
   if (ONE) {
     if (tokens(a) == 0) return;
-    e = route_one(a, unit, slice == 0 && unit == 0, sh.share);
+    e = route_one(a, unit, slice == 0 && unit == 0, sh.share, &place);
     if (tid == 0) ls.pair[0] = unit;
     __syncthreads();
   } else {
-    n = unit_pairs(a, unit, ls, &e);
+    n = unit_pairs(a, unit, ls, &e, &place);
     if (n == 0) return;
   }
 
@@ -527,8 +540,8 @@ __global__ __launch_bounds__(NT, NTK == 1 ? 4 : 2) void moe_hidden_kernel(MoeArg
   const Rows wu = {GATED ? (const uint8_t*)a.wu + row0 * pitch : nullptr,
                    MX && GATED ? a.su + row0 * 4 : nullptr, pitch, gp};
   for (int p0 = 0; p0 < n; p0 += 16 * NTK) {
-    if (n - p0 <= 16) pass<MX, GATED, 1>(a, sh.s1, ls, wg, wu, j0, nbe, n, p0, any);
-    else pass<MX, GATED, NTK>(a, sh.s, ls, wg, wu, j0, nbe, n, p0, any);
+    if (n - p0 <= 16) pass<MX, GATED, 1>(a, sh.s1, ls, wg, wu, j0, nbe, n, p0, place, any);
+    else pass<MX, GATED, NTK>(a, sh.s, ls, wg, wu, j0, nbe, n, p0, place, any);
     __syncthreads();
   }
   if (tid < nbe) a.on[(int64_t)unit * a.F + j0 + tid] = any[tid];
@@ -568,8 +581,8 @@ __global__ __launch_bounds__(NT, MX ? 2 : 3) void moe_down_kernel(MoeArgs a) {
     for (int v = 0; v < kFl; ++v) fl[v] = f0 < a.F ? *(const uint64_t*)(on + f0 + 8 * v) : 0;
   };
   flags(0);   // (a unit without tokens has none that mean anything)
-  int e;
-  const int n = unit_pairs(a, unit, ls, &e);
+  int e, place;
+  const int n = unit_pairs(a, unit, ls, &e, &place);
   if (n == 0) return;
   const int ncol = min(COLS, a.d - chunk * COLS);   // (the last chunk of codes may be half)
   const int col = chunk * COLS + min(CPL * l15, ncol - CPL);
@@ -616,7 +629,7 @@ __global__ __launch_bounds__(NT, MX ? 2 : 3) void moe_down_kernel(MoeArgs a) {
       __syncthreads();
       // 32 neurons a step, the steps shared out over the waves, the next
       // step's loads in flight
-      const uint32_t ho = (uint32_t)ls.pair[p0 + min(l15, nt - 1)] * (uint32_t)a.F * 4;
+      const uint32_t ho = (uint32_t)(place + p0 + min(l15, nt - 1)) * 4, hp4 = (uint32_t)(a.T * a.k) * 4;
       u32x2_t q[2][8];
       uint32_t sb[2][8];
       u32x4_t raw[2][8];
@@ -632,7 +645,7 @@ __global__ __launch_bounds__(NT, MX ? 2 : 3) void moe_down_kernel(MoeArgs a) {
           } else {
             raw[b][j] = *(const u32x4_t*)(wp + (r * rp + cb));
           }
-          hv[b][j] = *(const float*)((const uint8_t*)a.h + (r * 4 + ho));
+          hv[b][j] = *(const float*)((const uint8_t*)a.h + (r * hp4 + ho));
         }
       };
       auto step = [&](auto bb, int ks) {

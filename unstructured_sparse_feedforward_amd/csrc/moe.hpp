@@ -36,7 +36,8 @@ struct MoeArgs {
   int32_t* expert;           // [T k] the experts of each token by rank
   float* weight;             // [T k] their softmax weights
   uint8_t* on;               // [Y, F] neuron active for one of its tokens
-  float* h;                  // [T k, F] hidden activations of each pair
+  float* h;                  // [F, T k] hidden activations, the pairs in the order of their
+                             // experts: those of a unit's tokens side by side
   float* part;               // [T k, d] output of each pair
   float* y;                  // [T, d]
   int32_t* ids;              // [T, k] (nullable)

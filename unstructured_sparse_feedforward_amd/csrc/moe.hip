@@ -60,11 +60,8 @@ __device__ __forceinline__ double key_value(long long k) {
 // The logits, a wave an expert and token. They are summed in 64 bits: two
 // experts' then compare as their exact values do (the product of two bf16
 // values has 16 bits), whatever the order of summation.
-__global__ __launch_bounds__(NT) void moe_logits_kernel(MoeArgs a) {
+__device__ __forceinline__ double logit(const MoeArgs& a, int t, int e) {
   const int lane = threadIdx.x & 63;
-  const int e = blockIdx.x * kWaves + wave_id();
-  const int t = blockIdx.y;
-  if (e >= a.E || t >= tokens(a)) return;
   const uint16_t* x = a.x + (int64_t)t * a.d;
   const uint16_t* w = a.router + (int64_t)e * a.d;
   double s = 0.0;
@@ -78,12 +75,19 @@ __global__ __launch_bounds__(NT) void moe_logits_kernel(MoeArgs a) {
   }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
-  if (lane == 0) a.keys[(int64_t)t * a.E + e] = order_key(s);
+  return s;
+}
+__global__ __launch_bounds__(NT) void moe_logits_kernel(MoeArgs a) {
+  const int e = blockIdx.x * kWaves + wave_id();
+  const int t = blockIdx.y;
+  if (e >= a.E || t >= tokens(a)) return;
+  const double s = logit(a, t, e);
+  if ((threadIdx.x & 63) == 0) a.keys[(int64_t)t * a.E + e] = order_key(s);
 }
 
 // A token's k experts and their weights by rank (an expert's rank is the
-// number of experts before it), from the keys in memory. Called by all N
-// threads of a workgroup; ends with a barrier.
+// number of experts before it), from r.keys. Called by all N threads of a
+// workgroup; begins and ends with a barrier.
 struct Route {
   long long keys[kMoeMaxE];
   int before[kMoeMaxE];
@@ -93,12 +97,9 @@ struct Route {
   float p[kMoeMaxK];
 };
 template <int N>
-__device__ __forceinline__ void route(const MoeArgs& a, int t, Route& r) {
+__device__ __forceinline__ void route(const MoeArgs& a, Route& r) {
   const int tid = threadIdx.x;
-  for (int e = tid; e < a.E; e += N) {
-    r.keys[e] = a.keys[(int64_t)t * a.E + e];
-    r.before[e] = 0;
-  }
+  for (int e = tid; e < a.E; e += N) r.before[e] = 0;
   __syncthreads();
   // the comparisons shared out over all threads
   const int parts = max(N / a.E, 1);
@@ -139,24 +140,33 @@ __device__ __forceinline__ void route(const MoeArgs& a, int t, Route& r) {
   }
   __syncthreads();
 }
-__device__ __forceinline__ void give_routing(const MoeArgs& a, int t, const Route& r) {
-  const int i = t * a.k + threadIdx.x;
-  if (threadIdx.x < a.k) {
-    if (a.ids) a.ids[i] = r.expert[threadIdx.x];
-    if (a.probs) a.probs[i] = r.p[threadIdx.x];
-  }
-}
+// A workgroup a token. LOGITS: it computes them itself, for as many experts
+// as it has waves; with more, their 64-bit sums would keep the one CU busy
+// (64 experts, d = 2048: 8.3 us, in a kernel of their own over all CUs 3.0
+// and 3.5 here).
+constexpr int kFusedE = 16;
 
-// A workgroup a token.
-__global__ __launch_bounds__(NT) void moe_route_kernel(MoeArgs a) {
+template <bool LOGITS, int N>
+__global__ __launch_bounds__(N) void moe_route_kernel(MoeArgs a) {
   __shared__ Route r;
-  const int t = blockIdx.x;
+  const int t = blockIdx.x, tid = threadIdx.x;
   if (t >= tokens(a)) return;
-  route<NT>(a, t, r);
-  give_routing(a, t, r);
-  if (threadIdx.x < a.k) {
-    a.expert[t * a.k + threadIdx.x] = r.expert[threadIdx.x];
-    a.weight[t * a.k + threadIdx.x] = r.p[threadIdx.x];
+  if (LOGITS) {
+    const int e = wave_id();
+    if (e < a.E) {
+      const double s = logit(a, t, e);
+      if ((tid & 63) == 0) r.keys[e] = order_key(s);
+    }
+  } else {
+    for (int e = tid; e < a.E; e += N) r.keys[e] = a.keys[(int64_t)t * a.E + e];
+  }
+  route<N>(a, r);
+  if (tid < a.k) {
+    const int i = t * a.k + tid;
+    a.expert[i] = r.expert[tid];
+    a.weight[i] = r.p[tid];
+    if (a.ids) a.ids[i] = r.expert[tid];
+    if (a.probs) a.probs[i] = r.p[tid];
   }
 }
 
@@ -774,8 +784,12 @@ void moe_plan(bool mx, MoeArgs* a) {
 }
 
 hipError_t launch_moe(bool mx, const MoeArgs& a, hipStream_t s) {
-  moe_logits_kernel<<<dim3((a.E + kWaves - 1) / kWaves, a.T), NT, 0, s>>>(a);
-  if (!a.one) moe_route_kernel<<<a.T, NT, 0, s>>>(a);
+  if (!a.one && a.E <= kFusedE) {
+    moe_route_kernel<true, kFusedE * 64><<<a.T, kFusedE * 64, 0, s>>>(a);
+  } else {
+    moe_logits_kernel<<<dim3((a.E + kWaves - 1) / kWaves, a.T), NT, 0, s>>>(a);
+    if (!a.one) moe_route_kernel<false, NT><<<a.T, NT, 0, s>>>(a);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const bool gated = a.wu != nullptr;

@@ -23,19 +23,6 @@ namespace {
 constexpr int NT = 256;
 constexpr int kWaves = NT / 64;
 
-// Compile-time loop: f(Int<0>), .., f(Int<N - 1>).
-template <int V>
-struct Int {
-  static constexpr int value = V;
-};
-template <int N, int K = 0, typename F>
-__device__ __forceinline__ void unroll(F&& f) {
-  if constexpr (K < N) {
-    f(Int<K>{});
-    unroll<N, K + 1>(f);
-  }
-}
-
 // the wave's index, known to be the same in all its lanes
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
@@ -198,70 +185,111 @@ __device__ __forceinline__ f32x4_t mfma(const u32x4_t& w, const u32x4_t& v, cons
 
 // ---------------------------------------------------------------- products with x
 
-// acc[i][n] += rows r[i] (16 of them, one a lane's row) . x of 16 tokens
-// (xo[n]: the offset of a lane's token), over steps part, part + parts, .. of
-// d. The instruction's k order is free as long as both operands agree: lane l
-// takes 16 contiguous bytes of row l % 16, so that the four lanes of a row
-// cover 64 bytes: 32 bf16 values, the instruction's own order, or 128 codes,
-// four instructions' worth. D steps' loads are always in flight: a step's
-// registers are loaded again as soon as it is multiplied. Addresses are 32-bit
-// offsets from one that all lanes share: a register a row, no arithmetic.
-template <bool MX, int MT, int NTK>
-__device__ __forceinline__ void dots(const MoeArgs& a, const Rows& w, const int (&r)[MT],
-                                     const uint32_t (&xo)[NTK], int lane, int part, int parts,
-                                     f32x4_t (&acc)[MT][NTK]) {
-  const int kq = lane >> 4;
-  constexpr int D = MX ? 2 : 4, NF = MX ? 4 : 2;   // MFMAs a step and block
-  constexpr int SC = MX ? 128 : 64;                // columns a step
-  uint32_t po[MT], so[MT], xp[NTK];
+// acc[i][n] += rows 16 i .. of row() . x of 16 tokens (xo[n]: the offset of
+// a lane's token), over steps part, part + parts, .. of d: 64 columns of bf16,
+// 128 of codes.
+//
+// The rows go through a ring of D slots in LDS of the wave's own (no barrier:
+// the wave waits for its own oldest copies): a copy instruction covers whole
+// 64- or 128-byte pieces of rows, while loads straight into the matrix
+// instruction's lanes, in which neighbours hold different rows, take an access
+// each; 64 experts of 2048 x 1408 in 4 bits then kept the address units busy
+// for 25 of 27 us. A slot holds 16 rows (two blocks of codes one after the
+// other), 16-byte piece c of row r at position c ^ (r / 2) % 8 of 8 (codes: c ^
+// (r / 4) % 4 of 4), so that 16 lanes reading one piece of 16 rows meet
+// different banks. The instruction's k order is free as long as both operands
+// agree: lane l reads piece l / 16 of a row's four of 64 bytes, which are 32
+// bf16 values, the instruction's own order, or 128 codes, four instructions'
+// worth.
+template <bool MX>
+constexpr int kRing = MX ? 4 : 5;    // slots
+constexpr int kSlot = 2048;          // bytes
+
+template <bool MX, int MT, int NTK, typename F>
+__device__ __forceinline__ void dots(const MoeArgs& a, const Rows& w, F&& row,
+                                     const uint32_t (&xo)[NTK], char* ring, int lane, int part,
+                                     int parts, f32x4_t (&acc)[MT][NTK]) {
+  static_assert(MT == (MX ? 2 : 1), "a slot holds two copies");
+  constexpr int D = kRing<MX>, NF = MX ? 4 : 2;    // MFMAs a step and block
+  constexpr int SC = MX ? 128 : 64, SB = MX ? 64 : 128;   // columns and row bytes a step
+  constexpr int OPS = 2 + (MX ? MT : 0) + NTK * NF;       // loads a step
+  const int kq = lane >> 4, l15 = lane & 15;
+  // 32-bit offsets from an address that all lanes share
+  uint32_t po[2], so[MT], xp[NTK];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    po[i] = (uint32_t)r[i] * (uint32_t)w.pitch + kq * 16;
-    so[i] = (uint32_t)r[i] * 4 + kq;
+  for (int i = 0; i < 2; ++i) {
+    const int r = MX ? lane >> 2 : 8 * i + (lane >> 3);
+    const int c = MX ? (lane & 3) ^ ((r >> 2) & 3) : (lane & 7) ^ ((r >> 1) & 7);
+    po[i] = (uint32_t)row(MX ? 16 * i + r : r) * (uint32_t)w.pitch + c * 16;
+  }
+  if (MX) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) so[i] = (uint32_t)row(16 * i + l15) * 4 + kq;
   }
 #pragma unroll
   for (int n = 0; n < NTK; ++n) xp[n] = xo[n] + kq * (MX ? 64 : 16);
   const uint8_t* xb = (const uint8_t*)a.x;
-  u32x4_t q[D][MT][MX ? 1 : 2], xv[D][NTK][NF];
+  u32x4_t xv[D][NTK][NF];
   uint32_t sb[D][MT];
-  auto load = [&](auto ss, int g) {
+  auto load = [&](auto ss, int i) {
     constexpr int s = decltype(ss)::value;
+    const int64_t g = part + i * parts;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if constexpr (MX) {
-        q[s][i][0] = *(const u32x4_t*)(w.p + (int64_t)g * 64 + po[i]);
-        sb[s][i] = *(w.sc + g * w.gpitch + so[i]);
-      } else {
-        q[s][i][0] = *(const u32x4_t*)(w.p + (int64_t)g * 128 + po[i]);
-        q[s][i][1] = *(const u32x4_t*)(w.p + (int64_t)g * 128 + 64 + po[i]);
-      }
+    for (int c = 0; c < 2; ++c) copy16(w.p + g * SB, po[c], ring + s * kSlot + c * 1024);
+    if constexpr (MX) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) sb[s][m] = *(w.sc + g * w.gpitch + so[m]);
     }
 #pragma unroll
     for (int n = 0; n < NTK; ++n)
 #pragma unroll
       for (int f = 0; f < NF; ++f)
-        xv[s][n][f] = *(const u32x4_t*)(xb + (int64_t)g * (SC * 2) + f * (MX ? 16 : 64) + xp[n]);
+        xv[s][n][f] = *(const u32x4_t*)(xb + g * (SC * 2) + f * (MX ? 16 : 64) + xp[n]);
+  };
+  u32x4_t q[2];
+  auto read = [&](auto ss) {
+    const char* p = ring + decltype(ss)::value * kSlot;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      q[c] = *(const u32x4_t*)(MX ? p + c * 1024 + l15 * 64 + ((kq ^ ((l15 >> 2) & 3)) << 4)
+                                  : p + l15 * 128 + (((c * 4 + kq) ^ ((l15 >> 1) & 7)) << 4));
+    wait_point<wait_imm(63, 0)>();     // read before the slot is written again
+  };
+  auto multiply = [&](auto ss) {
+    constexpr int s = decltype(ss)::value;
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const u32x4_t wv = MX ? from_codes(q[m][f & 3], sb[s][m]) : q[f & 1];
+#pragma unroll
+        for (int n = 0; n < NTK; ++n) acc[m][n] = mfma(wv, xv[s][n][f], acc[m][n]);
+      }
   };
   const int G = a.d / SC;
+  const int n = G > part ? (G - part + parts - 1) / parts : 0;   // the wave's steps
   unroll<D>([&](auto s) {
-    if (part + decltype(s)::value * parts < G) load(s, part + decltype(s)::value * parts);
+    if (decltype(s)::value < n) load(s, decltype(s)::value);
   });
-  for (int g0 = part; g0 < G; g0 += D * parts) {
-    unroll<D>([&](auto ss) {
-      constexpr int s = decltype(ss)::value;
-      const int g = g0 + s * parts;
-      if (g >= G) return;
-#pragma unroll
-      for (int f = 0; f < NF; ++f)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const u32x4_t wv = MX ? from_codes(q[s][i][0][f], sb[s][i]) : q[s][i][MX ? 0 : f];
-#pragma unroll
-          for (int n = 0; n < NTK; ++n) acc[i][n] = mfma(wv, xv[s][n][f], acc[i][n]);
-        }
-      if (g + D * parts < G) load(ss, g + D * parts);
+  int i0 = 0;
+  // D steps in flight: the oldest has landed when the loads of D - 1 are left
+  for (; i0 + 2 * D <= n; i0 += D)
+    unroll<D>([&](auto s) {
+      wait_point<wait_imm((D - 1) * OPS, 15)>();
+      read(s);
+      multiply(s);
+      load(s, i0 + decltype(s)::value + D);
     });
-  }
+  for (; i0 < n; i0 += D)
+    unroll<D>([&](auto s) {
+      const int i = i0 + decltype(s)::value;
+      if (i >= n) return;
+      if (i + D <= n) wait_point<wait_imm((D - 1) * OPS, 15)>();
+      else wait_point<wait_imm(0, 15)>();
+      read(s);
+      multiply(s);
+      if (i + D < n) load(s, i + D);
+    });
 }
 
 // ---------------------------------------------------------------- hidden
@@ -278,6 +306,7 @@ constexpr int kSlice = kWaves * 16 * kBlocks<MX>;
 template <bool MX, int NTK>
 struct Shared {
   static constexpr int MT = kBlocks<MX>, SL = kSlice<MX>;
+  __align__(16) char ring[kWaves * kRing<MX> * kSlot];
   f32x4_t red[kWaves][MT][NTK][64];    // the waves' shares of a product with x
   float z[16 * NTK][SL + 4];           // gate pre-activations (padded rows)
   int act[SL];                         // active neurons of the slice, ascending
@@ -299,10 +328,8 @@ __device__ __forceinline__ int share_products(const MoeArgs& a, Shared<MX, NTK>&
   const int parts = kWaves >> lg, tile = wave >> (2 - lg), part = wave & (parts - 1);
   if (tile < tiles) {
     f32x4_t acc[MT][NTK] = {};
-    int r[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) r[i] = row((tile * MT + i) * 16 + (lane & 15));
-    dots<MX, MT, NTK>(a, w, r, xo, lane, part, parts, acc);
+    dots<MX, MT, NTK>(a, w, [&](int i) { return row(tile * MT * 16 + i); }, xo,
+                      sh.ring + wave * (kRing<MX> * kSlot), lane, part, parts, acc);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll

@@ -1,5 +1,6 @@
 // MXFP4 matrices, shared by the quantiser (mx.hip), the product
-// (mx_gemm.hip) and the expert layer (moe.hip).
+// (mx_gemm.hip) and the expert layer (moe.hip), and the copies into LDS of
+// the last two.
 //
 // A matrix [R, K] (blocks of 32 along K) is kept as
 //   codes  [R, Kp / 2] bytes, Kp = K rounded up to 128: element k of a row
@@ -17,6 +18,55 @@
 namespace sffn {
 
 __host__ __device__ __forceinline__ int64_t mx_padded(int64_t K) { return (K + 127) / 128 * 128; }
+
+// ---------------------------------------------------------------- copies into LDS
+
+// s_waitcnt immediate (vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt
+// 11:8); a field at its maximum does not wait.
+constexpr int wait_imm(int vm, int lgkm) {
+  return (vm & 0xF) | ((vm >> 4) << 14) | (7 << 4) | (lgkm << 8);
+}
+
+// A wait that neither the compiler nor its scheduler moves memory accesses
+// across.
+template <int IMM>
+__device__ __forceinline__ void wait_point() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(IMM);
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// 16 (4) bytes a lane from base + voff into LDS at lds + 16 (4) x lane: a
+// buffer load over a raw resource of the whole 32-bit range. Every offset
+// formed here is inside the operand.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, -1, 0x00020000);
+}
+__device__ __forceinline__ void copy16(const uint8_t* base, uint32_t voff, char* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(base), (lds_void*)lds, 16, voff, 0, 0, 0);
+}
+__device__ __forceinline__ void copy4(const uint8_t* base, uint32_t voff, char* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(base), (lds_void*)lds, 4, voff, 0, 0, 0);
+}
+
+// Compile-time loop: f(Int<0>), .., f(Int<N - 1>).
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+template <int N, int K = 0, typename F>
+__device__ __forceinline__ void unroll(F&& f) {
+  if constexpr (K < N) {
+    f(Int<K>{});
+    unroll<N, K + 1>(f);
+  }
+}
+
+// ---------------------------------------------------------------- launchers
 
 hipError_t launch_mx_quantize(Dtype dt, const void* x, int64_t rows, int64_t cols, int64_t ldx,
                               bool transposed, uint8_t* codes, uint8_t* scales, hipStream_t s);

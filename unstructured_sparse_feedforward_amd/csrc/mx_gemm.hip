@@ -79,40 +79,6 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx_few_kernel(MxGemmArgs g) {
   }
 }
 
-// ---------------------------------------------------------------- copies into LDS
-
-// s_waitcnt immediate (vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt
-// 11:8); a field at its maximum does not wait.
-constexpr int wait_imm(int vm, int lgkm) {
-  return (vm & 0xF) | ((vm >> 4) << 14) | (7 << 4) | (lgkm << 8);
-}
-
-// A wait that neither the compiler nor its scheduler moves memory accesses
-// across.
-template <int IMM>
-__device__ __forceinline__ void wait_point() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(IMM);
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-}
-
-typedef __attribute__((address_space(3))) void lds_void;
-
-// 16 (4) bytes a lane from base + voff into LDS at lds + 16 (4) x lane: a
-// buffer load over a raw resource of the whole 32-bit range. Every offset
-// formed here is inside the operand.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* base) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, -1, 0x00020000);
-}
-__device__ __forceinline__ void copy16(const uint8_t* base, uint32_t voff, char* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(base), (lds_void*)lds, 16, voff, 0, 0, 0);
-}
-__device__ __forceinline__ void copy4(const uint8_t* base, uint32_t voff, char* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(base), (lds_void*)lds, 4, voff, 0, 0, 0);
-}
-
 // ---------------------------------------------------------------- small tiles
 
 // A (32 I) x 64 tile a workgroup, whose four waves share out K by 128-wide
@@ -268,19 +234,6 @@ struct Big {
   static constexpr int LDS = NSLOT * SLOT;
   static constexpr int WGS = LDS > 80 * 1024 ? 1 : 2;   // workgroups a CU
 };
-
-// Compile-time loop: f(Int<0>), .., f(Int<N - 1>).
-template <int V>
-struct Int {
-  static constexpr int value = V;
-};
-template <int N, int K = 0, typename F>
-__device__ __forceinline__ void unroll(F&& f) {
-  if constexpr (K < N) {
-    f(Int<K>{});
-    unroll<N, K + 1>(f);
-  }
-}
 
 // An accumulator at the point of use. 256 of them are in AGPRs: read there,
 // one by one, or the compiler moves (and converts) them all before the

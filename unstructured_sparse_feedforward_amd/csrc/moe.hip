@@ -268,18 +268,29 @@ __device__ __forceinline__ void dots(const MoeArgs& a, const Rows& w, F&& row,
   };
   const int G = a.d / SC;
   const int n = G > part ? (G - part + parts - 1) / parts : 0;   // the wave's steps
-  unroll<D>([&](auto s) {
-    if (decltype(s)::value < n) load(s, decltype(s)::value);
-  });
   int i0 = 0;
-  // D steps in flight: the oldest has landed when the loads of D - 1 are left
-  for (; i0 + 2 * D <= n; i0 += D)
+  if (n >= 2 * D) {
+    // D steps in flight: the oldest has landed when the loads of D - 1 are
+    // left. (The first loads are not conditional here: the compiler's own
+    // waits for x would otherwise drain every load in flight at the loop's
+    // back edge.)
     unroll<D>([&](auto s) {
-      wait_point<wait_imm((D - 1) * OPS, 15)>();
-      read(s);
-      multiply(s);
-      load(s, i0 + decltype(s)::value + D);
+      load(s, decltype(s)::value);
+      order_point();
     });
+    for (; i0 + 2 * D <= n; i0 += D)
+      unroll<D>([&](auto s) {
+        wait_point<wait_imm((D - 1) * OPS, 15)>();
+        read(s);
+        multiply(s);
+        load(s, i0 + decltype(s)::value + D);
+      });
+  } else {
+    unroll<D>([&](auto s) {
+      if (decltype(s)::value < n) load(s, decltype(s)::value);
+      order_point();   // the waits count the loads step by step
+    });
+  }
   for (; i0 < n; i0 += D)
     unroll<D>([&](auto s) {
       const int i = i0 + decltype(s)::value;
@@ -306,13 +317,16 @@ constexpr int kSlice = kWaves * 16 * kBlocks<MX>;
 template <bool MX, int NTK>
 struct Shared {
   static constexpr int MT = kBlocks<MX>, SL = kSlice<MX>;
-  __align__(16) char ring[kWaves * kRing<MX> * kSlot];
   f32x4_t red[kWaves][MT][NTK][64];    // the waves' shares of a product with x
   float z[16 * NTK][SL + 4];           // gate pre-activations (padded rows)
   int act[SL];                         // active neurons of the slice, ascending
   uint8_t on[SL];
   int na;
 };
+
+// The waves' rings. (Dynamic LDS: for reads of a static object the compiler
+// waits for every copy into LDS in flight.)
+extern __shared__ __align__(16) char rings[];
 
 // The products of tiles of 16 MT rows with the pass's tokens: the waves share
 // out the tiles, and d where the tiles are fewer than the waves. row(i) is
@@ -329,7 +343,7 @@ __device__ __forceinline__ int share_products(const MoeArgs& a, Shared<MX, NTK>&
   if (tile < tiles) {
     f32x4_t acc[MT][NTK] = {};
     dots<MX, MT, NTK>(a, w, [&](int i) { return row(tile * MT * 16 + i); }, xo,
-                      sh.ring + wave * (kRing<MX> * kSlot), lane, part, parts, acc);
+                      rings + wave * (kRing<MX> * kSlot), lane, part, parts, acc);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -785,9 +799,10 @@ __global__ __launch_bounds__(64) void moe_sum_kernel(MoeArgs a) {
 template <bool MX, bool GATED>
 hipError_t launch_hidden(const MoeArgs& a, hipStream_t s) {
   const dim3 grid((a.F + a.nb - 1) / a.nb, a.Y);
-  if (a.one) moe_hidden_kernel<MX, GATED, true, 1><<<grid, NT, 0, s>>>(a);
-  else if (a.ntk == 1) moe_hidden_kernel<MX, GATED, false, 1><<<grid, NT, 0, s>>>(a);
-  else moe_hidden_kernel<MX, GATED, false, 2><<<grid, NT, 0, s>>>(a);
+  constexpr size_t lds = kWaves * kRing<MX> * kSlot;
+  if (a.one) moe_hidden_kernel<MX, GATED, true, 1><<<grid, NT, lds, s>>>(a);
+  else if (a.ntk == 1) moe_hidden_kernel<MX, GATED, false, 1><<<grid, NT, lds, s>>>(a);
+  else moe_hidden_kernel<MX, GATED, false, 2><<<grid, NT, lds, s>>>(a);
   return hipGetLastError();
 }
 

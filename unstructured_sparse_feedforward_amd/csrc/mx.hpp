@@ -27,12 +27,15 @@ constexpr int wait_imm(int vm, int lgkm) {
   return (vm & 0xF) | ((vm >> 4) << 14) | (7 << 4) | (lgkm << 8);
 }
 
-// A wait that neither the compiler nor its scheduler moves memory accesses
-// across.
-template <int IMM>
-__device__ __forceinline__ void wait_point() {
+// A point that neither the compiler nor its scheduler moves memory accesses
+// across, and a wait there.
+__device__ __forceinline__ void order_point() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
+}
+template <int IMM>
+__device__ __forceinline__ void wait_point() {
+  order_point();
   __builtin_amdgcn_s_waitcnt(IMM);
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("" ::: "memory");

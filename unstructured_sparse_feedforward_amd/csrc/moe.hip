@@ -813,11 +813,14 @@ void moe_plan(bool mx, MoeArgs* a) {
   a->one = a->T == 1 && a->E <= kOneE;
   a->by_pair = pairs < a->E || a->one;
   a->Y = a->by_pair ? pairs : a->E;
-  // as many neurons a workgroup as leave eight workgroups a CU, two for the
-  // few experts of one token
   const int least = mx ? 32 : 16;
   int nb = mx ? kSlice<true> : kSlice<false>;
-  while (nb > least && (int64_t)a->Y * ((a->F + nb - 1) / nb) < (a->T == 1 ? 512 : 2048)) nb /= 2;
+  // As many neurons a workgroup as leave this many workgroups: with bf16 eight
+  // a CU (64 tokens over 16 experts: 100 us, with four 104.5), two for the few
+  // experts of one token (28.5, 30.8 .. 32); codes, a quarter of the bytes a
+  // workgroup, four (32 tokens over 64 experts: 81, with eight 86.8).
+  const int enough = mx ? 1024 : a->T == 1 ? 512 : 2048;
+  while (nb > least && (int64_t)a->Y * ((a->F + nb - 1) / nb) < enough) nb /= 2;
   a->nb = nb;
   // two blocks of 16 tokens a pass where the experts have more than that
   a->ntk = pairs <= 12 * a->E ? 1 : 2;

@@ -41,13 +41,17 @@ __device__ __forceinline__ uint32_t pack8(const float* v, uint32_t sb) {
 __device__ __forceinline__ float ld(const float* p) { return *p; }
 __device__ __forceinline__ float ld(const uint16_t* p) { return bf16lo(*p); }
 
+// 8 elements in 16-byte loads that need no more than the elements' own
+// alignment (the hardware's unaligned access)
+typedef f32x4_t f32x4u_t __attribute__((aligned(4)));
+typedef u32x4_t u32x4u_t __attribute__((aligned(2)));
 __device__ __forceinline__ void load8(const float* p, float* v) {
-  const f32x4_t a = *(const f32x4_t*)p, b = *(const f32x4_t*)(p + 4);
+  const f32x4_t a = *(const f32x4u_t*)p, b = *(const f32x4u_t*)(p + 4);
 #pragma unroll
   for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
 }
 __device__ __forceinline__ void load8(const uint16_t* p, float* v) {
-  Vec<uint16_t, 8>::cvt(*(const u32x4_t*)p, v);
+  Vec<uint16_t, 8>::cvt(*(const u32x4u_t*)p, v);
 }
 
 // Rows as they are stored. A lane holds 8 consecutive elements, four lanes
@@ -59,7 +63,7 @@ constexpr int kQWg = kQRows * NT / 64;   // rows a workgroup
 
 template <typename E>
 __global__ __launch_bounds__(NT) void mx_quantize_kernel(const E* __restrict__ x, int64_t R,
-                                                         int64_t K, int64_t ldx, int vec,
+                                                         int64_t K, int64_t ldx,
                                                          uint8_t* __restrict__ codes,
                                                          uint8_t* __restrict__ scales) {
   __shared__ __align__(16) uint8_t sc[4][kQWg][4];
@@ -76,7 +80,7 @@ __global__ __launch_bounds__(NT) void mx_quantize_kernel(const E* __restrict__ x
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
     if (r < R) {
-      if (vec && c + 8 <= K) {
+      if (c + 8 <= K) {
         load8(p, v[i]);
       } else {
 #pragma unroll
@@ -157,8 +161,8 @@ __global__ __launch_bounds__(kTWaves * 64) void mx_quantize_t_kernel(
 }
 
 __device__ __forceinline__ void store8(float* p, const float* v) {
-  *(f32x4_t*)p = f32x4_t{v[0], v[1], v[2], v[3]};
-  *(f32x4_t*)(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+  *(f32x4u_t*)p = f32x4_t{v[0], v[1], v[2], v[3]};
+  *(f32x4u_t*)(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
 }
 __device__ __forceinline__ uint32_t bf16_bits(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);   // NaN stays NaN
@@ -167,7 +171,7 @@ __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
   u32x4_t o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = bf16_bits(v[2 * i]) | (bf16_bits(v[2 * i + 1]) << 16);
-  *(u32x4_t*)p = o;
+  *(u32x4u_t*)p = o;
 }
 __device__ __forceinline__ void st(float* p, float v) { *p = v; }
 __device__ __forceinline__ void st(uint16_t* p, float v) { *p = (uint16_t)bf16_bits(v); }
@@ -178,7 +182,7 @@ __device__ __forceinline__ void st(uint16_t* p, float v) { *p = (uint16_t)bf16_b
 template <typename E>
 __global__ __launch_bounds__(NT) void mx_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                            const uint8_t* __restrict__ scales,
-                                                           int64_t R, int64_t K, int vec,
+                                                           int64_t R, int64_t K,
                                                            E* __restrict__ out, int64_t ldo) {
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
@@ -203,7 +207,7 @@ __global__ __launch_bounds__(NT) void mx_dequantize_kernel(const uint8_t* __rest
     const f32x2_t e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], s, 3);
     const float v[8] = {a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
     E* o = out + (r0 + i) * ldo + c;
-    if (vec && c + 8 <= K) {
+    if (c + 8 <= K) {
       store8(o, v);
     } else {
 #pragma unroll
@@ -217,7 +221,6 @@ __global__ __launch_bounds__(NT) void mx_dequantize_kernel(const uint8_t* __rest
 
 hipError_t launch_mx_quantize(Dtype dt, const void* x, int64_t rows, int64_t cols, int64_t ldx,
                               bool transposed, uint8_t* codes, uint8_t* scales, hipStream_t s) {
-  const size_t es = dt == kBF16 ? 2 : 4;
   if (transposed) {
     // rows of x are the contracted axis
     const int64_t R = cols, K = rows;
@@ -231,13 +234,12 @@ hipError_t launch_mx_quantize(Dtype dt, const void* x, int64_t rows, int64_t col
                                                                 scales);
     return hipGetLastError();
   }
-  const int vec = (uintptr_t)x % 16 == 0 && (ldx * es) % 16 == 0;
   const dim3 grid((unsigned)((rows + kQWg - 1) / kQWg), (unsigned)((mx_padded(cols) + 511) / 512));
   if (dt == kBF16)
-    mx_quantize_kernel<uint16_t><<<grid, NT, 0, s>>>((const uint16_t*)x, rows, cols, ldx, vec,
-                                                     codes, scales);
+    mx_quantize_kernel<uint16_t><<<grid, NT, 0, s>>>((const uint16_t*)x, rows, cols, ldx, codes,
+                                                     scales);
   else
-    mx_quantize_kernel<float><<<grid, NT, 0, s>>>((const float*)x, rows, cols, ldx, vec, codes,
+    mx_quantize_kernel<float><<<grid, NT, 0, s>>>((const float*)x, rows, cols, ldx, codes,
                                                   scales);
   return hipGetLastError();
 }
@@ -245,14 +247,12 @@ hipError_t launch_mx_quantize(Dtype dt, const void* x, int64_t rows, int64_t col
 hipError_t launch_mx_dequantize(Dtype dt, const uint8_t* codes, const uint8_t* scales,
                                 int64_t rows, int64_t cols, void* out, int64_t ldo,
                                 hipStream_t s) {
-  const size_t es = dt == kBF16 ? 2 : 4;
-  const int vec = (uintptr_t)out % 16 == 0 && (ldo * es) % 16 == 0;
   const dim3 grid((unsigned)((rows + kQWg - 1) / kQWg), (unsigned)((cols + 511) / 512));
   if (dt == kBF16)
-    mx_dequantize_kernel<uint16_t><<<grid, NT, 0, s>>>(codes, scales, rows, cols, vec,
+    mx_dequantize_kernel<uint16_t><<<grid, NT, 0, s>>>(codes, scales, rows, cols,
                                                        (uint16_t*)out, ldo);
   else
-    mx_dequantize_kernel<float><<<grid, NT, 0, s>>>(codes, scales, rows, cols, vec, (float*)out,
+    mx_dequantize_kernel<float><<<grid, NT, 0, s>>>(codes, scales, rows, cols, (float*)out,
                                                     ldo);
   return hipGetLastError();
 }

@@ -425,8 +425,7 @@ sffn_status sffn_check(sffn_handle* h, hipStream_t stream);
  * (products: up to 2^21 rows in either operand), K up to 2^22; a size of 0
  * is valid (nothing is written; a product over K = 0 writes zeros). Codes
  * must be 16-byte and scales 4-byte aligned; float matrices need only their
- * elements' alignment (loads and stores are wider where 16-byte alignment
- * of pointer and row stride allows).
+ * elements' alignment.
  */
 sffn_status sffn_mx_bytes(int64_t rows, int64_t cols, size_t* code_bytes, size_t* scale_bytes);
 
@@ -467,9 +466,10 @@ sffn_status sffn_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int6
  * Only the selected experts' weights are read, the up and down rows only of
  * neurons that are active (strictly z > 0, as everywhere here) for one of
  * the tokens. Logits are summed in 64 bits, so that the choice of experts
- * does not depend on an order of summation; everything else in float32, h
- * entering the down product with 16 significant bits. Results repeat bit
- * for bit.
+ * does not depend on an order of summation; everything else in float32 (h
+ * enters the down product with its 24 bits, in three bf16 parts). The same
+ * call repeats bit for bit; a token's row may differ in its last bits when
+ * the other tokens of the call are others.
  *   d          model width; d % 128 == 0, d <= 8192
  *   d_ff       F, neurons an expert; F % 32 == 0, F <= 65536
  *   n_experts  E <= 1024, E F <= 2^27
@@ -535,8 +535,8 @@ sffn_status sffn_moe_forward(const sffn_moe_desc* desc, const void* x, const sff
                              float* probs, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /*
- * Per-kernel timing. While enabled, every kernel launch of the library is
- * bracketed by two HIP events recorded on the call's stream, so that each
+ * Per-kernel timing. While enabled, every kernel launch of the handle's
+ * calls is bracketed by two HIP events recorded on the call's stream, so that each
  * interval holds one kernel id's launches alone. sffn_profile_read waits
  * for the recorded events, writes for each kernel id k < n the summed
  * milliseconds and the

@@ -23,8 +23,9 @@ def forward(x, w_router, w_gate, w_up, w_down, k, normalize=True):
     Returns (y, ids, probs, bound): |y' - y| <= bound for a y' with
     float32 sums in any order (d, then F, then k terms and at most F / 32
     partial sums; a sum of n terms errs by at most n 2^-23 of the sum of
-    magnitudes, truncating adders included) and h rounded to 2^-16 of
-    itself. The bound on h covers a z whose sign the rounding flips."""
+    magnitudes, truncating adders included) and h rounded to 2^-23 of
+    itself (the product of z and u, and its sum of three bf16 parts, each
+    to half a step of 24 bits). The bound on h covers a z whose sign the rounding flips."""
     ids, probs = route(x, w_router, k, normalize)
     T, d = x.shape
     F = w_gate.shape[1]
@@ -42,7 +43,7 @@ def forward(x, w_router, w_gate, w_up, w_down, k, normalize=True):
                 u = w_up[e] @ x[t]
                 du = d * eps * (np.abs(w_up[e]) @ np.abs(x[t]))
             h = a * u
-            dh = a * du + (np.abs(u) + du) * dz + 2.0 ** -16 * np.abs(h)
+            dh = a * du + (np.abs(u) + du) * dz + eps * np.abs(h)
             y[t] += probs[t, r] * (h @ w_down[e])
             mag = (np.abs(h) + dh) @ np.abs(w_down[e])
             # the weights' exponential and quotient: a few units of 2^-23

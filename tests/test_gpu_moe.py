@@ -1,5 +1,5 @@
 """The expert layer on the GPU against its float64 oracle, within the bound
-that the oracle derives for float32 sums and a 16-bit h."""
+that the oracle derives for float32 sums."""
 import math
 
 import numpy as np
@@ -104,6 +104,39 @@ def test_nothing_active(weights):
     y = torch.full((9, 256), 7.0, device="cuda")
     layer.forward(x, wr, *ws, y=y)
     assert (y == 0).all()
+
+
+@pytest.mark.parametrize("weights", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("T,d,F,E,k,gated", [
+    # more neurons than the down product lists at a time, and the most
+    (3, 128, 8224, 2, 2, True), (40, 128, 8224, 2, 1, False), (2, 128, 65536, 1, 1, True)])
+def test_many_neurons(T, d, F, E, k, gated, weights):
+    print(T, d, F, E, k, gated, weights, flush=True)
+    layer, x, wr, ws = make(T, d, F, E, k, gated, weights, active=0.3)
+    check(layer, x, wr, ws, layer.forward(x, wr, *ws, return_routing=True))
+
+
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("T,E,k", [(1, 2, 1), (1, 64, 32), (1, 65, 2), (1, 127, 31), (1, 128, 32),
+                                   (1, 129, 32), (1, 300, 5), (1, 1024, 32), (3, 1024, 32),
+                                   (9, 16, 4), (9, 17, 4)])
+def test_many_experts(T, E, k, normalize):
+    """Around the sizes at which another kernel routes."""
+    print(T, E, k, normalize, flush=True)
+    layer, x, wr, ws = make(T, 128, 32, E, k, True, "bf16", normalize=normalize)
+    check(layer, x, wr, ws, layer.forward(x, wr, *ws, return_routing=True))
+
+
+@pytest.mark.parametrize("T", [1, 5])
+def test_extreme_logits(T):
+    """Logits so far apart that the smaller weights vanish, and all of them
+    negative: exact zeros, no NaN."""
+    layer, x, wr, ws = make(T, 128, 32, 40, 4, True, "bf16")
+    wr.zero_()
+    wr[:, 0] = -1e4 * torch.arange(1, 41, device="cuda").bfloat16()
+    y, ids, probs = layer.forward(x, wr, *ws, return_routing=True)
+    assert ids.tolist() == [[0, 1, 2, 3]] * T and probs.tolist() == [[1.0, 0.0, 0.0, 0.0]] * T
+    check(layer, x, wr, ws, (y, ids, probs))
 
 
 def test_everyone_to_one_expert():
@@ -245,5 +278,10 @@ def test_refusals_on_the_gpu():
               lambda: layer.forward(x.repeat(65, 1), wr, *ws),
               lambda: layer.forward(x, wr, *ws, routing=(one, one))):
         with pytest.raises(ValueError):
+            f()
+    odd = torch.empty(4 * 256 + 1, device="cuda", dtype=torch.bfloat16)[1:].view(4, 256)
+    for f in (lambda: layer.forward(odd, wr, *ws),
+              lambda: layer.forward(x, wr, *ws, y=torch.empty(1025, device="cuda")[1:].view(4, 256))):
+        with pytest.raises(sffn.SffnError):
             f()
     assert layer.forward(x[:0], wr, *ws).shape == (0, 256)

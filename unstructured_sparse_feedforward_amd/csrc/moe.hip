@@ -6,15 +6,26 @@
 //
 // With few tokens the time is that of reading the selected experts'
 // weights, so every weight is read once (per 16 or 32 of its expert's
-// tokens). Four launches:
-//   route   logits, top k and weights, a workgroup a token;
+// tokens). The launches:
+//   logits  x W_r^T in 64 bits, a wave an expert and token;
+//   route   top k and weights, a workgroup a token (for few experts together
+//           with the logits; a single token's is part of the next kernel);
 //   hidden  a workgroup has an expert and a slice of its neurons: it computes
-//           z for all of the expert's tokens, and u only for the neurons that are active (z > 0) for one of
-//           them, as in the rest of the library;
+//           z for all of the expert's tokens, and u only for the neurons that
+//           are active (z > 0) for one of them, as in the rest of the library;
 //   down    a workgroup has an expert and a chunk of y's columns, and reads
 //           those of the active neurons' rows;
 //   sum     the token's k outputs, weighted, in the order of their ranks (no
-//           float atomics: results repeat bit for bit).
+//           float atomics: results repeat bit for bit). A launch of its own,
+//           2.5 to 4 us: summing in the down kernel's last workgroup a token
+//           takes a device-wide fence in all of them, which cost 10.
+//
+// Measured, launches included, all weights out of the caches: one token over
+// 6 of 64 bf16 experts of 2048 x 1408, a sixth of the neurons active, 28 us
+// (46 MB: 9.4 us at 4.9 TB/s; hidden 14, down 6.5, two small launches 6); 32
+// tokens over 64 experts of that size in 4 bits 81 us (hidden 40, down 25);
+// 64 tokens over 16 bf16 experts of 2048 x 5632, few active, 97 us (hidden 77
+// us, 5.0 TB/s: bound by memory; routing 5, down 10, sum 4).
 #include "moe.hpp"
 
 namespace sffn {
@@ -127,6 +138,7 @@ __device__ __forceinline__ void route(const MoeArgs& a, Route& r) {
   }
   __syncthreads();
 }
+
 // A workgroup a token. LOGITS: it computes them itself, for as many experts
 // as it has waves; with more, their 64-bit sums would keep the one CU busy
 // (64 experts, d = 2048: 8.3 us, in a kernel of their own over all CUs 3.0
@@ -202,8 +214,8 @@ __device__ __forceinline__ f32x4_t mfma(const u32x4_t& w, const u32x4_t& v, cons
 // bf16 values, the instruction's own order, or 128 codes, four instructions'
 // worth.
 template <bool MX>
-constexpr int kRing = MX ? 4 : 5;    // slots
-constexpr int kSlot = 2048;          // bytes
+constexpr int kRing = MX ? 4 : 5;    // slots (a step of the bf16 ring is half the arithmetic)
+constexpr int kSlot = 2048;          // bytes of a slot, two copies of 64 lanes x 16
 
 template <bool MX, int MT, int NTK, typename F>
 __device__ __forceinline__ void dots(const MoeArgs& a, const Rows& w, F&& row,
@@ -489,8 +501,11 @@ __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, cons
 
 // The routing of a single token, for at most kOneE experts: lane l has the
 // keys of experts l and 64 + l, each wave compares them with its share of the
-// experts, and the shares are added. Returns the expert of rank `rank`;
-// *place: the chosen experts before it; `give`: hand the routing on. Called by all threads; holds a barrier.
+// experts, and the shares are added. Returns the expert of rank `rank`, in
+// *place the number of chosen experts of lower index; `give`: write the
+// routing for the kernels to come. Called by all threads; holds a barrier.
+// (Saves a launch: one token over 64 bf16 experts 28.4 us, routed in a kernel
+// of its own 31.5; over 128 4-bit ones 24.7 and 29.3.)
 constexpr int kOneE = 128;
 __device__ __forceinline__ int route_one(const MoeArgs& a, int rank, bool give,
                                          int (&share)[kWaves][kOneE], int* place) {
@@ -606,7 +621,9 @@ constexpr int kSeg = kFl * 8 * NT;   // neurons whose active ones are listed at 
 // A lane loads CPL columns of 8 neurons (16 bytes of bf16, 8 of codes) and
 // turns them into CPL operands, one a column: operand q of lane l holds
 // column CPL (l % 16) + q at k = neurons 8 (l / 16) .. + 7, and the results
-// of a lane are 4 CPL consecutive columns of token l % 16.
+// of a lane are 4 CPL consecutive columns of token l % 16. (A chunk is 256
+// bytes of a bf16 row, 128 of codes: the rows are scattered, and shorter
+// pieces would cost more accesses for the same bytes.)
 template <bool MX>
 constexpr int kCpl = MX ? 16 : 8;
 
@@ -680,7 +697,8 @@ __global__ __launch_bounds__(NT, MX ? 2 : 3) void moe_down_kernel(MoeArgs a) {
       __syncthreads();
       // 32 neurons a step, the steps shared out over the waves, the next
       // step's loads in flight
-      const uint32_t ho = (uint32_t)(place + p0 + min(l15, nt - 1)) * 4, hp4 = (uint32_t)(a.T * a.k) * 4;
+      const uint32_t ho = (uint32_t)(place + p0 + min(l15, nt - 1)) * 4;
+      const uint32_t hp4 = (uint32_t)(a.T * a.k) * 4;
       u32x2_t q[2][8];
       uint32_t sb[2][8];
       u32x4_t raw[2][8];
@@ -811,6 +829,8 @@ hipError_t launch_hidden(const MoeArgs& a, hipStream_t s) {
 void moe_plan(bool mx, MoeArgs* a) {
   const int pairs = a->T * a->k;
   a->one = a->T == 1 && a->E <= kOneE;
+  // units of the fewer of pairs and experts (8 tokens of 6 over 64 experts
+  // 78 us, with a unit for every expert 82; 4 tokens 60.8, 58.5)
   a->by_pair = pairs < a->E || a->one;
   a->Y = a->by_pair ? pairs : a->E;
   const int least = mx ? 32 : 16;
@@ -822,7 +842,10 @@ void moe_plan(bool mx, MoeArgs* a) {
   const int enough = mx ? 1024 : a->T == 1 ? 512 : 2048;
   while (nb > least && (int64_t)a->Y * ((a->F + nb - 1) / nb) < enough) nb /= 2;
   a->nb = nb;
-  // two blocks of 16 tokens a pass where the experts have more than that
+  // Two blocks of 16 tokens a pass where the experts have more than that: a
+  // mean of 12 tokens costs the same either way (96 tokens of 8 over 64 bf16
+  // experts of 2048 x 1408: 254, 252 us), 8 tokens 206 and 211, 16 tokens 319
+  // and 301.
   a->ntk = pairs <= 12 * a->E ? 1 : 2;
   const int cols = 16 * (mx ? kCpl<true> : kCpl<false>);
   a->chunks = (a->d + cols - 1) / cols;

@@ -623,7 +623,8 @@ constexpr int kSeg = kFl * 8 * NT;   // neurons whose active ones are listed at 
 // column CPL (l % 16) + q at k = neurons 8 (l / 16) .. + 7, and the results
 // of a lane are 4 CPL consecutive columns of token l % 16. (A chunk is 256
 // bytes of a bf16 row, 128 of codes: the rows are scattered, and shorter
-// pieces would cost more accesses for the same bytes.)
+// pieces cost more accesses for the same bytes. 32 tokens over 64 4-bit
+// experts: 80 us, with 8 columns a lane and more workgroups 86.)
 template <bool MX>
 constexpr int kCpl = MX ? 16 : 8;
 

@@ -237,13 +237,24 @@ struct Big {
 
 // An accumulator at the point of use. 256 of them are in AGPRs: read there,
 // one by one, or the compiler moves (and converts) them all before the
-// epilogue's branch, which spills.
+// epilogue's branch, which spills. (The compiler adds no wait states between
+// a matrix instruction and inline asm that reads its result: see
+// settle_sums.)
 template <int MI>
 __device__ __forceinline__ float sum_of(float a) {
   if constexpr (MI < 4) return a;
   float v;
   asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
   return v;
+}
+
+// Before the first sum_of after a matrix instruction: its result may be read
+// 18 wait states later at the earliest.
+template <int MI>
+__device__ __forceinline__ void settle_sums() {
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (MI == 4) asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 template <int MI, int NS, typename O>
@@ -423,6 +434,7 @@ __global__ __launch_bounds__(256, (Big<MI, NS>::WGS)) void mx_big_kernel(MxGemmA
       pslot = slot;
       slot = next;
     }
+    settle_sums<MI>();
     int m0, n0;
     coords(L, m0, n0);
     O* out = (O*)g.out + (int64_t)(m0 + wr * C_::WM + 4 * hi) * g.ldo + n0 + wc * 128 + l31;
@@ -489,7 +501,8 @@ hipError_t launch(const MxGemmArgs& g, hipStream_t s) {
   if (t64 <= 128)
     mx_mid_kernel<1, O><<<dim3((unsigned)n64, (unsigned)m32), 256, Mid<1>::LDS, s>>>(g);
   else if (t64 <= 512 || g.K == 0)   // (no tile of the others is ever empty)
-    mx_mid_kernel<2, O><<<dim3((unsigned)n64, (unsigned)((g.M + 63) / 64)), 256, Mid<2>::LDS, s>>>(g);
+    mx_mid_kernel<2, O><<<dim3((unsigned)n64, (unsigned)((g.M + 63) / 64)), 256, Mid<2>::LDS,
+                          s>>>(g);
   else if (t256 <= 160 || g.K <= 1024)
     mx_big_kernel<2, 3, O><<<2 * kCus, 256, Big<2, 3>::LDS, s>>>(g);
   else

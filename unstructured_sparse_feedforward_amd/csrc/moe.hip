@@ -25,7 +25,7 @@
 // Measured, launches included, all weights out of the caches: one token over
 // 6 of 64 bf16 experts of 2048 x 1408, a sixth of the neurons active, 28 us
 // (46 MB: 9.4 us at 4.9 TB/s; hidden 14, down 6.5, two small launches 6); 32
-// tokens over 64 experts of that size in 4 bits 81 us (hidden 40, down 25);
+// tokens over 64 experts of that size in 4 bits 78 us (hidden 37, down 25);
 // 64 tokens over 16 bf16 experts of 2048 x 5632, few active, 97 us (hidden 77
 // us, 5.0 TB/s: bound by memory; routing 5, down 10, sum 4).
 #include "moe.hpp"
@@ -200,8 +200,8 @@ __device__ __forceinline__ f32x4_t mfma(const u32x4_t& w, const u32x4_t& v, cons
 // ---------------------------------------------------------------- products with x
 
 // acc[i][n] += rows 16 i .. of row() . x of 16 tokens (xo[n]: the offset of
-// a lane's token), over steps part, part + parts, .. of d: 64 columns of bf16,
-// 128 of codes.
+// token l % 16 for lane l; XL: of token l / 16), over steps part, part +
+// parts, .. of d: 64 columns of bf16, 128 of codes.
 //
 // The rows go through a ring of D slots in LDS of the wave's own (no barrier:
 // the wave waits for its own oldest copies): a copy instruction covers whole
@@ -215,18 +215,31 @@ __device__ __forceinline__ f32x4_t mfma(const u32x4_t& w, const u32x4_t& v, cons
 // agree: lane l reads piece l / 16 of a row's four of 64 bytes, which are 32
 // bf16 values, the instruction's own order, or 128 codes, four instructions'
 // worth.
+//
+// XL (codes, up to kStaged tokens): x goes through the ring too. Loaded
+// straight into the instruction's lanes it takes an access for every token
+// and 16 bytes, four instructions a step; one copy brings a step's 256 bytes
+// of four tokens, 16-byte piece c of token t at position c ^ t of 16. With 32
+// tokens over 64 4-bit experts (three each) 77.7 us in place of 81.4. (bf16
+// steps have half the x to load for twice the weights: even.)
 template <bool MX>
-constexpr int kRing = MX ? 4 : 5;    // slots (a step of the bf16 ring is half the arithmetic)
-constexpr int kSlot = 2048;          // bytes of a slot, two copies of 64 lanes x 16
+constexpr int kRing = MX ? 3 : 5;      // slots: with four of codes registers spill
+constexpr int kSlot = 2048;            // bytes: two copies of 64 lanes x 16
+constexpr int kStaged = 4;
+template <bool XL>
+constexpr int kStep = kSlot + (XL ? 1024 : 0);
+template <bool MX>
+constexpr int kRingBytes = kRing<MX> * kStep<MX>;
 
-template <bool MX, int MT, int NTK, typename F>
+template <bool MX, int MT, int NTK, bool XL, typename F>
 __device__ __forceinline__ void dots(const MoeArgs& a, const Rows& w, F&& row,
                                      const uint32_t (&xo)[NTK], char* ring, int lane, int part,
                                      int parts, f32x4_t (&acc)[MT][NTK]) {
   static_assert(MT == (MX ? 2 : 1), "a slot holds two copies");
+  static_assert(!XL || (MX && NTK == 1), "staged x is one copy of a step of codes");
   constexpr int D = kRing<MX>, NF = MX ? 4 : 2;    // MFMAs a step and block
   constexpr int SC = MX ? 128 : 64, SB = MX ? 64 : 128;   // columns and row bytes a step
-  constexpr int OPS = 2 + (MX ? MT : 0) + NTK * NF;       // loads a step
+  constexpr int OPS = 2 + (MX ? MT : 0) + (XL ? 1 : NTK * NF);  // loads a step
   const int kq = lane >> 4, l15 = lane & 15;
   // 32-bit offsets from an address that all lanes share
   uint32_t po[2], so[MT], xp[NTK];
@@ -241,32 +254,43 @@ __device__ __forceinline__ void dots(const MoeArgs& a, const Rows& w, F&& row,
     for (int i = 0; i < MT; ++i) so[i] = (uint32_t)row(16 * i + l15) * 4 + kq;
   }
 #pragma unroll
-  for (int n = 0; n < NTK; ++n) xp[n] = xo[n] + kq * (MX ? 64 : 16);
+  for (int n = 0; n < NTK; ++n)
+    xp[n] = xo[n] + (XL ? (l15 ^ kq) * 16 : kq * (MX ? 64 : 16));
   const uint8_t* xb = (const uint8_t*)a.x;
-  u32x4_t xv[D][NTK][NF];
+  u32x4_t xv[XL ? 1 : D][NTK][NF];
   uint32_t sb[D][MT];
   auto load = [&](auto ss, int i) {
     constexpr int s = decltype(ss)::value;
     const int64_t g = part + i * parts;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) copy16(w.p + g * SB, po[c], ring + s * kSlot + c * 1024);
+    for (int c = 0; c < 2; ++c) copy16(w.p + g * SB, po[c], ring + s * kStep<XL> + c * 1024);
     if constexpr (MX) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) sb[s][m] = *(w.sc + g * w.gpitch + so[m]);
     }
+    if constexpr (XL) {
+      copy16(xb + g * (SC * 2), xp[0], ring + s * kStep<XL> + kSlot);
+    } else {
 #pragma unroll
-    for (int n = 0; n < NTK; ++n)
+      for (int n = 0; n < NTK; ++n)
 #pragma unroll
-      for (int f = 0; f < NF; ++f)
-        xv[s][n][f] = *(const u32x4_t*)(xb + g * (SC * 2) + f * (MX ? 16 : 64) + xp[n]);
+        for (int f = 0; f < NF; ++f)
+          xv[s][n][f] = *(const u32x4_t*)(xb + g * (SC * 2) + f * (MX ? 16 : 64) + xp[n]);
+    }
   };
   u32x4_t q[2];
   auto read = [&](auto ss) {
-    const char* p = ring + decltype(ss)::value * kSlot;
+    const char* p = ring + decltype(ss)::value * kStep<XL>;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
       q[c] = *(const u32x4_t*)(MX ? p + c * 1024 + l15 * 64 + ((kq ^ ((l15 >> 2) & 3)) << 4)
                                   : p + l15 * 128 + (((c * 4 + kq) ^ ((l15 >> 1) & 7)) << 4));
+    if constexpr (XL) {
+      const int t = l15 & (kStaged - 1);
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+        xv[0][0][f] = *(const u32x4_t*)(p + kSlot + t * 256 + (((kq * 4 + f) ^ t) << 4));
+    }
     wait_point<wait_imm(63, 0)>();     // read before the slot is written again
   };
   auto multiply = [&](auto ss) {
@@ -277,7 +301,7 @@ __device__ __forceinline__ void dots(const MoeArgs& a, const Rows& w, F&& row,
       for (int m = 0; m < MT; ++m) {
         const u32x4_t wv = MX ? from_codes(q[m][f & 3], sb[s][m]) : q[f & 1];
 #pragma unroll
-        for (int n = 0; n < NTK; ++n) acc[m][n] = mfma(wv, xv[s][n][f], acc[m][n]);
+        for (int n = 0; n < NTK; ++n) acc[m][n] = mfma(wv, xv[XL ? 0 : s][n][f], acc[m][n]);
       }
   };
   const int G = a.d / SC;
@@ -331,7 +355,6 @@ constexpr int kSlice = kWaves * 16 * kBlocks<MX>;
 template <bool MX, int NTK>
 struct Shared {
   static constexpr int MT = kBlocks<MX>, SL = kSlice<MX>;
-  f32x4_t red[kWaves][MT][NTK][64];    // the waves' shares of a product with x
   float z[16 * NTK][SL + 4];           // gate pre-activations (padded rows)
   int act[SL];                         // active neurons of the slice, ascending
   uint8_t on[SL];
@@ -339,16 +362,20 @@ struct Shared {
 };
 
 // The waves' rings. (Dynamic LDS: for reads of a static object the compiler
-// waits for every copy into LDS in flight.)
+// waits for every copy into LDS in flight.) A wave's ring, when its copies
+// have all landed, also holds its share of a product.
 extern __shared__ __align__(16) char rings[];
 
 // The products of tiles of 16 MT rows with the pass's tokens: the waves share
 // out the tiles, and d where the tiles are fewer than the waves. row(i) is
-// the row of position i. Leaves the shares in sh.red, joined by share_sum.
-template <bool MX, int NTK, typename F>
-__device__ __forceinline__ int share_products(const MoeArgs& a, Shared<MX, NTK>& sh,
-                                              const Rows& w, const uint32_t (&xo)[NTK], int tiles,
-                                              F&& row) {
+// the row of position i. Leaves the shares in the rings, joined by share_sum.
+template <bool MX, int NTK>
+__device__ __forceinline__ f32x4_t& share_of(int wave, int i, int t, int lane) {
+  return *(f32x4_t*)(rings + wave * kRingBytes<MX> + ((i * NTK + t) * 64 + lane) * 16);
+}
+template <bool MX, int NTK, bool XL, typename F>
+__device__ __forceinline__ int share_products(const MoeArgs& a, const Rows& w,
+                                              const uint32_t (&xo)[NTK], int tiles, F&& row) {
   constexpr int MT = kBlocks<MX>;
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
@@ -356,22 +383,21 @@ __device__ __forceinline__ int share_products(const MoeArgs& a, Shared<MX, NTK>&
   const int parts = kWaves >> lg, tile = wave >> (2 - lg), part = wave & (parts - 1);
   if (tile < tiles) {
     f32x4_t acc[MT][NTK] = {};
-    dots<MX, MT, NTK>(a, w, [&](int i) { return row(tile * MT * 16 + i); }, xo,
-                      rings + wave * (kRing<MX> * kSlot), lane, part, parts, acc);
+    dots<MX, MT, NTK, XL>(a, w, [&](int i) { return row(tile * MT * 16 + i); }, xo,
+                      rings + wave * kRingBytes<MX>, lane, part, parts, acc);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int t = 0; t < NTK; ++t) sh.red[wave][i][t][lane] = acc[i][t];
+      for (int t = 0; t < NTK; ++t) share_of<MX, NTK>(wave, i, t, lane) = acc[i][t];
   }
   return parts;
 }
 template <bool MX, int NTK>
-__device__ __forceinline__ f32x4_t share_sum(const Shared<MX, NTK>& sh, int parts, int block,
-                                             int t, int l) {
+__device__ __forceinline__ f32x4_t share_sum(int parts, int block, int t, int l) {
   constexpr int MT = kBlocks<MX>;
   const int w0 = block / MT * parts;
-  f32x4_t s = sh.red[w0][block % MT][t][l];
-  for (int p = 1; p < parts; ++p) s += sh.red[w0 + p][block % MT][t][l];
+  f32x4_t s = share_of<MX, NTK>(w0, block % MT, t, l);
+  for (int p = 1; p < parts; ++p) s += share_of<MX, NTK>(w0 + p, block % MT, t, l);
   return s;
 }
 
@@ -424,7 +450,7 @@ __device__ __forceinline__ int unit_pairs(const MoeArgs& a, int unit, Lists& ls,
 
 // 16 NTK of the unit's tokens (list positions p0 ..) through the slice's
 // neurons j0 .. j0 + nbe: their h, and in `any` the neurons active for one.
-template <bool MX, bool GATED, int NTK>
+template <bool MX, bool GATED, int NTK, bool XL>
 __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, const Lists& ls,
                                      const Rows& wg, const Rows& wu, int j0, int nbe, int n,
                                      int p0, int place, uint8_t* any) {
@@ -436,17 +462,19 @@ __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, cons
   const int P = a.T * a.k;
   uint32_t xo[NTK];
 #pragma unroll
-  for (int i = 0; i < NTK; ++i)
-    xo[i] = (uint32_t)(ls.pair[p0 + min(i * 16 + (lane & 15), nt - 1)] / a.k) * (uint32_t)(a.d * 2);
+  for (int i = 0; i < NTK; ++i) {
+    const int tk = i * 16 + (XL ? lane >> 4 : lane & 15);
+    xo[i] = (uint32_t)(ls.pair[p0 + min(tk, nt - 1)] / a.k) * (uint32_t)(a.d * 2);
+  }
 
   if (tid < kSlice<MX>) sh.on[tid] = 0;
   const int blocks = nbe / 16;
-  int parts = share_products<MX, NTK>(a, sh, wg, xo, (blocks + MT - 1) / MT,
+  int parts = share_products<MX, NTK, XL>(a, wg, xo, (blocks + MT - 1) / MT,
                                       [&](int i) { return j0 + min(i, nbe - 1); });
   __syncthreads();
   for (int e = tid; e < blocks * NTK * 64; e += NT) {
     const int block = e / (NTK * 64), t = (e >> 6) % NTK, l = e & 63;
-    const f32x4_t s = share_sum<MX, NTK>(sh, parts, block, t, l);
+    const f32x4_t s = share_sum<MX, NTK>(parts, block, t, l);
     const int tk = t * 16 + (l & 15), j = block * 16 + 4 * (l >> 4);
     *(f32x4_t*)&sh.z[tk][j] = s;
     if (tk < nt) {
@@ -478,13 +506,13 @@ __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, cons
   __syncthreads();
   const int na = sh.na;
   if (na == 0) return;
-  parts = share_products<MX, NTK>(a, sh, wu, xo, (na + 16 * MT - 1) / (16 * MT),
+  parts = share_products<MX, NTK, XL>(a, wu, xo, (na + 16 * MT - 1) / (16 * MT),
                                   [&](int i) { return j0 + sh.act[min(i, na - 1)]; });
   __syncthreads();
   // h of the active neurons; the others' is not read
   for (int e = tid; e < (na + 15) / 16 * NTK * 64; e += NT) {
     const int block = e / (NTK * 64), t = (e >> 6) % NTK, l = e & 63;
-    const f32x4_t u = share_sum<MX, NTK>(sh, parts, block, t, l);
+    const f32x4_t u = share_sum<MX, NTK>(parts, block, t, l);
     const int tk = t * 16 + (l & 15);
     if (tk < nt) {
       float* o = a.h + (int64_t)j0 * P + place + p0 + tk;
@@ -608,8 +636,12 @@ __global__ __launch_bounds__(NT, NTK == 1 ? 4 : 2) void moe_hidden_kernel(MoeArg
   const Rows wu = {GATED ? (const uint8_t*)a.wu + row0 * pitch : nullptr,
                    MX && GATED ? a.su + row0 * 4 : nullptr, pitch, gp};
   for (int p0 = 0; p0 < n; p0 += 16 * NTK) {
-    if (n - p0 <= 16) pass<MX, GATED, 1>(a, sh.s1, ls, wg, wu, j0, nbe, n, p0, place, any);
-    else pass<MX, GATED, NTK>(a, sh.s, ls, wg, wu, j0, nbe, n, p0, place, any);
+    if (MX && n - p0 <= kStaged)
+      pass<MX, GATED, 1, MX>(a, sh.s1, ls, wg, wu, j0, nbe, n, p0, place, any);
+    else if (n - p0 <= 16)
+      pass<MX, GATED, 1, false>(a, sh.s1, ls, wg, wu, j0, nbe, n, p0, place, any);
+    else
+      pass<MX, GATED, NTK, false>(a, sh.s, ls, wg, wu, j0, nbe, n, p0, place, any);
     __syncthreads();
   }
   if (tid < nbe) a.on[(int64_t)unit * a.F + j0 + tid] = any[tid];
@@ -626,7 +658,7 @@ constexpr int kSeg = kFl * 8 * NT;   // neurons whose active ones are listed at 
 // of a lane are 4 CPL consecutive columns of token l % 16. (A chunk is 256
 // bytes of a bf16 row, 128 of codes: the rows are scattered, and shorter
 // pieces cost more accesses for the same bytes. 32 tokens over 64 4-bit
-// experts: 80 us, with 8 columns a lane and more workgroups 86.)
+// experts: 80 us, 8 columns a lane and twice the workgroups 86.)
 template <bool MX>
 constexpr int kCpl = MX ? 16 : 8;
 
@@ -820,7 +852,7 @@ __global__ __launch_bounds__(64) void moe_sum_kernel(MoeArgs a) {
 template <bool MX, bool GATED>
 hipError_t launch_hidden(const MoeArgs& a, hipStream_t s) {
   const dim3 grid((a.F + a.nb - 1) / a.nb, a.Y);
-  constexpr size_t lds = kWaves * kRing<MX> * kSlot;
+  constexpr size_t lds = kWaves * kRingBytes<MX>;
   if (a.one) moe_hidden_kernel<MX, GATED, true, 1><<<grid, NT, lds, s>>>(a);
   else if (a.ntk == 1) moe_hidden_kernel<MX, GATED, false, 1><<<grid, NT, lds, s>>>(a);
   else moe_hidden_kernel<MX, GATED, false, 2><<<grid, NT, lds, s>>>(a);

@@ -112,3 +112,9 @@ def test_python_refusals():
                              "contiguous")):
         with pytest.raises(ValueError, match=why):
             sffn.MXTensor(c, s, r, k)
+
+
+def test_empty_on_the_cpu_is_refused():
+    """Its pointers would reach a kernel through mx_dequantize."""
+    with pytest.raises(ValueError, match="GPU"):
+        sffn.mx_empty(4, 128, "cpu")

@@ -7,4 +7,5 @@ layer, and :mod:`.workloads` draws the seeded synthetic inputs.
 """
 from .binding import SparseFFN, SffnError, load_library  # noqa: F401
 from .moe import SparseMoE  # noqa: F401
-from .mxfp4 import MXTensor, mx_dequantize, mx_matmul, mx_quantize  # noqa: F401
+from .mxfp4 import (MXTensor, mx_dequantize, mx_empty, mx_matmul,  # noqa: F401
+                    mx_quantize)

@@ -67,6 +67,8 @@ def mx_empty(rows: int, cols: int, device) -> MXTensor:
     g = (cols + 127) // 128
     q = MXTensor.__new__(MXTensor)
     q._buf = buf = torch.empty(rows * g * 68, dtype=torch.uint8, device=device)
+    if not buf.is_cuda:
+        raise ValueError("device must be a GPU")
     q.rows, q.cols, q.device, q._codes, q._scales = rows, cols, buf.device, None, None
     q._pc = buf.data_ptr()
     q._ps = q._pc + rows * g * 64

@@ -499,8 +499,7 @@ class SparseFFN:
                                                  _ptr(w_down), _ptr(act), _ptr(dy), T, _ptr(dx),
                                                  _ptr(dwg), _ptr(dwu), _ptr(dwd),
                                                  float(l1_coeff), ws, nb, _stream()),
-                    "sffn_backward_dense", "sffn_mx_bytes", "sffn_mx_quantize", "sffn_mx_dequantize",
-           "sffn_mx_matmul", "sffn_moe_workspace_bytes", "sffn_moe_forward")
+                    "sffn_backward_dense")
         return dx, dwg, dwu, dwd
 
     def hybrid_check(self, hy) -> int:

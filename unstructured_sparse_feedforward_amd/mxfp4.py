@@ -88,11 +88,13 @@ def _launch(device: torch.device, what: str, f, *args) -> None:
         raise SffnError(st, f"{what}: {load_library().sffn_status_string(st).decode()}")
 
 
-def _matrix(t: torch.Tensor, what: str) -> int:
-    """The row stride of a 2-D float matrix with contiguous rows."""
+def _matrix(t: torch.Tensor, what: str):
+    """(rows, columns, row stride, type's number) of a 2-D float matrix with
+    contiguous rows."""
     if not t.is_cuda:
         raise ValueError(f"{what} must be on the GPU")
-    if t.dtype not in _DTYPES:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{what} must be float32 or bfloat16, not {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{what} must have 2 dimensions, not {t.dim()}")
@@ -101,23 +103,26 @@ def _matrix(t: torch.Tensor, what: str) -> int:
     if one != 1 and cols > 1:
         raise ValueError(f"{what} must have contiguous rows")
     if rows <= 1:
-        return cols
+        return rows, cols, cols, dt
     if ld < cols:
         raise ValueError(f"{what}'s rows overlap")
-    return ld
+    return rows, cols, ld, dt
 
 
 def _result(out: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtype,
             device: torch.device):
     """(out, its row stride, its type's number), made when not given."""
     if out is None:
-        if dtype not in _DTYPES:
+        dt = _DTYPES.get(dtype)
+        if dt is None:
             raise ValueError(f"dtype must be float32 or bfloat16, not {dtype}")
-        return torch.empty((rows, cols), dtype=dtype, device=device), cols, _DTYPES[dtype]
-    ld = _matrix(out, "out")
-    if out.shape != (rows, cols) or out.device != device:
+        # (0.3 us less of the host's time than torch.empty of a shape)
+        out = torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+        return out, cols, dt
+    r, c, ld, dt = _matrix(out, "out")
+    if r != rows or c != cols or out.device != device:
         raise ValueError(f"out must be {rows} x {cols} on {device}")
-    return out, ld, _DTYPES[out.dtype]
+    return out, ld, dt
 
 
 def mx_quantize(x: torch.Tensor, transposed: bool = False,
@@ -126,16 +131,15 @@ def mx_quantize(x: torch.Tensor, transposed: bool = False,
     stride) in MXFP4. With ``transposed`` the result is x^T's, its blocks
     down the columns of x: the form of a weight stored [F, d] for a product
     over F. ``out`` may pass an MXTensor of the result's size to reuse."""
-    ld = _matrix(x, "x")
-    rows, cols = x.shape
+    rows, cols, ld, dt = _matrix(x, "x")
     R, K = (cols, rows) if transposed else (rows, cols)
     device = x.device
     if out is None:
         out = mx_empty(R, K, device)
     elif out.rows != R or out.cols != K or out.device != device:
         raise ValueError(f"out must be {R} x {K} on {device}")
-    _launch(device, "sffn_mx_quantize", load_library().sffn_mx_quantize, x.data_ptr(),
-            _DTYPES[x.dtype], rows, cols, ld, 1 if transposed else 0, out._pc, out._ps)
+    _launch(device, "sffn_mx_quantize", load_library().sffn_mx_quantize, x.data_ptr(), dt,
+            rows, cols, ld, 1 if transposed else 0, out._pc, out._ps)
     return out
 
 

@@ -84,13 +84,14 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx_few_kernel(MxGemmArgs g) {
 // A (32 I) x 64 tile a workgroup, whose four waves share out K by 128-wide
 // groups. With few tiles the time is the latency of the operands' loads, so
 // each wave has a ring of its own in LDS, filled by direct copies kMidSlots
-// groups ahead: nothing is shared before the sums, so there is no barrier
+// groups ahead (two, which leave room for a second workgroup on the CU: 1024
+// x 2048 x 2048 10.2 us, with four 12.1): nothing is shared before the sums, so there is no barrier
 // in the loop, only the wave's wait for its own oldest copies. A slot holds
 // the rows' codes, row r's 16-byte piece c at position c ^ (r / 4) % 4 (so
 // that 16 lanes reading one piece of 16 rows meet 16 different bank
 // groups), then their scale dwords. Lane l holds row l % 32 of a 32-row
 // block and k = 32 (l / 32) .. + 31 of a 64-wide step.
-constexpr int kMidSlots = 4;
+constexpr int kMidSlots = 2;
 
 template <int I>
 struct Mid {
@@ -475,10 +476,10 @@ __global__ __launch_bounds__(256, (Big<MI, NS>::WGS)) void mx_big_kernel(MxGemmA
 // M x N x K; the sides of each border):
 //   few rows:    1 x 5632 x 2048 4.0
 //   32 x 64:     up to 128 tiles of 64 x 64, which leave CUs without one:
-//                256 x 2048 x 2048 (128 tiles) 5.4, 64 x 64 6.2;
-//                128 x 5632 x 2048 (176) 8.0, 64 x 64 6.7
+//                256 x 2048 x 2048 (128 tiles) 5.5, 64 x 64 5.8;
+//                256 x 4096 x 2048 (256) 6.5, 64 x 64 6.2
 //   64 x 64:     up to 512 such tiles, two a CU: 1024 x 2048 x 2048 (512)
-//                11.5, 128 x 256 12.3; 512 x 5632 x 2048 (704) 16.6, 13.0
+//                10.2, 128 x 256 12.3; 512 x 5632 x 2048 (704) 13.4, 13.2
 //   128 x 256:   two workgroups a CU, better while a 256 x 256 tile each
 //                leaves CUs idle (4096 x 2048 x 5632, 128 of them: 33.0, 256 x
 //                256 37.7; 2048 x 5632 x 2048, 176: 23.4, 22.2) and for short K,

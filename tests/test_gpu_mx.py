@@ -152,7 +152,10 @@ def _assert_product(out, a, b):
 SIZES = [(1, 1, 1), (1, 16, 128), (1, 5632, 2048), (2, 17, 33), (16, 100, 1000), (17, 64, 256),
          (32, 33, 4096), (33, 48, 129), (64, 1003, 640), (65, 65, 65), (100, 200, 300),
          (128, 128, 128), (129, 257, 384), (333, 1003, 1999), (256, 256, 2048), (257, 511, 130),
-         (1000, 1100, 512), (700, 2048, 1408)]
+         (1000, 1100, 512), (700, 2048, 1408),
+         # few rows, K up to 4096 and above; long K
+         (1, 300, 5000), (3, 40, 4096), (9, 64, 4097), (16, 1003, 16384), (64, 64, 16384),
+         (40, 700, 8192), (2, 15, 4200)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])

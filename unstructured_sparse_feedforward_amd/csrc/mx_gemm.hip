@@ -22,61 +22,85 @@ __device__ __forceinline__ void put(uint16_t* p, float v) {
 
 // ---------------------------------------------------------------- few rows
 
-// M <= 16 MT rows of a: one workgroup for 16 rows of b, whose waves share
-// out K by 128-wide groups and add their sums in LDS. The rows of b are the
-// instruction's first operand: lane l holds row l % 16, k = 32 (l / 16) ..
-// + 31, and of the result four consecutive n of row m = l % 16.
-constexpr int kFewWaves = 8;
+// M <= 16 rows of a: one workgroup for 16 rows of b, whose waves share out K
+// by 128-wide groups and add their sums in LDS. Each wave has a ring of its
+// own in LDS, filled by direct copies kFewSlots groups ahead: loads straight
+// into the instruction's lanes, which hold different rows, take an access
+// each (16 x 16384 x 4096: 11.4 us, so 7.8; 16 x 1024 x 16384: 10.5, 5.4). The
+// rows of b are the instruction's first operand: lane l holds row l % 16, k =
+// 32 (l / 16) .. + 31, and of the result four consecutive n of row m = l % 16.
+// A slot holds the 16 rows of b and those of a, row r's 16-byte piece c at
+// position c ^ (r / 4) % 4 (so that 16 lanes reading one piece of 16 rows meet
+// 16 different bank groups), then their scale dwords.
+//
+// W waves: 8 for long K, 4 else (1 x 1024 x 16384 5.4 us, with 4 6.3; 1 x 5632
+// x 2048 3.35, 2.95; even at K = 4096).
+constexpr int kFewSlots = 2;                   // with three 3.1 us for the last
+constexpr int kFewSlot = 2 * 1024 + 2 * 256;   // 64 dwords of scales of either
+constexpr int kFewRing = kFewSlots * kFewSlot;
 
-template <int MT, typename O>
-__global__ __launch_bounds__(kFewWaves * 64) void mx_few_kernel(MxGemmArgs g) {
-  __shared__ f32x4_t red[kFewWaves][MT][64];
+template <int W, typename O>
+__global__ __launch_bounds__(W * 64) void mx_few_kernel(MxGemmArgs g) {
+  extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kq = lane >> 4, l15 = lane & 15;
   const int64_t rb = mx_padded(g.K) / 2;
   const int G = (int)(rb / 64);
   const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int64_t n = min(n0 + (lane & 15), g.N - 1);
-  const int kq = lane >> 4;
-  const uint8_t* pb = g.b + n * rb + kq * 16;
-  const uint8_t* pbs = g.b_sc + n * 4 + kq;
-  const uint8_t* pa[MT];
-  const uint8_t* pas[MT];
+  char* ring = smem + wave * kFewRing;
+
+  // rows past the end repeat the last one
+  const int lr = lane >> 2, lc = (lane & 3) ^ ((lane >> 4) & 3);
+  const int ma = (int)g.M - 1, nb = (int)min(g.N - 1 - n0, (int64_t)15);
+  const uint32_t va = (uint32_t)min(lr, ma) * (uint32_t)rb + lc * 16;
+  const uint32_t vb = (uint32_t)min(lr, nb) * (uint32_t)rb + lc * 16;
+  const uint32_t vsa = (uint32_t)min(l15, ma) * 4, vsb = (uint32_t)min(l15, nb) * 4;
+  const uint8_t* pb = g.b + n0 * rb;
+  auto copy = [&](int t, int slot) {
+    char* s = ring + slot * kFewSlot;
+    copy16(pb + (int64_t)t * 64, vb, s);
+    copy16(g.a + (int64_t)t * 64, va, s + 1024);
+    copy4(g.b_sc + ((int64_t)t * g.N + n0) * 4, vsb, s + 2048);
+    copy4(g.a_sc + (int64_t)t * g.M * 4, vsa, s + 2304);
+  };
+  f32x4_t acc = {};
+  // a wave's groups are wave, wave + W, ..; past the last it copies that
+  // again, so that the number of copies in flight is always the same
+  const int mine = G > wave ? (G - wave + W - 1) / W : 0;
+  const int last = wave + W * (mine - 1);
+  if (mine > 0) {
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t m = min((int64_t)(i * 16 + (lane & 15)), g.M - 1);
-    pa[i] = g.a + m * rb + kq * 16;
-    pas[i] = g.a_sc + m * 4 + kq;
-  }
-  f32x4_t acc[MT] = {};
-#pragma unroll 4
-  for (int t = wave; t < G; t += kFewWaves) {
-    const i32x4_t bv = *(const i32x4_t*)(pb + (int64_t)t * 64);
-    const int bs = pbs[(int64_t)t * g.N * 4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const i32x4_t av = *(const i32x4_t*)(pa[i] + (int64_t)t * 64);
-      const int as = pas[i][(int64_t)t * g.M * 4];
-      acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(bv), frag(av), acc[i], kFp4,
-                                                                kFp4, 0, bs, 0, as);
+    for (int p = 0; p < kFewSlots; ++p) copy(min(wave + W * p, last), p);
+    int slot = 0;
+    for (int q = 0; q < mine; ++q) {
+      // the oldest slot's copies have landed
+      wait_point<wait_imm((kFewSlots - 1) * 4, 15)>();
+      const char* s = ring + slot * kFewSlot;
+      const int c = l15 * 64 + ((kq ^ ((l15 >> 2) & 3)) << 4);
+      const i32x4_t bv = *(const i32x4_t*)(s + c), av = *(const i32x4_t*)(s + 1024 + c);
+      const int bs = *(const uint8_t*)(s + 2048 + l15 * 4 + kq);
+      const int as = *(const uint8_t*)(s + 2304 + l15 * 4 + kq);
+      // everything read before the slot is written again
+      wait_point<wait_imm(63, 0)>();
+      copy(min(wave + W * (q + kFewSlots), last), slot);
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(bv), frag(av), acc, kFp4, kFp4,
+                                                             0, bs, 0, as);
+      slot = slot + 1 == kFewSlots ? 0 : slot + 1;
     }
   }
-#pragma unroll
-  for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[i];
+  // a wave's ring takes its sums once its copies have landed
+  wait_point<wait_imm(0, 0)>();
+  *(f32x4_t*)(ring + lane * 16) = acc;
   __syncthreads();
-  for (int e = threadIdx.x; e < MT * 64; e += kFewWaves * 64) {
-    const int i = e >> 6, l = e & 63;
-    f32x4_t s = red[0][i][l];
+  if (threadIdx.x >= 256) return;
+  // output (m, n) is value n % 4 of lane 16 (n / 4) + m
+  const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
+  const char* r = smem + (16 * (n >> 2) + m) * 16 + (n & 3) * 4;
+  float sum = *(const float*)r;
 #pragma unroll
-    for (int w = 1; w < kFewWaves; ++w) s += red[w][i][l];
-    const int64_t m = i * 16 + (l & 15);
-    if (m >= g.M) continue;
-    const int64_t nn = n0 + 4 * (l >> 4);
-    O* o = (O*)g.out + m * g.ldo + nn;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (nn + j < g.N) put(o + j, s[j]);
-  }
+  for (int w = 1; w < W; ++w) sum += *(const float*)(r + w * kFewRing);
+  if (m < g.M && n <= nb) put((O*)g.out + m * g.ldo + n0 + n, sum);
 }
 
 // ---------------------------------------------------------------- small tiles
@@ -474,7 +498,9 @@ __global__ __launch_bounds__(256, (Big<MI, NS>::WGS)) void mx_big_kernel(MxGemmA
 
 // The kernel by the number of tiles, measured with float32 results (us,
 // M x N x K; the sides of each border):
-//   few rows:    1 x 5632 x 2048 4.0
+//   few rows:    up to 16: 1 x 5632 x 2048 3.0, 32 x 64 tiles 3.6; 16 x
+//                16384 x 4096 7.8, 64 x 64 7.2 (from a graph, as the few
+//                rows' other figures)
 //   32 x 64:     up to 128 tiles of 64 x 64, which leave CUs without one:
 //                256 x 2048 x 2048 (128 tiles) 5.5, 64 x 64 5.8;
 //                256 x 4096 x 2048 (256) 6.5, 64 x 64 6.2
@@ -490,11 +516,10 @@ __global__ __launch_bounds__(256, (Big<MI, NS>::WGS)) void mx_big_kernel(MxGemmA
 //                on random operands, run at 6.0 PFLOP/s here (power).
 template <typename O>
 hipError_t launch(const MxGemmArgs& g, hipStream_t s) {
-  if (g.M <= 64) {
+  if (g.M <= 16) {
     const unsigned grid = (unsigned)((g.N + 15) / 16);
-    if (g.M <= 16) mx_few_kernel<1, O><<<grid, kFewWaves * 64, 0, s>>>(g);
-    else if (g.M <= 32) mx_few_kernel<2, O><<<grid, kFewWaves * 64, 0, s>>>(g);
-    else mx_few_kernel<4, O><<<grid, kFewWaves * 64, 0, s>>>(g);
+    if (g.K <= 4096) mx_few_kernel<4, O><<<grid, 256, 4 * kFewRing, s>>>(g);
+    else mx_few_kernel<8, O><<<grid, 512, 8 * kFewRing, s>>>(g);
     return hipGetLastError();
   }
   const int64_t m32 = (g.M + 31) / 32, n64 = (g.N + 63) / 64, t64 = (g.M + 63) / 64 * n64;

@@ -63,6 +63,12 @@ class SparseMoE:
                              f"{t.dtype} {tuple(t.shape)} on {t.device}")
         return t.data_ptr()
 
+    @staticmethod
+    def _new(rows: int, cols: int, dtype: torch.dtype, device) -> Tuple[torch.Tensor, int]:
+        # (0.3 us less of the host's time than torch.empty of a shape)
+        t = torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+        return t, t.data_ptr()
+
     def _weight(self, w: Weight, device, what: str) -> Tuple[int, Optional[int]]:
         E, F, d = self.n_experts, self.d_ff, self.d
         if self.weights == "bf16":
@@ -109,18 +115,19 @@ class SparseMoE:
             pn = self._plain(n_tokens, tuple(n_tokens.shape), torch.int32, dev, "n_tokens")
             if n_tokens.numel() != 1:
                 raise ValueError("n_tokens must have one element")
+        k = self.top_k
         if y is None:
-            y = torch.empty((T, self.d), dtype=torch.float32, device=dev)
-        py = self._plain(y, (T, self.d), torch.float32, dev, "y")
+            y, py = self._new(T, self.d, torch.float32, dev)
+        else:
+            py = self._plain(y, (T, self.d), torch.float32, dev, "y")
         ids = probs = pi = pp = None
-        if return_routing or routing is not None:
-            if routing is None:
-                ids = torch.empty((T, self.top_k), dtype=torch.int32, device=dev)
-                probs = torch.empty((T, self.top_k), dtype=torch.float32, device=dev)
-            else:
-                ids, probs = routing
-            pi = self._plain(ids, (T, self.top_k), torch.int32, dev, "ids")
-            pp = self._plain(probs, (T, self.top_k), torch.float32, dev, "probs")
+        if routing is not None:
+            ids, probs = routing
+            pi = self._plain(ids, (T, k), torch.int32, dev, "ids")
+            pp = self._plain(probs, (T, k), torch.float32, dev, "probs")
+        elif return_routing:
+            ids, pi = self._new(T, k, torch.int32, dev)
+            probs, pp = self._new(T, k, torch.float32, dev)
         if T > 0:
             nb = self.workspace_bytes(T)
             # torch's allocations are 512-byte aligned

@@ -116,6 +116,28 @@ def test_many_neurons(T, d, F, E, k, gated, weights):
     check(layer, x, wr, ws, layer.forward(x, wr, *ws, return_routing=True))
 
 
+@pytest.mark.parametrize("weights", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("T,d,F,E,k,gated", [
+    # an expert's tokens and neurons over several workgroups: all in one expert,
+    # uneven blocks, ranges of neurons that the last one cuts
+    (128, 128, 2080, 1, 1, True), (33, 256, 4128, 2, 1, True), (200, 128, 2048, 3, 2, False),
+    (17, 128, 5632, 1, 1, True), (1, 128, 4128, 8, 2, True), (256, 128, 96, 1, 1, True),
+    (70, 128, 64, 2, 2, True)])
+def test_few_experts(T, d, F, E, k, gated, weights):
+    print(T, d, F, E, k, gated, weights, flush=True)
+    layer, x, wr, ws = make(T, d, F, E, k, gated, weights, active=0.3)
+    out = layer.forward(x, wr, *ws, return_routing=True)
+    check(layer, x, wr, ws, out)
+    assert torch.equal(layer.forward(x, wr, *ws), out[0])
+    # the same call with fewer valid tokens than it was planned for
+    n = torch.tensor([T // 3 + 1], dtype=torch.int32, device="cuda")
+    m = int(n)
+    y = torch.full((T, d), 7.0, device="cuda")
+    layer.forward(x, wr, *ws, y=y, n_tokens=n, routing=(out[1], out[2]))
+    assert (y[m:] == 7).all()
+    check(layer, x[:m], wr, ws, (y[:m], out[1][:m], out[2][:m]))
+
+
 @pytest.mark.parametrize("normalize", [True, False])
 @pytest.mark.parametrize("T,E,k", [(1, 2, 1), (1, 64, 32), (1, 65, 2), (1, 127, 31), (1, 128, 32),
                                    (1, 129, 32), (1, 300, 5), (1, 1024, 32), (3, 1024, 32),

@@ -55,9 +55,9 @@ Layout layout(const MoeArgs& a) {
   L.keys = take(T * a.E * 8);
   L.expert = take(pairs * 4);
   L.weight = take(pairs * 4);
-  L.on = take((size_t)a.Y * a.F);
+  L.on = take((size_t)a.zh * a.Y * a.F);
   L.h = take(pairs * a.F * 4);
-  L.part = take(pairs * a.d * 4);
+  L.part = take((size_t)a.split * pairs * a.d * 4);
   L.total = o;
   return L;
 }

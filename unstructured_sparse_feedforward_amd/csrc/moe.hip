@@ -453,7 +453,7 @@ __device__ __forceinline__ int unit_pairs(const MoeArgs& a, int unit, Lists& ls,
 template <bool MX, bool GATED, int NTK, bool XL>
 __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, const Lists& ls,
                                      const Rows& wg, const Rows& wu, int j0, int nbe, int n,
-                                     int p0, int place, uint8_t* any) {
+                                     int p0, int place, bool more, uint8_t* any) {
   constexpr int MT = kBlocks<MX>;
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
@@ -482,8 +482,8 @@ __device__ __forceinline__ void pass(const MoeArgs& a, Shared<MX, NTK>& sh, cons
       for (int q = 0; q < 4; ++q)
         if (s[q] > 0.0f) sh.on[j + q] = any[j + q] = 1;   // every writer stores the same
       // non-gated: h is z itself; gated: a neuron that only another pass
-      // finds active has h = 0 here
-      if (!GATED || n > 16 * NTK || p0 > 0) {
+      // of the workgroup finds active has h = 0 here
+      if (!GATED || more) {
         float* o = a.h + (int64_t)(j0 + j) * P + place + p0 + tk;
 #pragma unroll
         for (int q = 0; q < 4; ++q) o[q * P] = !GATED && s[q] > 0.0f ? s[q] : 0.0f;
@@ -614,7 +614,7 @@ __global__ __launch_bounds__(NT, NTK == 1 ? 4 : 2) void moe_hidden_kernel(MoeArg
     Shared<MX, NTK> s;
   } sh;
   const int tid = threadIdx.x;
-  const int slice = blockIdx.x, unit = blockIdx.y;
+  const int slice = blockIdx.x, unit = blockIdx.y, z = blockIdx.z;
   int e, n = 1, place;
   if (tid < kSlice<MX>) any[tid] = 0;
   if (ONE) {
@@ -624,7 +624,7 @@ __global__ __launch_bounds__(NT, NTK == 1 ? 4 : 2) void moe_hidden_kernel(MoeArg
     __syncthreads();
   } else {
     n = unit_pairs(a, unit, ls, &e, &place);
-    if (n == 0) return;
+    if (n <= 16 * NTK * z) return;
   }
 
   const int j0 = slice * a.nb;
@@ -635,16 +635,17 @@ __global__ __launch_bounds__(NT, NTK == 1 ? 4 : 2) void moe_hidden_kernel(MoeArg
   const Rows wg = {(const uint8_t*)a.wg + row0 * pitch, MX ? a.sg + row0 * 4 : nullptr, pitch, gp};
   const Rows wu = {GATED ? (const uint8_t*)a.wu + row0 * pitch : nullptr,
                    MX && GATED ? a.su + row0 * 4 : nullptr, pitch, gp};
-  for (int p0 = 0; p0 < n; p0 += 16 * NTK) {
+  const bool more = n > 16 * NTK * a.zh;
+  for (int p0 = 16 * NTK * z; p0 < n; p0 += 16 * NTK * a.zh) {
     if (MX && n - p0 <= kStaged)
-      pass<MX, GATED, 1, MX>(a, sh.s1, ls, wg, wu, j0, nbe, n, p0, place, any);
+      pass<MX, GATED, 1, MX>(a, sh.s1, ls, wg, wu, j0, nbe, n, p0, place, more, any);
     else if (n - p0 <= 16)
-      pass<MX, GATED, 1, false>(a, sh.s1, ls, wg, wu, j0, nbe, n, p0, place, any);
+      pass<MX, GATED, 1, false>(a, sh.s1, ls, wg, wu, j0, nbe, n, p0, place, more, any);
     else
-      pass<MX, GATED, NTK, false>(a, sh.s, ls, wg, wu, j0, nbe, n, p0, place, any);
+      pass<MX, GATED, NTK, false>(a, sh.s, ls, wg, wu, j0, nbe, n, p0, place, more, any);
     __syncthreads();
   }
-  if (tid < nbe) a.on[(int64_t)unit * a.F + j0 + tid] = any[tid];
+  if (tid < nbe) a.on[((int64_t)z * a.Y + unit) * a.F + j0 + tid] = any[tid];
 }
 
 // ---------------------------------------------------------------- down
@@ -676,19 +677,25 @@ __global__ __launch_bounds__(NT, 2) void moe_down_kernel(MoeArgs a) {
   const int wave = wave_id();
   const int kq = lane >> 4, l15 = lane & 15;
   const int chunk = blockIdx.x, unit = blockIdx.y;
-  const uint8_t* on = a.on + (int64_t)unit * a.F;
-  // the active flags of the neurons from s0 on, 8 x kFl a thread (F is a
-  // multiple of 32)
+  // the workgroup's blocks of 16 tokens, p_first and every 16 zd from there
+  // on, and its range of neurons
+  const int p_first = ((int)blockIdx.z & (a.zd - 1)) * 16;
+  const int range = (int)blockIdx.z >> (31 - __builtin_clz(a.zd));
+  const int f_begin = range * a.fs, f_end = min(a.F, f_begin + a.fs);
+  // the flags of the neurons active for the tokens at p0, from s0 on, 8 x kFl
+  // a thread (F and fs are multiples of 32)
   uint64_t fl[kFl];
-  auto flags = [&](int s0) {
+  auto flags = [&](int p0, int s0) {
+    const int z = (p0 >> (a.ntk + 3)) & (a.zh - 1);   // ntk is 1 or 2
+    const uint8_t* on = a.on + ((int64_t)z * a.Y + unit) * a.F;
     const int f0 = s0 + tid * (8 * kFl);
 #pragma unroll
-    for (int v = 0; v < kFl; ++v) fl[v] = f0 < a.F ? *(const uint64_t*)(on + f0 + 8 * v) : 0;
+    for (int v = 0; v < kFl; ++v) fl[v] = f0 < f_end ? *(const uint64_t*)(on + f0 + 8 * v) : 0;
   };
-  flags(0);   // (a unit without tokens has none that mean anything)
+  flags(p_first, f_begin);   // (a unit without tokens has none that mean anything)
   int e, place;
   const int n = unit_pairs(a, unit, ls, &e, &place);
-  if (n == 0) return;
+  if (n <= p_first) return;
   const int ncol = min(COLS, a.d - chunk * COLS);   // (the last chunk of codes may be half)
   const int col = chunk * COLS + min(CPL * l15, ncol - CPL);
   const int64_t pitch = MX ? a.d / 2 : (int64_t)a.d * 2;
@@ -699,12 +706,12 @@ __global__ __launch_bounds__(NT, 2) void moe_down_kernel(MoeArgs a) {
   // (its scales: one or two 128-column groups)
   const uint8_t* sp = MX ? a.sd + (int64_t)e * a.F * 4 + (col >> 7) * gp + ((col >> 5) & 3) : nullptr;
 
-  for (int p0 = 0; p0 < n; p0 += 16) {
+  for (int p0 = p_first; p0 < n; p0 += 16 * a.zd) {
     const int nt = min(n - p0, 16);
     f32x4_t acc[CPL] = {};
-    for (int s0 = 0; s0 < a.F; s0 += kSeg) {
+    for (int s0 = f_begin; s0 < f_end; s0 += kSeg) {
       // list the segment's active neurons
-      if (s0 || p0) flags(s0);
+      if (s0 > f_begin || p0 > p_first) flags(p0, s0);
       const int f0 = s0 + tid * (8 * kFl);
       int mine = 0;
 #pragma unroll
@@ -829,7 +836,8 @@ __global__ __launch_bounds__(NT, 2) void moe_down_kernel(MoeArgs a) {
         for (int w = 1; w < kWaves / 2; ++w) s[q] += red[w][q0 + q][l][r];
       }
       if (tk < nt && c < ncol)
-        *(f32x4_t*)(a.part + (int64_t)ls.pair[p0 + tk] * a.d + chunk * COLS + c) = s;
+        *(f32x4_t*)(a.part + ((int64_t)range * a.T * a.k + ls.pair[p0 + tk]) * a.d +
+                    chunk * COLS + c) = s;
     }
     __syncthreads();
   }
@@ -847,13 +855,18 @@ __global__ __launch_bounds__(64) void moe_sum_kernel(MoeArgs a) {
   const float* q = a.part + (int64_t)t * a.k * a.d + c;
   f32x4_t s = {};
 #pragma unroll 8
-  for (int r = 0; r < a.k; ++r) s += *(const f32x4_t*)(q + (int64_t)r * a.d) * p[r];
+  for (int r = 0; r < a.k; ++r) {
+    f32x4_t v = *(const f32x4_t*)(q + (int64_t)r * a.d);
+    for (int i = 1; i < a.split; ++i)
+      v += *(const f32x4_t*)(q + ((int64_t)i * a.T * a.k + r) * a.d);
+    s += v * p[r];
+  }
   *(f32x4_t*)(a.y + (int64_t)t * a.d + c) = s;
 }
 
 template <bool MX, bool GATED>
 hipError_t launch_hidden(const MoeArgs& a, hipStream_t s) {
-  const dim3 grid((a.F + a.nb - 1) / a.nb, a.Y);
+  const dim3 grid((a.F + a.nb - 1) / a.nb, a.Y, a.zh);
   constexpr size_t lds = kWaves * kRingBytes<MX>;
   if (a.one) moe_hidden_kernel<MX, GATED, true, 1><<<grid, NT, lds, s>>>(a);
   else if (a.ntk == 1) moe_hidden_kernel<MX, GATED, false, 1><<<grid, NT, lds, s>>>(a);
@@ -886,6 +899,22 @@ void moe_plan(bool mx, MoeArgs* a) {
   a->ntk = pairs <= 12 * a->E ? 1 : 2;
   const int cols = 16 * (mx ? kCpl<true> : kCpl<false>);
   a->chunks = (a->d + cols - 1) / cols;
+  // Where workgroups are few, an expert's blocks of tokens go to several, and
+  // in the down kernel ranges of at least 1024 neurons do (their outputs are
+  // added in the sum kernel): 128 tokens to one bf16 expert of 2048 x 5632 88
+  // us, without 374; one token to 2 of 8 28.8, without 31.7. Ranges up to
+  // 256 workgroups (64 tokens over 16 experts of 5632 neurons: 99.1 us, up to
+  // 512 99.9), with several blocks of tokens 512 (128 tokens of 2 over 4
+  // experts of 2816: 107.8, up to 256 112.7).
+  int blocks = 1;      // of 16 tokens, the mean of an expert, up to a power of two
+  while (!a->by_pair && 16 * blocks * a->E < pairs) blocks *= 2;
+  a->zh = a->Y * ((a->F + nb - 1) / nb) < 1024 ? (blocks + a->ntk - 1) / a->ntk : 1;
+  a->zd = a->chunks * a->Y < 512 ? blocks : 1;
+  a->split = 1;
+  while (a->chunks * a->Y * a->zd * a->split < (blocks > 1 ? 512 : 256) &&
+         a->F / (2 * a->split) >= 1024)
+    a->split *= 2;
+  a->fs = ((a->F + a->split - 1) / a->split + 31) / 32 * 32;
 }
 
 hipError_t launch_moe(bool mx, const MoeArgs& a, hipStream_t s) {
@@ -901,7 +930,7 @@ hipError_t launch_moe(bool mx, const MoeArgs& a, hipStream_t s) {
   e = mx ? (gated ? launch_hidden<true, true>(a, s) : launch_hidden<true, false>(a, s))
          : (gated ? launch_hidden<false, true>(a, s) : launch_hidden<false, false>(a, s));
   if (e != hipSuccess) return e;
-  const dim3 grid(a.chunks, a.Y);
+  const dim3 grid(a.chunks, a.Y, a.zd * a.split);
   if (mx) moe_down_kernel<true><<<grid, NT, 0, s>>>(a);
   else moe_down_kernel<false><<<grid, NT, 0, s>>>(a);
   e = hipGetLastError();

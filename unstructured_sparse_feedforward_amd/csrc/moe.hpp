@@ -31,20 +31,24 @@ struct MoeArgs {
   int nb;                    // neurons a workgroup of the hidden kernel
   int chunks;                // column chunks of the down kernel
   int ntk;                   // blocks of 16 tokens a pass of the hidden kernel
+  int zh;                    // workgroups that share out a unit's passes there
+  int zd;                    // workgroups that share out its blocks of 16 tokens in the down
+                             // kernel (both powers of two)
+  int split, fs;             // ranges of neurons there, of fs each
   // workspace
   long long* keys;           // [T, E] the logits as ordered integers
   int32_t* expert;           // [T k] the experts of each token by rank
   float* weight;             // [T k] their softmax weights
-  uint8_t* on;               // [Y, F] neuron active for one of its tokens
+  uint8_t* on;               // [zh, Y, F] neuron active for one of the passes' tokens
   float* h;                  // [F, T k] hidden activations, the pairs in the order of their
                              // experts: those of a unit's tokens side by side
-  float* part;               // [T k, d] output of each pair
+  float* part;               // [split, T k, d] output of each pair, by ranges of neurons
   float* y;                  // [T, d]
   int32_t* ids;              // [T, k] (nullable)
   float* probs;              // [T, k] (nullable)
 };
 
-// fills Y .. ntk from the sizes
+// fills Y .. fs from the sizes
 void moe_plan(bool mx, MoeArgs* a);
 hipError_t launch_moe(bool mx, const MoeArgs& a, hipStream_t s);
 

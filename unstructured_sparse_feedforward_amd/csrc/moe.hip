@@ -14,7 +14,8 @@
 //           z for all of the expert's tokens, and u only for the neurons that
 //           are active (z > 0) for one of them, as in the rest of the library;
 //   down    a workgroup has an expert and a chunk of y's columns, and reads
-//           those of the active neurons' rows;
+//           those of the active neurons' rows (in both, with few experts, for
+//           a share of the expert's tokens, and here of its neurons);
 //   sum     the token's k outputs, weighted, in the order of their ranks (no
 //           float atomics: results repeat bit for bit). A launch of its own,
 //           2.5 to 4 us: summing in the down kernel's last workgroup a token

@@ -418,7 +418,10 @@ sffn_status sffn_check(sffn_handle* h, hipStream_t stream);
  *           from K on are 0
  *   scales  [Kp / 128, R, 4] bytes: byte b of (g, r) is the scale's
  *           exponent plus 127 for elements 128 g + 32 b .. + 31 of row r;
- *           255 makes those elements NaN
+ *           255 makes those elements NaN. The bytes of blocks that lie
+ *           from K on are 0: sffn_mx_quantize writes them so, and scales
+ *           made elsewhere must have them so (a 255 there makes the row's
+ *           products NaN)
  * sffn_mx_bytes gives the two sizes. The calls take no handle: they run on
  * the current device, on the caller's stream, allocate nothing and keep no
  * state, so calls on different streams may overlap. Sizes: R up to 2^27

@@ -59,7 +59,7 @@ def values(codes, exps):
 
 def pack(codes, exps):
     """The library's layout: (codes [R, Kp / 2], scales [Kp / 128, R, 4]),
-    unspecified scale bytes of the padding as 0."""
+    the scale bytes of blocks past K as 0."""
     R, K = codes.shape
     Kp = -(-K // 128) * 128
     c = np.zeros((R, Kp), np.uint8)

@@ -265,3 +265,42 @@ def test_gate_preactivations_into_twell():
     m = gu.valid_slots(tw)
     rows = np.nonzero(m)[0]
     assert np.array_equal(tw["val"][m], zc[rows, tw["idx"][m]])
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("R,K", [(3, 1), (17, 33), (5, 200), (40, 300), (70, 1185)])
+def test_padding_is_written_as_zero(R, K, transposed):
+    """Codes from K on and the scale bytes of blocks there, whatever the
+    memory held."""
+    out = sffn.mx_empty(R, K, "cuda")
+    out.codes.fill_(0xFF)
+    out.scales.fill_(0xFF)
+    x = _rand((R, K), R + K)
+    sffn.mx_quantize(x.t().contiguous() if transposed else x, transposed=transposed, out=out)
+    c, s = mo.pack(*mo.quantize(x.double().cpu().numpy()))
+    assert np.array_equal(out.codes.cpu().numpy(), c)
+    assert np.array_equal(out.scales.cpu().numpy(), s)
+
+
+@pytest.mark.parametrize("fill", [255, 254, 127])
+@pytest.mark.parametrize("M,N,K", [
+    # few rows, with K over four and eight waves; 32 x 64 and 64 x 64 tiles;
+    # 128 x 256 and 256 x 256 tiles; one, two and three blocks of padding
+    (1, 70, 1), (5, 40, 200), (16, 33, 4160), (100, 200, 300), (40, 70, 4129), (1000, 1100, 513),
+    (2500, 2000, 300), (2047, 2305, 96), (3841, 3700, 1100), (4096, 4096, 2049)])
+def test_scales_past_the_last_column_do_not_matter(M, N, K, fill):
+    """Matrices whose scale bytes of the blocks past K are NaN's, the
+    largest and 1, as memory that nobody cleared may hold: the same product
+    and the same values."""
+    def other(q):
+        s = q.scales.clone()
+        live = -(-K // 32) - (q.scales.shape[0] - 1) * 4
+        assert live < 4
+        s[-1, :, live:] = fill
+        return sffn.MXTensor(q.codes.clone(), s, q.rows, q.cols)
+    a, b = sffn.mx_quantize(_rand((M, K), 1)), sffn.mx_quantize(_rand((N, K), 2))
+    want = sffn.mx_matmul(a, b)
+    assert torch.isfinite(want).all()
+    for p, q in ((other(a), b), (a, other(b)), (other(a), other(b))):
+        assert torch.equal(sffn.mx_matmul(p, q), want)
+    assert torch.equal(sffn.mx_dequantize(other(a)), sffn.mx_dequantize(a))

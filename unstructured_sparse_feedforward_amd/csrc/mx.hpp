@@ -7,7 +7,10 @@
 //          in byte k / 2, the even one in the low nibble;
 //   scales [Kp / 128, R, 4] bytes: byte b of (g, r) is the scale exponent
 //          plus 127 (255: NaN) of the block at k = 128 g + 32 b of row r.
-// The padding elements' codes are 0. The scales of consecutive rows are
+// The padding elements' codes are 0, and so are the scale bytes of blocks that
+// are all padding. (The product multiplies those too. Masking their scales in
+// its kernels cost 1 to 7% of every product: 8192 x 8192 x 8192 256 to 269 us,
+// 1 x 5632 x 2048 3.27 to 3.38.) The scales of consecutive rows are
 // consecutive dwords, so that a GEMM fetches those of a tile's rows for one
 // 128-wide k step as one run, and a lane has the four of its row in a
 // register (the scaled MFMAs select a byte of it).

@@ -28,7 +28,10 @@ class MXTensor:
     elements along a row. ``codes`` [rows, Kp / 2] and ``scales`` [Kp / 128,
     rows, 4] are uint8 tensors, Kp = cols rounded up to 128; include/sffn.h
     gives the layout. Made by :func:`mx_quantize` or :func:`mx_empty`, or
-    from codes and scales kept elsewhere (contiguous, on one GPU)."""
+    from codes and scales kept elsewhere (contiguous, on one GPU; the codes
+    of elements from cols on are 0). The scale bytes of blocks that lie from
+    cols on have to be 0 for a product: here those of ``scales`` are cleared,
+    on its device's current stream."""
 
     __slots__ = ("rows", "cols", "device", "_codes", "_scales", "_buf", "_pc", "_ps")
 
@@ -42,6 +45,9 @@ class MXTensor:
                 raise ValueError("codes and scales must be contiguous uint8 tensors")
         if not codes.is_cuda or codes.device != scales.device:
             raise ValueError("codes and scales must be on one GPU")
+        live = -(-cols // 32) % 4
+        if live:
+            scales[-1, :, live:].zero_()
         self.rows, self.cols, self.device = rows, cols, codes.device
         self._codes, self._scales, self._buf = codes, scales, None
         self._pc, self._ps = codes.data_ptr(), scales.data_ptr()

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import moe_pins as mp
 import unstructured_sparse_feedforward_amd as sffn
 from oracle import moe_oracle as mo
 
@@ -307,3 +308,24 @@ def test_refusals_on_the_gpu():
         with pytest.raises(sffn.SffnError):
             f()
     assert layer.forward(x[:0], wr, *ws).shape == (0, 256)
+
+
+@pytest.mark.parametrize("weights", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("T,d,F", [(1, 128, 32), (4, 128, 128), (5, 256, 96), (16, 128, 64),
+                                   (40, 256, 256), (200, 128, 128)])
+def test_h_enters_the_down_product_with_24_bits(T, d, F, gated, weights):
+    """Results that float32 holds exactly and that need every bit of h."""
+    x, gate, up, down, y = mp.hidden_24_bits(T, d, F, gated, seed=T + d)
+    bf = lambda a: torch.from_numpy(a).cuda().to(torch.bfloat16)
+    # two experts; the second, which these are, has the larger logit
+    ws = [None if w is None else torch.stack([bf(np.flip(w, 0).copy()), bf(w)])
+          for w in (gate, up, down)]
+    wr = torch.zeros(2, d, device="cuda", dtype=torch.bfloat16)
+    wr[1, 3] = 1.0
+    if weights == "mxfp4":
+        ws = [None if w is None else sffn.mx_quantize(w.view(2 * F, d)) for w in ws]
+    layer = sffn.SparseMoE(d, F, 2, 1, gated=gated, weights=weights)
+    out, ids, probs = layer.forward(bf(x), wr, *ws, return_routing=True)
+    assert (ids == 1).all() and (probs == 1).all()
+    assert np.array_equal(out.double().cpu().numpy(), y)

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import moe_pins as mp
 import unstructured_sparse_feedforward_amd as sffn
 from oracle import moe_oracle as mo
 from unstructured_sparse_feedforward_amd import binding as B
@@ -132,3 +133,26 @@ def test_python_refusals():
     m = sffn.SparseMoE(256, 96, 8, 2)
     with pytest.raises(ValueError, match="GPU"):
         m.forward(torch.zeros(1, 256, dtype=torch.bfloat16), None, None, None, None)
+
+
+@pytest.mark.parametrize("gated", [True, False])
+def test_pins_tell_the_parts_of_h_apart(gated):
+    """The exact inputs of the GPU tests: three bfloat16 parts of h give
+    their y, two or one do not, for any neuron."""
+    x, gate, up, down, y = mp.hidden_24_bits(7, 128, 96, gated)
+    for w in (x, gate, down) + ((up,) if gated else ()):
+        assert np.array_equal(mp.bf16(w), w)
+    h = x @ gate.T if up is None else (x @ gate.T) * (x @ up.T)
+    assert np.array_equal(h.astype(np.float32), h)      # 24 bits, no rounding
+    oy, *_ = mo.forward(x, np.zeros((1, 128)), gate[None], None if up is None else up[None],
+                        down[None], 1)
+    assert np.array_equal(oy, y)
+    rest, parts = h, []
+    for _ in range(3):
+        parts.append(mp.bf16(rest))
+        rest = rest - parts[-1]
+    assert (rest == 0).all()
+    cols = (down != 0).any(0)
+    for n in (1, 2):
+        assert (sum(parts[:n]) @ down != y)[:, cols].all()
+    assert np.array_equal(sum(parts) @ down, y)

@@ -468,8 +468,10 @@ sffn_status sffn_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int6
  *   y = sum_r p_r ReLU(x W_1,e(r)) W_2,e(r)                      non-gated
  * Only the selected experts' weights are read, the up and down rows only of
  * neurons that are active (strictly z > 0, as everywhere here) for one of
- * the tokens. Logits are summed in 64 bits, so that the choice of experts
- * does not depend on an order of summation; everything else in float32 (h
+ * the tokens. Logits are float64 sums in an order that depends on d alone, so
+ * that a token's experts are the same in every call; the sums are exact
+ * where the products of a logit (zeros aside) lie within a factor of 2^37 /
+ * d of each other, and ties are those of the sums. Everything else is float32 (h
  * enters the down product with its 24 bits, in three bf16 parts). The same
  * call repeats bit for bit; a token's row may differ in its last bits when
  * the other tokens of the call are others.

@@ -1,5 +1,5 @@
 """Inputs of the expert layer for which the results are known exactly, and
-differ if h carries fewer bits than it is said to."""
+differ if the logits or h carry fewer bits than they are said to."""
 import numpy as np
 
 
@@ -40,3 +40,15 @@ def bf16(v):
     b = np.asarray(v, np.float32).view(np.uint32).astype(np.uint64)
     b = (b + 0x7FFF + (b >> 16 & 1)) & 0xFFFF0000
     return b.astype(np.uint32).view(np.float32).astype(np.float64)
+
+
+def near_tie(E, d):
+    """Router rows [E, d] for an x of ones at columns 0 and d - 1 (0
+    elsewhere), exact in bfloat16: the last expert's logit is 2^-40 above
+    the second one's (the first's, if there are two), which a sum in 32 bits
+    does not see; all others' are 0. ids of the two largest."""
+    low, high = (1 if E > 2 else 0), E - 1
+    w = np.zeros((E, d))
+    w[[low, high], 0] = 1.0
+    w[high, d - 1] = 2.0 ** -40
+    return w, [high, low]

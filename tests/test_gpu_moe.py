@@ -329,3 +329,41 @@ def test_h_enters_the_down_product_with_24_bits(T, d, F, gated, weights):
     out, ids, probs = layer.forward(bf(x), wr, *ws, return_routing=True)
     assert (ids == 1).all() and (probs == 1).all()
     assert np.array_equal(out.double().cpu().numpy(), y)
+
+
+# the kernels that route: the hidden kernel (one token, up to 128 experts), the
+# router's with the logits in it (up to 16 experts) and without
+ROUTES = [(1, 2), (1, 16), (1, 17), (1, 64), (1, 65), (1, 128), (1, 129), (1, 1024), (5, 2), (5, 16),
+          (5, 17), (5, 300), (3, 1024)]
+
+
+@pytest.mark.parametrize("d", [128, 640, 8192])
+@pytest.mark.parametrize("T,E", ROUTES)
+def test_logits_in_64_bits(T, E, d):
+    """Two logits that 32 bits do not tell apart: the larger one, of higher
+    index, comes first."""
+    if E * d > 1 << 18:
+        E = (1 << 18) // d      # (the weights stay small)
+    w, want = mp.near_tie(E, d)
+    layer, x, wr, ws = make(T, d, 32, E, 2, True, "bf16")
+    x.zero_()
+    x[:, [0, d - 1]] = 1.0
+    wr.copy_(torch.from_numpy(w))
+    out = layer.forward(x, wr, *ws, return_routing=True)
+    assert out[1].tolist() == [want] * T
+    check(layer, x, wr, ws, out)
+
+
+@pytest.mark.parametrize("T,E", ROUTES)
+def test_logits_are_summed_in_one_order(T, E):
+    """Products too far apart for exact sums: a lane's columns are added in
+    ascending order, whichever kernel routes."""
+    layer, x, wr, ws = make(T, 128, 32, E, 2, True, "bf16")
+    x.zero_()
+    x[:, :3] = 1.0
+    wr.zero_()
+    wr[:, 0] = -1.0
+    wr[0, :3] = torch.tensor([1.0, 2.0 ** 60, -2.0 ** 60])      # (1 + 2^60) - 2^60 = 0
+    wr[E - 1, :3] = torch.tensor([2.0 ** 60, -2.0 ** 60, 1.0])  # 1
+    _, ids, _ = layer.forward(x, wr, *ws, return_routing=True)
+    assert ids.tolist() == [[E - 1, 0]] * T

@@ -156,3 +156,14 @@ def test_pins_tell_the_parts_of_h_apart(gated):
     for n in (1, 2):
         assert (sum(parts[:n]) @ down != y)[:, cols].all()
     assert np.array_equal(sum(parts) @ down, y)
+
+
+@pytest.mark.parametrize("E", [2, 16, 64])
+def test_near_tie_needs_64_bits(E):
+    w, ids = mp.near_tie(E, 128)
+    x = np.zeros((1, 128))
+    x[0, [0, 127]] = 1.0
+    assert np.array_equal(mp.bf16(w), w)
+    assert mo.route(x, w, 2, True)[0].tolist() == [ids]
+    low = (w.astype(np.float32) @ x[0].astype(np.float32)).astype(np.float64)
+    assert sorted(range(E), key=lambda e: (-low[e], e))[:2] == ids[::-1]

@@ -58,9 +58,12 @@ __device__ __forceinline__ double key_value(long long k) {
 
 // ---------------------------------------------------------------- router
 
-// The logits, a wave an expert and token. They are summed in 64 bits: two
-// experts' then compare as their exact values do (the product of two bf16
-// values has 16 bits), whatever the order of summation.
+// The logits, a wave an expert and token, summed in 64 bits in an order that
+// depends on d alone (a lane's columns ascending, then the lanes pairwise), so
+// that a token's choice of experts is the same in every call. The product of
+// two bf16 values has 16 bits: the sums are exact, and logits compare as their
+// exact values do, where the products of a logit (zeros aside) lie within a
+// factor of 2^37 / d of each other. Beyond that ties are those of the sums.
 __device__ __forceinline__ double logit(const MoeArgs& a, int t, int e) {
   const int lane = threadIdx.x & 63;
   const uint16_t* x = a.x + (int64_t)t * a.d;

@@ -367,3 +367,29 @@ def test_logits_are_summed_in_one_order(T, E):
     wr[E - 1, :3] = torch.tensor([2.0 ** 60, -2.0 ** 60, 1.0])  # 1
     _, ids, _ = layer.forward(x, wr, *ws, return_routing=True)
     assert ids.tolist() == [[E - 1, 0]] * T
+
+
+@pytest.mark.parametrize("active", [0.1, 0.8])
+@pytest.mark.parametrize("T,d,F,E,k,gated,weights", [
+    # the longest slices (64 neurons of bf16, 128 of codes): every wave a tile
+    # of its own, and with eight in ten active more than 64 neurons of codes in
+    # the up product. One block of 16 tokens a pass, the last slice cut (32 of
+    # 64, 96 of 128) and whole, d of one step and of many
+    (64, 128, 1120, 128, 8, True, "bf16"), (64, 128, 1120, 128, 8, True, "mxfp4"),
+    (64, 128, 1152, 128, 8, True, "bf16"), (64, 128, 1152, 128, 8, True, "mxfp4"),
+    (64, 128, 1120, 128, 8, False, "bf16"), (64, 128, 1120, 128, 8, False, "mxfp4"),
+    # a single token
+    (1, 128, 4064, 32, 32, True, "bf16"), (1, 128, 4064, 32, 32, True, "mxfp4"),
+    (1, 1024, 1056, 32, 32, True, "bf16"), (1, 1024, 4096, 32, 32, True, "mxfp4"),
+    # a unit for each pair of several tokens
+    (3, 128, 1440, 128, 32, True, "bf16"), (3, 128, 1440, 128, 32, True, "mxfp4"),
+    # two blocks a pass, one pass and several
+    (128, 128, 1120, 128, 16, True, "bf16"), (128, 128, 1120, 128, 16, True, "mxfp4"),
+    (200, 128, 4064, 32, 4, True, "bf16"), (200, 128, 4064, 32, 4, True, "mxfp4"),
+    (128, 128, 1152, 128, 16, False, "mxfp4")])
+def test_longest_slices(T, d, F, E, k, gated, weights, active):
+    print(T, d, F, E, k, gated, weights, active, flush=True)
+    layer, x, wr, ws = make(T, d, F, E, k, gated, weights, active=active)
+    out = layer.forward(x, wr, *ws, return_routing=True)
+    check(layer, x, wr, ws, out)
+    assert torch.equal(layer.forward(x, wr, *ws), out[0])

@@ -380,7 +380,7 @@ def test_logits_are_summed_in_one_order(T, E):
     (64, 128, 1120, 128, 8, False, "bf16"), (64, 128, 1120, 128, 8, False, "mxfp4"),
     # a single token
     (1, 128, 4064, 32, 32, True, "bf16"), (1, 128, 4064, 32, 32, True, "mxfp4"),
-    (1, 1024, 1056, 32, 32, True, "bf16"), (1, 1024, 4096, 32, 32, True, "mxfp4"),
+    (1, 1024, 4064, 32, 32, True, "bf16"), (1, 1024, 4096, 32, 32, True, "mxfp4"),
     # a unit for each pair of several tokens
     (3, 128, 1440, 128, 32, True, "bf16"), (3, 128, 1440, 128, 32, True, "mxfp4"),
     # two blocks a pass, one pass and several

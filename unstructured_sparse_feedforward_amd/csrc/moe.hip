@@ -883,18 +883,31 @@ hipError_t launch_hidden(const MoeArgs& a, hipStream_t s) {
 void moe_plan(bool mx, MoeArgs* a) {
   const int pairs = a->T * a->k;
   a->one = a->T == 1 && a->E <= kOneE;
-  // units of the fewer of pairs and experts (8 tokens of 6 over 64 experts
-  // 78 us, with a unit for every expert 82; 4 tokens 60.8, 58.5)
+  // Units of the fewer of pairs and experts: of 6 of 64 bf16 experts of 2048 x
+  // 1408, 2, 4 and 8 tokens take 41.2, 53.1 and 75.7 us, with a unit for every
+  // expert 43.5, 56.8 and 78.7; of 8 of 128 4-bit ones of 2048 x 768, 2, 8 and 15
+  // tokens 31.5, 43.0 and 60.5, and 36.2, 46.3 and 61.8.
   a->by_pair = pairs < a->E || a->one;
   a->Y = a->by_pair ? pairs : a->E;
   const int least = mx ? 32 : 16;
   int nb = mx ? kSlice<true> : kSlice<false>;
-  // As many neurons a workgroup as leave this many workgroups: with bf16 eight
-  // a CU (64 tokens over 16 experts: 100 us, with four 104.5), two for the few
-  // experts of one token (28.5, 30.8 .. 32); codes, a quarter of the bytes a
-  // workgroup, four (32 tokens over 64 experts: 81, with eight 86.8).
-  const int enough = mx ? 1024 : a->T == 1 ? 512 : 2048;
-  while (nb > least && (int64_t)a->Y * ((a->F + nb - 1) / nb) < enough) nb /= 2;
+  // Neurons a workgroup: the most (64 of bf16, 128 of codes) where that leaves
+  // eight workgroups a CU, with codes, a quarter of the bytes, four (bf16: 64
+  // tokens over 16 experts of 5632 neurons 142 us, by four a CU 146; codes: 32
+  // tokens over 64 experts 81, by eight 86.8). Else half as many, and a quarter
+  // only where half leaves less than two workgroups a CU, so that x and the
+  // start of the rings are paid for less often (4 tokens of 6 over 64 experts:
+  // bf16 32 neurons 53.1, 16 58.6, 64 55.5; codes 64 neurons 39.6, 32 43.0; one
+  // token to 8 of 32 experts of 2816 neurons: 32 neurons 41.1, 16 46.5; to 4 of
+  // 16, d = 4096: 16 43.2, 32 46.5). Several tokens' long rows keep the first
+  // border for the quarter as well (16 tokens of 2 over 16 bf16 experts of 2816
+  // neurons: d = 4096 124 us, by the second border 130; d = 2560 89.5, 84.7; 40 of
+  // 4 over 28 4-bit ones of 1440, d = 3584: 81.7, 84.6).
+  const int longest = nb, most = mx ? 1024 : 2048;
+  const int fewest = a->d >= 3584 && !a->one ? most : 512;
+  while (nb > least &&
+         (int64_t)a->Y * ((a->F + nb - 1) / nb) < (nb == longest ? most : fewest))
+    nb /= 2;
   a->nb = nb;
   // Two blocks of 16 tokens a pass where the experts have more than that: a
   // mean of 12 tokens costs the same either way (96 tokens of 8 over 64 bf16

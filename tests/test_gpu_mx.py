@@ -304,3 +304,23 @@ def test_scales_past_the_last_column_do_not_matter(M, N, K, fill):
     for p, q in ((other(a), b), (a, other(b)), (other(a), other(b))):
         assert torch.equal(sffn.mx_matmul(p, q), want)
     assert torch.equal(sffn.mx_dequantize(other(a)), sffn.mx_dequantize(a))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [
+    # 8 to 16 rows of many columns: the borders at 8 rows, at K = 2048 and at
+    # 224 and 448 tiles of 64 columns (7/8 of one and two rounds of the CUs), the
+    # last one cut; 320 tiles do not fill theirs
+    (7, 14336, 2048), (8, 14336, 2048), (8, 14336, 2047), (8, 14272, 2100), (13, 14300, 2081),
+    (16, 16384, 4200), (17, 16384, 2048), (9, 16385, 2048), (12, 20480, 2176), (16, 28610, 2050)])
+def test_matmul_few_rows_of_many_columns(M, N, K, dtype):
+    a = sffn.mx_quantize(_rand((M, K), M + K))
+    b = sffn.mx_quantize(_rand((N, K), N + K + 1))
+    av, bv = sffn.mx_dequantize(a).double(), sffn.mx_dequantize(b).double()
+    ref, mag = av @ bv.t(), av.abs() @ bv.abs().t()
+    out = sffn.mx_matmul(a, b, dtype=dtype)
+    tol = K * 2.0 ** -23 * mag
+    if dtype == torch.bfloat16:
+        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs()
+    assert ((out.double() - ref).abs() <= tol).all()
+    assert torch.equal(out, sffn.mx_matmul(a, b, dtype=dtype))

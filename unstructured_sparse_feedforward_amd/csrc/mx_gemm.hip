@@ -26,7 +26,7 @@ __device__ __forceinline__ void put(uint16_t* p, float v) {
 // by 128-wide groups and add their sums in LDS. Each wave has a ring of its
 // own in LDS, filled by direct copies kFewSlots groups ahead: loads straight
 // into the instruction's lanes, which hold different rows, take an access
-// each (16 x 16384 x 4096: 11.4 us, so 7.8; 16 x 1024 x 16384: 10.5, 5.4). The
+// each (16 x 1024 x 16384: 10.5 us, so 5.4). The
 // rows of b are the instruction's first operand: lane l holds row l % 16, k =
 // 32 (l / 16) .. + 31, and of the result four consecutive n of row m = l % 16.
 // A slot holds the 16 rows of b and those of a, row r's 16-byte piece c at
@@ -498,10 +498,17 @@ __global__ __launch_bounds__(256, (Big<MI, NS>::WGS)) void mx_big_kernel(MxGemmA
 
 // The kernel by the number of tiles, measured with float32 results (us,
 // M x N x K; the sides of each border):
-//   few rows:    up to 16: 1 x 5632 x 2048 3.0, 32 x 64 tiles 3.6; 16 x
-//                16384 x 4096 7.8, 64 x 64 7.2 (from a graph, as the few
-//                rows' other figures)
-//   32 x 64:     up to 128 tiles of 64 x 64, which leave CUs without one:
+//   few rows:    up to 16 (from graphs, on matrices b that the caches do not
+//                hold): 1 x 5632 x 2048 3.8, 32 x 64 tiles 4.4; 16 x 20480 x
+//                4096 (320 tiles: a second round of the CUs for 64 of them)
+//                12.9, 14.3; 2 x 16320 x 16384 30.0, 33.0
+//   32 x 64:     for 8 to 16 rows and K from 2048 on where the tiles fill
+//                their rounds of the CUs to 7/8, since their copies of a serve
+//                64 rows of b, the few rows' 16: 16 x 16384 x 4096 9.2, few
+//                rows 10.7; 16 x 65536 x 8192 62.3, 80.6; 8 x 14336 x 2048
+//                6.05, 6.37. (4 x 16384 x 16384 33.1, 32.7; 16 x 16320 x 1024
+//                4.67, 4.59.) And
+//                up to 128 tiles of 64 x 64, which leave CUs without one:
 //                256 x 2048 x 2048 (128 tiles) 5.5, 64 x 64 5.8;
 //                256 x 4096 x 2048 (256) 6.5, 64 x 64 6.2
 //   64 x 64:     up to 512 such tiles, two a CU: 1024 x 2048 x 2048 (512)
@@ -516,15 +523,17 @@ __global__ __launch_bounds__(256, (Big<MI, NS>::WGS)) void mx_big_kernel(MxGemmA
 //                on random operands, run at 6.0 PFLOP/s here (power).
 template <typename O>
 hipError_t launch(const MxGemmArgs& g, hipStream_t s) {
-  if (g.M <= 16) {
+  const int64_t m32 = (g.M + 31) / 32, n64 = (g.N + 63) / 64, t64 = (g.M + 63) / 64 * n64;
+  const bool filled = 8 * n64 >= 7 * kCus * ((n64 + kCus - 1) / kCus);
+  const bool wide = g.M >= 8 && g.M <= 16 && g.K >= 2048 && filled;
+  if (g.M <= 16 && !wide) {
     const unsigned grid = (unsigned)((g.N + 15) / 16);
     if (g.K <= 4096) mx_few_kernel<4, O><<<grid, 256, 4 * kFewRing, s>>>(g);
     else mx_few_kernel<8, O><<<grid, 512, 8 * kFewRing, s>>>(g);
     return hipGetLastError();
   }
-  const int64_t m32 = (g.M + 31) / 32, n64 = (g.N + 63) / 64, t64 = (g.M + 63) / 64 * n64;
   const int64_t t256 = ((g.M + 255) / 256) * ((g.N + 255) / 256);
-  if (t64 <= 128)
+  if (wide || t64 <= 128)
     mx_mid_kernel<1, O><<<dim3((unsigned)n64, (unsigned)m32), 256, Mid<1>::LDS, s>>>(g);
   else if (t64 <= 512 || g.K == 0)   // (no tile of the others is ever empty)
     mx_mid_kernel<2, O><<<dim3((unsigned)n64, (unsigned)((g.M + 63) / 64)), 256, Mid<2>::LDS,

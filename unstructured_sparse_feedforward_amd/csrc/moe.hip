@@ -918,7 +918,7 @@ void moe_plan(bool mx, MoeArgs* a) {
   a->chunks = (a->d + cols - 1) / cols;
   // Where workgroups are few, an expert's blocks of tokens go to several, and
   // in the down kernel ranges of at least 1024 neurons do (their outputs are
-  // added in the sum kernel): 128 tokens to one bf16 expert of 2048 x 5632 88
+  // added in the sum kernel): 128 tokens to one bf16 expert of 2048 x 5632 86
   // us, without 374; one token to 2 of 8 28.8, without 31.7. Ranges up to
   // 256 workgroups (64 tokens over 16 experts of 5632 neurons: 99.1 us, up to
   // 512 99.9), with several blocks of tokens 512 (128 tokens of 2 over 4

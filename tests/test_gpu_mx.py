@@ -324,3 +324,16 @@ def test_matmul_few_rows_of_many_columns(M, N, K, dtype):
         tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs()
     assert ((out.double() - ref).abs() <= tol).all()
     assert torch.equal(out, sffn.mx_matmul(a, b, dtype=dtype))
+
+
+@pytest.mark.parametrize("made", [True, False])
+@pytest.mark.parametrize("built", [True, False])
+def test_matrices_of_inference_mode(made, built):
+    """Codes and scales made in inference mode or outside, an MXTensor built
+    of them in the mode or outside."""
+    with torch.inference_mode(made):
+        q = sffn.mx_quantize(_rand((6, 200), 1))
+    with torch.inference_mode(built):
+        r = sffn.MXTensor(q.codes, q.scales, 6, 200)
+        out = sffn.mx_matmul(r, q)
+    assert torch.equal(out, sffn.mx_matmul(q, q))

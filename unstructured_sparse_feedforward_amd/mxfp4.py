@@ -47,7 +47,8 @@ class MXTensor:
             raise ValueError("codes and scales must be on one GPU")
         live = -(-cols // 32) % 4
         if live:
-            scales[-1, :, live:].zero_()
+            with torch.inference_mode():   # scales may have been made in it
+                scales[-1, :, live:].zero_()
         self.rows, self.cols, self.device = rows, cols, codes.device
         self._codes, self._scales, self._buf = codes, scales, None
         self._pc, self._ps = codes.data_ptr(), scales.data_ptr()

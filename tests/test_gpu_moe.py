@@ -393,3 +393,22 @@ def test_longest_slices(T, d, F, E, k, gated, weights, active):
     out = layer.forward(x, wr, *ws, return_routing=True)
     check(layer, x, wr, ws, out)
     assert torch.equal(layer.forward(x, wr, *ws), out[0])
+
+
+@pytest.mark.parametrize("weights", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("T,E,k,n", [
+    # a single token routed by the hidden kernel and by its own; a unit for each
+    # pair of fewer tokens than the call's, and of none
+    (1, 8, 2, 0), (1, 8, 2, 1), (1, 130, 3, 0), (1, 130, 3, 1), (4, 64, 6, 0), (4, 64, 6, 1),
+    (4, 64, 6, 3), (5, 200, 32, 2)])
+def test_padded_batch_of_few_tokens(T, E, k, n, weights):
+    layer, x, wr, ws = make(T, 256, 96, E, k, True, weights)
+    x[n:] = float("nan")
+    y = torch.full((T, 256), 7.0, device="cuda")
+    ids = torch.full((T, k), -9, dtype=torch.int32, device="cuda")
+    probs = torch.full((T, k), 5.0, device="cuda")
+    nt = torch.tensor([n], dtype=torch.int32, device="cuda")
+    layer.forward(x, wr, *ws, y=y, n_tokens=nt, routing=(ids, probs))
+    assert (y[n:] == 7).all() and (ids[n:] == -9).all() and (probs[n:] == 5).all()
+    if n:
+        check(layer, x[:n], wr, ws, (y[:n], ids[:n], probs[:n]))

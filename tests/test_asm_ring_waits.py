@@ -295,7 +295,7 @@ def _ring(per=4, slots=2, body=None, first=None):
             + ["v_mfma_f32 a0", "s_cbranch_scc1 .LBB0_1", _W[0], _W[1] % 0, "s_endpgm"])
 
 
-def test_checker_on_a_product():
+def test_the_check_on_a_product():
     assert not _product_faults(Code(_ring()), 4, 2, 4, 4) and not Code(_ring()).order_faults()
     for body, first in ((3, None), (5, None), (None, 7), (None, 9)):
         assert _product_faults(Code(_ring(body=body, first=first)), 4, 2, 4, 4)
@@ -308,7 +308,7 @@ def test_checker_on_a_product():
     assert _product_faults(Code(t[:at] + ["global_load_dword v1, v2, s[0:1]"] + t[at:]), 4, 2, 4, 4)
 
 
-def test_checker_on_hidden_steps():
+def test_the_check_on_hidden_steps():
     load = "global_load_dwordx4 v[0:3], v8, s[0:1]"
 
     def steps(mx, step, left):

@@ -73,6 +73,7 @@ typedef int32_t sffn_status;
 #define SFFN_BF16 1
 /* element type of an expert layer's weights (microscaled 4-bit, below) */
 #define SFFN_MXFP4 2
+#define SFFN_MXFP8 3
 
 /* forward modes */
 #define SFFN_SPARSE 0   /* gate GEMM + TwELL, sparse up/down, dense path for flagged rows */
@@ -458,6 +459,173 @@ sffn_status sffn_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int6
 sffn_status sffn_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
                            const uint8_t* b_codes, const uint8_t* b_scales, int64_t N, int64_t K,
                            void* out, int32_t out_dtype, int64_t ldo, hipStream_t stream);
+
+/*
+ * Microscaled 8-bit floating point (MXFP8), the form of activations beside
+ * 4-bit weights: as MXFP4, with one byte an element, a signed e4m3 value (up
+ * to 448), codes [R, Kp] bytes, and the same scales. Sizes and alignments
+ * are MXFP4's.
+ */
+sffn_status sffn_mx8_bytes(int64_t rows, int64_t cols, size_t* code_bytes, size_t* scale_bytes);
+
+/* Quantise x as sffn_mx_quantize does (not transposed): a block's exponent
+ * is that of its largest magnitude less 8, at least -127; elements round to
+ * the nearest value (ties to the even code) and saturate at 448. */
+sffn_status sffn_mx8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols,
+                              int64_t ldx, uint8_t* codes, uint8_t* scales, hipStream_t stream);
+
+/* The values the codes stand for, as sffn_mx_dequantize. Exact as float32,
+ * and as bf16 down to its subnormals. */
+sffn_status sffn_mx8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                int64_t cols, void* out, int32_t dtype, int64_t ldo,
+                                hipStream_t stream);
+
+/* sffn_mx_matmul for a in MXFP8 (tokens) and b in MXFP4 (weights). Products
+ * are exact, sums float32. Codes of a must not be NaN (0x7F, 0xFF). */
+sffn_status sffn_mx8_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
+                            const uint8_t* b_codes, const uint8_t* b_scales, int64_t N, int64_t K,
+                            void* out, int32_t out_dtype, int64_t ldo, hipStream_t stream);
+
+/*
+ * What stands between two layers: the residual's addition and the
+ * root-mean-square norm of the sum,
+ *   s = x + residual (rounded to the residual's type),
+ *   r = 1 / sqrt(mean(s^2) + eps),   y = s r w,
+ * over rows of up to 16384 columns (SFFN_E_UNSUPPORTED above, and above 2^27
+ * rows). Sums are float32 (a row's squares must not overflow); the same call
+ * repeats bit for bit, and a row's result does not depend on the other rows.
+ * Every matrix is float32 or bf16 with contiguous rows, its own row stride
+ * (>= cols elements) and no more than its elements' alignment.
+ *   x             [rows, cols]
+ *   residual      nullable: then s = x
+ *   residual_out  [rows, cols] of residual_dtype: s (NULL iff residual is).
+ *                 May be residual itself, or x where the types agree; apart
+ *                 from that, and from out = x, no result may overlap an
+ *                 operand.
+ *   weight        w [cols], nullable: 1
+ *   out           y: float32, bf16 (rounded once), or MXFP8 codes (16-byte
+ *                 aligned; SFFN_MXFP8, ldo is not used) of the [rows, cols]
+ *                 matrix, quantised from the float32 y
+ *   out_scales    their scales (SFFN_MXFP8; else NULL)
+ *   rstd          r [rows], nullable: the backward pass takes it
+ */
+typedef struct sffn_norm {
+  const void* x;
+  const void* residual;
+  void* residual_out;
+  const void* weight;
+  void* out;
+  uint8_t* out_scales;
+  float* rstd;
+  int64_t ldx;
+  int64_t ldr;
+  int64_t ldro;
+  int64_t ldo;
+  int32_t x_dtype;
+  int32_t residual_dtype;
+  int32_t weight_dtype;
+  int32_t out_dtype;
+} sffn_norm;
+
+/* eps >= 0. n_rows (device int32, nullable): only the first *n_rows rows (at
+ * most rows) count; results of the others are left as they were. No handle:
+ * runs on the current device, on the stream, keeps no state. A size of 0 is
+ * valid: nothing is written. */
+sffn_status sffn_rms_norm(const sffn_norm* norm, int64_t rows, int64_t cols, float eps,
+                          const int32_t* n_rows, hipStream_t stream);
+
+/*
+ * Its gradient: with xh = s r and g = dy w,
+ *   ds      = r (g - xh mean(g xh)) + dstream,   the gradient of x and of
+ *             residual alike
+ *   dweight = sum over rows of dy xh
+ * (the roundings of s and y count as the identity).
+ *   dy, s    [rows, cols]; s is residual_out of the forward pass (x where
+ *            there was no residual)
+ *   dstream  nullable: the gradient that reaches s beside the norm's
+ *   weight   nullable: 1
+ *   rstd     [rows] float32 of the forward pass
+ *   ds       [rows, cols], may be dy, s or dstream where the types agree
+ *   dweight  [cols] float32, nullable (NULL without a weight); written by
+ *            rows == 0 too (zeros)
+ * Sums are float32, of rows in an order that depends on the sizes alone.
+ */
+typedef struct sffn_norm_grad {
+  const void* dy;
+  const void* s;
+  const void* dstream;
+  const void* weight;
+  const float* rstd;
+  void* ds;
+  float* dweight;
+  int64_t lddy;
+  int64_t lds;
+  int64_t lddstream;
+  int64_t ldds;
+  int32_t dy_dtype;
+  int32_t s_dtype;
+  int32_t dstream_dtype;
+  int32_t weight_dtype;
+  int32_t ds_dtype;
+} sffn_norm_grad;
+
+/* The workspace (256-byte aligned; not shared by calls that overlap) is for
+ * dweight and may be NULL without it. */
+sffn_status sffn_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes);
+sffn_status sffn_rms_norm_backward(const sffn_norm_grad* grad, int64_t rows, int64_t cols,
+                                   void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * The choice of a token's experts from the router's logits l [T, E]:
+ *   scores   s = softmax(l) over the E experts, or (sigmoid = 1)
+ *            s = 1 / (1 + exp(-l))
+ *   c        s + bias, the bias [E] for balance (nullable)
+ *   groups   of E / groups consecutive experts each; the score of one is the
+ *            sum of its group_best (1 or 2) largest c, and only experts of the
+ *            top_groups groups with the largest score are chosen from
+ *   ids      the top_k experts with the largest c, in descending order (ties,
+ *            of groups too: the lower index first)
+ *   probs    scale s of the chosen experts, or (normalize = 1) scale s / (the
+ *            sum of the chosen s); without the bias
+ * Experts are compared in 64 bits, without a bias by their logits (which have
+ * the scores' order). Logits may be -infinity (an expert that is masked, of
+ * score 0, chosen only where nothing else is left); a token whose chosen
+ * experts all have score 0 gets weights 0. A NaN or +infinity leaves a
+ * token's indices valid and its weights unspecified, and other tokens alone.
+ *   n_experts  E <= 1024, a multiple of groups
+ *   top_k      k <= min(32, top_groups E / groups)
+ *   groups     <= 64 (1: no groups); group_best <= E / groups
+ *   scale      finite
+ * (SFFN_E_ARG for sizes below 1, a bad flag or sizes that do not fit together,
+ * SFFN_E_UNSUPPORTED beyond the limits.)
+ */
+typedef struct sffn_route_desc {
+  int32_t n_experts;
+  int32_t top_k;
+  int32_t groups;
+  int32_t top_groups;
+  int32_t group_best;
+  int32_t sigmoid;
+  int32_t normalize;
+  float scale;
+} sffn_route_desc;
+
+/* logits [T, E] of dtype with row stride ldl >= E, ids [T, k] int32, probs
+ * [T, k] float32; T up to 2^27. n_tokens as in sffn_moe_forward. No handle,
+ * no workspace, no state. */
+sffn_status sffn_route(const sffn_route_desc* desc, const void* logits, int32_t dtype, int64_t T,
+                       int64_t ldl, const float* bias, const int32_t* n_tokens, int32_t* ids,
+                       float* probs, hipStream_t stream);
+
+/* The gradient of the logits [T, E] (dl_dtype, row stride lddl >= E, every
+ * element written) from that of the weights, dprobs [T, k] float32; the choice
+ * itself, and with it the bias, has none. logits and ids are the forward
+ * pass's; an index outside 0 .. E - 1 counts as an expert that was not
+ * chosen. */
+sffn_status sffn_route_backward(const sffn_route_desc* desc, const float* dprobs,
+                                const void* logits, int32_t dtype, int64_t T, int64_t ldl,
+                                const int32_t* ids, const int32_t* n_tokens, void* dlogits,
+                                int32_t dl_dtype, int64_t lddl, hipStream_t stream);
 
 /*
  * A whole mixture-of-experts layer for few tokens (decoding batches). With

@@ -24,6 +24,7 @@ SFFN_E_CAPACITY = -4
 SFFN_F32 = 0
 SFFN_BF16 = 1
 SFFN_MXFP4 = 2
+SFFN_MXFP8 = 3
 SFFN_SPARSE = 0
 SFFN_DENSE = 1
 SFFN_OP_PACK = 0
@@ -43,7 +44,10 @@ EXPORTS = ("sffn_create", "sffn_destroy", "sffn_last_error", "sffn_status_string
            "sffn_hybrid_check", "sffn_backward", "sffn_forward_noalloc",
            "sffn_choose_mode", "sffn_train_dense_act_bytes", "sffn_forward_train_dense",
            "sffn_backward_dense", "sffn_mx_bytes", "sffn_mx_quantize", "sffn_mx_dequantize",
-           "sffn_mx_matmul", "sffn_moe_workspace_bytes", "sffn_moe_forward")
+           "sffn_mx_matmul", "sffn_moe_workspace_bytes", "sffn_moe_forward", "sffn_mx8_bytes",
+           "sffn_mx8_quantize", "sffn_mx8_dequantize", "sffn_mx8_matmul", "sffn_rms_norm",
+           "sffn_rms_norm_backward_workspace_bytes", "sffn_rms_norm_backward", "sffn_route",
+           "sffn_route_backward")
 SFFN_K_COUNT = 24
 
 
@@ -83,6 +87,34 @@ class SffnMoeWeights(ctypes.Structure):
 
 
 SFFN_MOE_MAX_TOKENS = 256
+
+
+class SffnNorm(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("residual_out", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("out_scales", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64),
+                ("ldro", ctypes.c_int64), ("ldo", ctypes.c_int64), ("x_dtype", ctypes.c_int32),
+                ("residual_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
+
+
+class SffnNormGrad(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("s", ctypes.c_void_p), ("dstream", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("ds", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("lds", ctypes.c_int64),
+                ("lddstream", ctypes.c_int64), ("ldds", ctypes.c_int64),
+                ("dy_dtype", ctypes.c_int32), ("s_dtype", ctypes.c_int32),
+                ("dstream_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("ds_dtype", ctypes.c_int32)]
+
+
+class SffnRouteDesc(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("sigmoid", ctypes.c_int32),
+                ("normalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
 
 _lib = None
 
@@ -162,6 +194,26 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                      ctypes.POINTER(SffnMoeWeights), i64, vp, vp, vp, vp, vp, sz,
                                      vp]
     lib.sffn_moe_forward.restype = i32
+    lib.sffn_mx8_bytes.argtypes = lib.sffn_mx_bytes.argtypes
+    lib.sffn_mx8_bytes.restype = i32
+    lib.sffn_mx8_quantize.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+    lib.sffn_mx8_quantize.restype = i32
+    lib.sffn_mx8_dequantize.argtypes = lib.sffn_mx_dequantize.argtypes
+    lib.sffn_mx8_dequantize.restype = i32
+    lib.sffn_mx8_matmul.argtypes = lib.sffn_mx_matmul.argtypes
+    lib.sffn_mx8_matmul.restype = i32
+    lib.sffn_rms_norm.argtypes = [ctypes.POINTER(SffnNorm), i64, i64, ctypes.c_float, vp, vp]
+    lib.sffn_rms_norm.restype = i32
+    lib.sffn_rms_norm_backward_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(sz)]
+    lib.sffn_rms_norm_backward_workspace_bytes.restype = i32
+    lib.sffn_rms_norm_backward.argtypes = [ctypes.POINTER(SffnNormGrad), i64, i64, vp, sz, vp]
+    lib.sffn_rms_norm_backward.restype = i32
+    lib.sffn_route.argtypes = [ctypes.POINTER(SffnRouteDesc), vp, i32, i64, i64, vp, vp, vp, vp,
+                               vp]
+    lib.sffn_route.restype = i32
+    lib.sffn_route_backward.argtypes = [ctypes.POINTER(SffnRouteDesc), vp, vp, i32, i64, i64, vp,
+                                        vp, vp, i32, i64, vp]
+    lib.sffn_route_backward.restype = i32
     _lib = lib
     return lib
 

@@ -1,5 +1,5 @@
-// MXFP4 matrices, shared by the quantiser (mx.hip), the product
-// (mx_gemm.hip) and the expert layer (moe.hip), and the copies into LDS of
+// MXFP4 matrices, shared by the quantiser (mx.hip), the products
+// (mx_gemm.hip, mx8_gemm.hip) and the expert layer (moe.hip), and the copies into LDS of
 // the last two.
 //
 // A matrix [R, K] (blocks of 32 along K) is kept as
@@ -79,6 +79,14 @@ hipError_t launch_mx_quantize(Dtype dt, const void* x, int64_t rows, int64_t col
 hipError_t launch_mx_dequantize(Dtype dt, const uint8_t* codes, const uint8_t* scales,
                                 int64_t rows, int64_t cols, void* out, int64_t ldo, hipStream_t s);
 
+// The same for MXFP8 (e4m3 elements): codes [R, Kp] bytes, element k of a row
+// in byte k, the scales as above.
+hipError_t launch_mx8_quantize(Dtype dt, const void* x, int64_t rows, int64_t cols, int64_t ldx,
+                               uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_mx8_dequantize(Dtype dt, const uint8_t* codes, const uint8_t* scales,
+                                 int64_t rows, int64_t cols, void* out, int64_t ldo,
+                                 hipStream_t s);
+
 // out[m, n] = sum_k a[m, k] b[n, k], stored as float32 or bf16
 struct MxGemmArgs {
   const uint8_t* a;
@@ -90,5 +98,7 @@ struct MxGemmArgs {
   int64_t ldo;
 };
 hipError_t launch_mx_gemm(Dtype out_dt, const MxGemmArgs& g, hipStream_t s);
+// a in MXFP8, b in MXFP4
+hipError_t launch_mx8_gemm(Dtype out_dt, const MxGemmArgs& g, hipStream_t s);
 
 }  // namespace sffn

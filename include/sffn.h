@@ -707,6 +707,17 @@ sffn_status sffn_moe_forward(const sffn_moe_desc* desc, const void* x, const sff
                              int64_t T, const int32_t* n_tokens, float* y, int32_t* ids,
                              float* probs, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* The layer with experts that the caller has chosen (sffn_route, or any
+ * other way) in place of its router's: y = sum_r probs_r expert_{ids_r}(x).
+ * ids [T, k] int32, probs [T, k] float32 (any values); w->router must be NULL,
+ * and desc.normalize is not used. An index outside 0 .. E - 1 adds nothing (a
+ * pair that was dropped, or another rank's); one that a token has twice
+ * counts with both weights. Workspace and the rest as in sffn_moe_forward. */
+sffn_status sffn_moe_forward_chosen(const sffn_moe_desc* desc, const void* x,
+                                    const sffn_moe_weights* w, int64_t T, const int32_t* n_tokens,
+                                    const int32_t* ids, const float* probs, float* y, void* ws,
+                                    size_t ws_bytes, hipStream_t stream);
+
 /*
  * Per-kernel timing. While enabled, every kernel launch of the handle's
  * calls is bracketed by two HIP events recorded on the call's stream, so that each

@@ -47,7 +47,7 @@ EXPORTS = ("sffn_create", "sffn_destroy", "sffn_last_error", "sffn_status_string
            "sffn_mx_matmul", "sffn_moe_workspace_bytes", "sffn_moe_forward", "sffn_mx8_bytes",
            "sffn_mx8_quantize", "sffn_mx8_dequantize", "sffn_mx8_matmul", "sffn_rms_norm",
            "sffn_rms_norm_backward_workspace_bytes", "sffn_rms_norm_backward", "sffn_route",
-           "sffn_route_backward")
+           "sffn_route_backward", "sffn_moe_forward_chosen")
 SFFN_K_COUNT = 24
 
 
@@ -194,6 +194,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                      ctypes.POINTER(SffnMoeWeights), i64, vp, vp, vp, vp, vp, sz,
                                      vp]
     lib.sffn_moe_forward.restype = i32
+    lib.sffn_moe_forward_chosen.argtypes = [ctypes.POINTER(SffnMoeDesc), vp,
+                                            ctypes.POINTER(SffnMoeWeights), i64, vp, vp, vp, vp,
+                                            vp, sz, vp]
+    lib.sffn_moe_forward_chosen.restype = i32
     lib.sffn_mx8_bytes.argtypes = lib.sffn_mx_bytes.argtypes
     lib.sffn_mx8_bytes.restype = i32
     lib.sffn_mx8_quantize.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]

@@ -30,9 +30,11 @@ struct Layout {
   size_t keys, expert, weight, on, h, part, total;
 };
 
-// the sizes of a call, with what moe_plan derives from them
-MoeArgs sizes(const sffn_moe_desc& D, int64_t T) {
+// the sizes of a call, with what moe_plan derives from them (given: the caller
+// chooses the experts)
+MoeArgs sizes(const sffn_moe_desc& D, int64_t T, const int32_t* given) {
   MoeArgs a = {};
+  a.in_ids = given;
   a.T = (int)T;
   a.d = D.d;
   a.F = D.d_ff;
@@ -62,32 +64,15 @@ Layout layout(const MoeArgs& a) {
   return L;
 }
 
-}  // namespace
-
-extern "C" {
-
-sffn_status sffn_moe_workspace_bytes(const sffn_moe_desc* desc, int64_t T, size_t* bytes) {
-  const sffn_status st = validate(desc);
-  if (st != SFFN_OK) return st;
-  if (!bytes || T < 0) return SFFN_E_ARG;
-  if (T > SFFN_MOE_MAX_TOKENS) return SFFN_E_UNSUPPORTED;
-  *bytes = T == 0 ? 0 : layout(sizes(*desc, T)).total;
-  return SFFN_OK;
-}
-
-sffn_status sffn_moe_forward(const sffn_moe_desc* desc, const void* x, const sffn_moe_weights* w,
-                             int64_t T, const int32_t* n_tokens, float* y, int32_t* ids,
-                             float* probs, void* ws, size_t ws_bytes, hipStream_t stream) {
-  const sffn_status st = validate(desc);
-  if (st != SFFN_OK) return st;
-  const sffn_moe_desc& D = *desc;
-  if (!w || T < 0) return SFFN_E_ARG;
-  if (T > SFFN_MOE_MAX_TOKENS) return SFFN_E_UNSUPPORTED;
-  if (T == 0) return SFFN_OK;
+// a call whose experts come from its router, or are ids and probs
+sffn_status forward(const sffn_moe_desc& D, const void* x, const sffn_moe_weights* w, int64_t T,
+                    const int32_t* n_tokens, float* y, const int32_t* in_ids,
+                    const float* in_probs, int32_t* ids, float* probs, void* ws, size_t ws_bytes,
+                    hipStream_t stream) {
   const bool mx = D.weights == SFFN_MXFP4;
-  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(w->router, 16) || !aligned(w->gate, 16) ||
-      !aligned(w->down, 16))
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(w->gate, 16) || !aligned(w->down, 16))
     return SFFN_E_ARG;
+  if (in_ids ? w->router != nullptr : !aligned(w->router, 16)) return SFFN_E_ARG;
   if (D.gated ? !aligned(w->up, 16) : w->up != nullptr) return SFFN_E_ARG;
   if (mx) {
     if (!aligned(w->gate_scales, 4) || !aligned(w->down_scales, 4)) return SFFN_E_ARG;
@@ -98,12 +83,13 @@ sffn_status sffn_moe_forward(const sffn_moe_desc* desc, const void* x, const sff
   if ((n_tokens && !aligned(n_tokens, 4)) || (ids && !aligned(ids, 4)) ||
       (probs && !aligned(probs, 4)))
     return SFFN_E_ARG;
-  MoeArgs a = sizes(D, T);
+  MoeArgs a = sizes(D, T, in_ids);
   const Layout L = layout(a);
   if (!aligned(ws, kAlign) || ws_bytes < L.total) return SFFN_E_ARG;
   char* base = (char*)ws;
   a.x = (const uint16_t*)x;
   a.router = (const uint16_t*)w->router;
+  a.in_probs = in_probs;
   a.wg = w->gate;
   a.wu = w->up;
   a.wd = w->down;
@@ -121,6 +107,47 @@ sffn_status sffn_moe_forward(const sffn_moe_desc* desc, const void* x, const sff
   a.ids = ids;
   a.probs = probs;
   return launch_moe(mx, a, stream) == hipSuccess ? SFFN_OK : SFFN_E_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+sffn_status sffn_moe_workspace_bytes(const sffn_moe_desc* desc, int64_t T, size_t* bytes) {
+  const sffn_status st = validate(desc);
+  if (st != SFFN_OK) return st;
+  if (!bytes || T < 0) return SFFN_E_ARG;
+  if (T > SFFN_MOE_MAX_TOKENS) return SFFN_E_UNSUPPORTED;
+  // (of either call: any pointer says that the experts are given)
+  static const int32_t given = 0;
+  const size_t own = T == 0 ? 0 : layout(sizes(*desc, T, nullptr)).total;
+  const size_t other = T == 0 ? 0 : layout(sizes(*desc, T, &given)).total;
+  *bytes = own > other ? own : other;
+  return SFFN_OK;
+}
+
+sffn_status sffn_moe_forward(const sffn_moe_desc* desc, const void* x, const sffn_moe_weights* w,
+                             int64_t T, const int32_t* n_tokens, float* y, int32_t* ids,
+                             float* probs, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const sffn_status st = validate(desc);
+  if (st != SFFN_OK) return st;
+  if (!w || T < 0) return SFFN_E_ARG;
+  if (T > SFFN_MOE_MAX_TOKENS) return SFFN_E_UNSUPPORTED;
+  if (T == 0) return SFFN_OK;
+  return forward(*desc, x, w, T, n_tokens, y, nullptr, nullptr, ids, probs, ws, ws_bytes, stream);
+}
+
+sffn_status sffn_moe_forward_chosen(const sffn_moe_desc* desc, const void* x,
+                                    const sffn_moe_weights* w, int64_t T, const int32_t* n_tokens,
+                                    const int32_t* ids, const float* probs, float* y, void* ws,
+                                    size_t ws_bytes, hipStream_t stream) {
+  const sffn_status st = validate(desc);
+  if (st != SFFN_OK) return st;
+  if (!w || T < 0) return SFFN_E_ARG;
+  if (T > SFFN_MOE_MAX_TOKENS) return SFFN_E_UNSUPPORTED;
+  if (T == 0) return SFFN_OK;
+  if (!aligned(ids, 4) || !aligned(probs, 4)) return SFFN_E_ARG;
+  return forward(*desc, x, w, T, n_tokens, y, ids, probs, nullptr, nullptr, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

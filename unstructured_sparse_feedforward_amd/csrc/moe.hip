@@ -9,7 +9,8 @@
 // tokens). The launches:
 //   logits  x W_r^T in 64 bits, a wave an expert and token;
 //   route   top k and weights, a workgroup a token (for few experts together
-//           with the logits; a single token's is part of the next kernel);
+//           with the logits; a single token's is part of the next kernel; in
+//           place of both, take, where the caller has chosen the experts);
 //   hidden  a workgroup has an expert and a slice of its neurons: it computes
 //           z for all of the expert's tokens, and u only for the neurons that
 //           are active (z > 0) for one of them, as in the rest of the library;
@@ -173,6 +174,29 @@ __global__ __launch_bounds__(N) void moe_route_kernel(MoeArgs a) {
     if (a.ids) a.ids[i] = r.expert[tid];
     if (a.probs) a.probs[i] = r.p[tid];
   }
+}
+
+// Experts and weights given by the caller, a thread a (token, rank) pair: an
+// index that is no expert's becomes -1, whose pair no later kernel computes or
+// adds; of one that a token has twice the first pair takes both weights, so
+// that an expert has a token once (its list of pairs has room for that).
+__global__ __launch_bounds__(64) void moe_take_kernel(MoeArgs a) {
+  const int i = blockIdx.x * 64 + threadIdx.x;
+  const int t = i / a.k, r = i % a.k;
+  if (t >= tokens(a)) return;
+  const int32_t* ids = a.in_ids + (int64_t)t * a.k;
+  const float* p = a.in_probs + (int64_t)t * a.k;
+  const int e = ids[r];
+  bool mine = e >= 0 && e < a.E;
+  float w = 0.0f;
+#pragma unroll 8
+  for (int q = 0; q < a.k; ++q)
+    if (ids[q] == e) {
+      if (q < r) mine = false;
+      else w += p[q];
+    }
+  a.expert[i] = mine ? e : -1;
+  a.weight[i] = w;
 }
 
 // ---------------------------------------------------------------- weights
@@ -424,6 +448,7 @@ __device__ __forceinline__ int unit_pairs(const MoeArgs& a, int unit, Lists& ls,
   const bool pairs = a.by_pair;
   if (pairs && unit >= np) return 0;
   const int e = pairs ? a.expert[unit] : unit;
+  if (e < 0) return 0;
   *expert = e;
   int n = 0, less = 0;
   for (int i0 = 0; i0 < np; i0 += NT) {
@@ -850,6 +875,8 @@ __global__ __launch_bounds__(NT, 2) void moe_down_kernel(MoeArgs a) {
 // ---------------------------------------------------------------- sum
 
 // y of a token: a wave 256 columns, the k outputs in the order of their ranks
+// (GIVEN: those of its pairs that have an expert)
+template <bool GIVEN>
 __global__ __launch_bounds__(64) void moe_sum_kernel(MoeArgs a) {
   const int t = blockIdx.y, lane = threadIdx.x;
   if (t >= tokens(a)) return;
@@ -860,6 +887,7 @@ __global__ __launch_bounds__(64) void moe_sum_kernel(MoeArgs a) {
   f32x4_t s = {};
 #pragma unroll 8
   for (int r = 0; r < a.k; ++r) {
+    if (GIVEN && a.expert[(int64_t)t * a.k + r] < 0) continue;
     f32x4_t v = *(const f32x4_t*)(q + (int64_t)r * a.d);
     for (int i = 1; i < a.split; ++i)
       v += *(const f32x4_t*)(q + ((int64_t)i * a.T * a.k + r) * a.d);
@@ -882,7 +910,7 @@ hipError_t launch_hidden(const MoeArgs& a, hipStream_t s) {
 
 void moe_plan(bool mx, MoeArgs* a) {
   const int pairs = a->T * a->k;
-  a->one = a->T == 1 && a->E <= kOneE;
+  a->one = a->T == 1 && a->E <= kOneE && !a->in_ids;
   // Units of the fewer of pairs and experts: of 6 of 64 bf16 experts of 2048 x
   // 1408, 2, 4 and 8 tokens take 41.2, 53.1 and 75.7 us, with a unit for every
   // expert 43.5, 56.8 and 78.7; of 8 of 128 4-bit ones of 2048 x 768, 2, 8 and 15
@@ -935,7 +963,9 @@ void moe_plan(bool mx, MoeArgs* a) {
 }
 
 hipError_t launch_moe(bool mx, const MoeArgs& a, hipStream_t s) {
-  if (!a.one && a.E <= kFusedE) {
+  if (a.in_ids) {
+    moe_take_kernel<<<(a.T * a.k + 63) / 64, 64, 0, s>>>(a);
+  } else if (!a.one && a.E <= kFusedE) {
     moe_route_kernel<true, kFusedE * 64><<<a.T, kFusedE * 64, 0, s>>>(a);
   } else {
     moe_logits_kernel<<<dim3((a.E + kWaves - 1) / kWaves, a.T), NT, 0, s>>>(a);
@@ -952,7 +982,9 @@ hipError_t launch_moe(bool mx, const MoeArgs& a, hipStream_t s) {
   else moe_down_kernel<false><<<grid, NT, 0, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  moe_sum_kernel<<<dim3((a.d + 255) / 256, a.T), 64, 0, s>>>(a);
+  const dim3 sum((a.d + 255) / 256, a.T);
+  if (a.in_ids) moe_sum_kernel<true><<<sum, 64, 0, s>>>(a);
+  else moe_sum_kernel<false><<<sum, 64, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -22,6 +22,8 @@ struct MoeArgs {
   int T, d, F, E, k;
   int normalize;
   const int32_t* t_dev;      // nullable: the number of valid tokens
+  const int32_t* in_ids;     // [T, k] the tokens' experts and their weights as given by the
+  const float* in_probs;     // caller, in place of the router (nullable, both)
   // A unit is an expert, or, when the (token, rank) pairs are fewer than the
   // experts, a pair (the pair of an expert's first token works for all of
   // the expert's tokens, the others have no tokens): Y of them.
@@ -48,7 +50,7 @@ struct MoeArgs {
   float* probs;              // [T, k] (nullable)
 };
 
-// fills Y .. fs from the sizes
+// fills Y .. fs from the sizes (and whether the experts are given)
 void moe_plan(bool mx, MoeArgs* a);
 hipError_t launch_moe(bool mx, const MoeArgs& a, hipStream_t s);
 

@@ -81,24 +81,38 @@ class SparseMoE:
             raise ValueError(f"{what} must be an MXTensor of {E * F} x {d} on {device}")
         return w._pc, w._ps
 
-    def forward(self, x: torch.Tensor, w_router: torch.Tensor, w_gate: Weight,
+    def forward(self, x: torch.Tensor, w_router: Optional[torch.Tensor], w_gate: Weight,
                 w_up: Optional[Weight], w_down: Weight, y: Optional[torch.Tensor] = None,
                 n_tokens: Optional[torch.Tensor] = None, return_routing: bool = False,
-                routing: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
+                routing: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                chosen: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
         """y [T, d] float32 for ``x`` [T, d] bfloat16; with
         ``return_routing`` (y, ids [T, k] int32, probs [T, k] float32), the
         chosen experts in descending order of their logits and their
         weights. ``n_tokens``, an int32 tensor of one element on the GPU,
         says how many of the rows are tokens: the others are neither read
         nor written (in results made here they are uninitialised). ``y`` and
-        ``routing`` (ids, probs) may pass result tensors to reuse."""
+        ``routing`` (ids, probs) may pass result tensors to reuse.
+
+        ``chosen`` (ids [T, k] int32, probs [T, k] float32), what
+        :class:`MoERouter` gives, takes the place of the layer's own router:
+        ``w_router`` is then None, and y the sum of the experts' outputs with
+        these weights. An index that is no expert's adds nothing, one that a
+        token has twice counts with both weights."""
         if x.dim() != 2 or not x.is_cuda:
             raise ValueError("x must be a [T, d] tensor on the GPU")
         T, dev = x.shape[0], x.device
         if T > SFFN_MOE_MAX_TOKENS:
             raise ValueError(f"{T} tokens: at most {SFFN_MOE_MAX_TOKENS} a call")
         px = self._plain(x, (T, self.d), torch.bfloat16, dev, "x")
-        pr = self._plain(w_router, (self.n_experts, self.d), torch.bfloat16, dev, "w_router")
+        if chosen is None:
+            if w_router is None:
+                raise ValueError("w_router is missing: no experts are given")
+            pr = self._plain(w_router, (self.n_experts, self.d), torch.bfloat16, dev, "w_router")
+        elif w_router is not None or return_routing or routing is not None:
+            raise ValueError("the chosen experts are given: no w_router, return_routing or routing")
+        else:
+            pr = None
         g, gs = self._weight(w_gate, dev, "w_gate")
         if self.gated:
             if w_up is None:
@@ -121,7 +135,10 @@ class SparseMoE:
         else:
             py = self._plain(y, (T, self.d), torch.float32, dev, "y")
         ids = probs = pi = pp = None
-        if routing is not None:
+        if chosen is not None:
+            ci = self._plain(chosen[0], (T, k), torch.int32, dev, "chosen ids")
+            cp = self._plain(chosen[1], (T, k), torch.float32, dev, "chosen probs")
+        elif routing is not None:
             ids, probs = routing
             pi = self._plain(ids, (T, k), torch.int32, dev, "ids")
             pp = self._plain(probs, (T, k), torch.float32, dev, "probs")
@@ -132,6 +149,10 @@ class SparseMoE:
             nb = self.workspace_bytes(T)
             # torch's allocations are 512-byte aligned
             ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-            _launch(dev, "sffn_moe_forward", self.lib.sffn_moe_forward, self._desc, px,
-                    ctypes.byref(w), T, pn, py, pi, pp, ws.data_ptr(), nb)
+            if chosen is not None:
+                _launch(dev, "sffn_moe_forward_chosen", self.lib.sffn_moe_forward_chosen,
+                        self._desc, px, ctypes.byref(w), T, pn, ci, cp, py, ws.data_ptr(), nb)
+            else:
+                _launch(dev, "sffn_moe_forward", self.lib.sffn_moe_forward, self._desc, px,
+                        ctypes.byref(w), T, pn, py, pi, pp, ws.data_ptr(), nb)
         return (y, ids, probs) if return_routing else y

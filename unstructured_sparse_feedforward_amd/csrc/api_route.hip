@@ -37,6 +37,7 @@ sffn_status validate(const sffn_route_desc* D, RouteArgs* a) {
   a->sigmoid = D->sigmoid;
   a->normalize = D->normalize;
   a->scale = D->scale;
+  a->inv_per = 1.0f / (float)per;
   return SFFN_OK;
 }
 

@@ -17,21 +17,15 @@
 // below the part's largest exponent, e2m1's at most 3 (0.5 under 4), 13 in
 // all, so that nothing is cut and only float32 additions round, as in the
 // rest of the library.
-#include "mx.hpp"
+#include <cstdlib>
+#include "mx_gemm.hpp"
 
 namespace sffn {
 namespace {
 
-typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
-constexpr int kFp8 = 0, kFp4 = 4;   // operand format fields of the f8f6f4 instructions
-
-// 16 bytes (32 elements) of a 4-bit operand: the instruction reads the first
-// four registers. 2 x 16 bytes of an 8-bit one: in a lane group g of n, the
-// first are k = 16 g .. + 15, the second 16 n + 16 g .. + 15. (The scale of
-// the 32 elements from k = 32 g is that of lane group g for either.)
-__device__ __forceinline__ i32x8_t frag(const i32x4_t v) {
-  return i32x8_t{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
-}
+// Of an 8-bit operand a lane group g of n holds 2 x 16 bytes, k = 16 g .. + 15
+// and 16 n + 16 g .. + 15; of a 4-bit one 16 bytes, k = 32 g .. + 31. (The
+// scale of the 32 elements from k = 32 g is that of lane group g for either.)
 
 // The two parts of an 8-bit operand: the bytes with bit 6 (an exponent field of
 // 8 or more), and the others.
@@ -44,11 +38,6 @@ __device__ __forceinline__ void parts(const i32x4_t a, const i32x4_t b, i32x8_t&
     hi[i] = (int32_t)(x & m);
     lo[i] = (int32_t)(x & ~m);
   }
-}
-
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(uint16_t* p, float v) {
-  *p = __builtin_bit_cast(uint16_t, (__bf16)v);   // to nearest even; NaN stays NaN
 }
 
 // ---------------------------------------------------------------- small tiles
@@ -186,10 +175,266 @@ __global__ __launch_bounds__(256) void mx8_mid_kernel(MxGemmArgs g) {
   }
 }
 
+// ---------------------------------------------------------------- large tiles
+
+// A (64 MI) x 256 tile a workgroup of 4 waves (2 x 2), a wave (32 MI) x 128
+// of it: MI x 4 blocks of the 32 x 32 x 64 instruction, two of them for the two
+// parts of a. Both operands stream through a ring of NS LDS slots filled by
+// direct copies, 128 k (128 bytes of a row of a, 64 of b, and their four scale
+// bytes) a slot. The ring runs on across the tiles of a workgroup. A slot
+// holds the rows' codes, a's and then b's, in the pieces of the small tiles,
+// then the rows' scale dwords, those of the 32-row blocks of a wave's rows side
+// by side: one read gives a lane its scales of an operand.
+//
+// A stage is two substeps of 64 k. Substep 0 multiplies fragments that are
+// in registers while those of substep 1 are read; then the wave waits for
+// its copies of the next stage, the barrier makes everyone's visible (and
+// frees the slot, whose last fragments are in registers), and substep 1
+// multiplies while the next stage's first fragments are read. Every
+// substep starts some of the copies, NS stages ahead.
+template <int MI, int NS>
+struct Big {
+  static constexpr int BM = 64 * MI, BN = 256, WM = 32 * MI;
+  static constexpr int B = BM * 128, S = B + BN * 64;   // b's rows, the scales
+  static constexpr int SLOT = S + (BM + BN) * 4;
+  static constexpr int CA = 2 * MI + 1, CB = 5;   // copies a wave and stage
+  static constexpr int LDS = NS * SLOT;
+};
+
+template <int MI, int NS, typename O>
+__global__ __launch_bounds__(256, 1) void mx8_big_kernel(MxGemmArgs g) {
+  typedef Big<MI, NS> C_;
+  constexpr int BM = C_::BM, BN = C_::BN, SLOT = C_::SLOT, CA = C_::CA, CB = C_::CB;
+  constexpr int LPS = CA + CB;
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave >> 1, wc = wave & 1;
+  const int hi = lane >> 5, l31 = lane & 31;
+  const int M = (int)g.M, N = (int)g.N;
+  const int64_t Kp = mx_padded(g.K);
+  const int G = (int)(Kp / 128);
+
+  // Tiles in groups of kGroupM row tiles, all column tiles of a group before
+  // the next; each XCD takes a contiguous eighth of that order, so that its
+  // CUs share row panels in its L2.
+  const int mt = (M + BM - 1) / BM, ntl = (N + BN - 1) / BN;
+  const int ntiles = mt * ntl;
+  const int per = (ntiles + kNXcd - 1) / kNXcd;
+  const int t_begin = (blockIdx.x % kNXcd) * per;
+  const int t_end = min(ntiles, t_begin + per);
+  const int step = gridDim.x / kNXcd;
+  int L = t_begin + (int)(blockIdx.x / kNXcd);
+  if (L >= t_end) return;
+  auto coords = [&](int t, int& m0, int& n0) {
+    const int grp = t / (kGroupM * ntl);
+    const int gsz = min(mt - grp * kGroupM, kGroupM);
+    const int rr = t - grp * kGroupM * ntl;
+    m0 = (grp * kGroupM + rr % gsz) * BM;
+    n0 = (rr / gsz) * BN;
+  };
+
+  // copy state: the tile and stage whose copies go out next. A wave copies
+  // rows 16 MI wave .. of a, 8 a copy (lane l row l / 8, piece l % 8 of the
+  // slot), 64 wave .. of b, 16 a copy (row l / 4, piece l % 4), and 64 rows'
+  // scales of each (of a, with MI = 2, two waves the same ones). Rows past the
+  // end repeat the last one.
+  const int ar = lane >> 3, br = lane >> 2;
+  const int asw = MI == 4 ? wave : (wave & 1);
+  uint32_t va[2 * MI], vb[4], vsa, vsb;
+  const uint8_t *pa, *pb;
+  int cm0, cn0, ct = L, ck = 0;
+  auto set_tile = [&]() {
+    coords(ct, cm0, cn0);
+    pa = g.a + (int64_t)cm0 * Kp;
+    pb = g.b + (int64_t)cn0 * (Kp / 2);
+    const int ma = M - 1 - cm0, nb = N - 1 - cn0;
+#pragma unroll
+    for (int i = 0; i < 2 * MI; ++i)
+      va[i] = (uint32_t)min(wave * (16 * MI) + i * 8 + ar, ma) * (uint32_t)Kp +
+              (((lane & 7) ^ ((4 * i + (ar >> 1)) & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      vb[i] = (uint32_t)min(wave * 64 + i * 16 + br, nb) * (uint32_t)(Kp / 2) +
+              (((lane & 3) ^ ((br >> 2) & 3)) << 4);
+    const int qa = asw * 64 + lane, qb = wave * 64 + lane;
+    vsa = (uint32_t)min(qa / (32 * MI) * C_::WM + qa % MI * 32 + qa / MI % 32, ma) * 4;
+    vsb = (uint32_t)min(qb / 128 * 128 + qb % 4 * 32 + qb / 4 % 32, nb) * 4;
+  };
+  // copy i of the copy state's stage into a slot: CA of a, CB of b, the scales
+  // last
+  auto copy_a = [&](int slot, int i) {
+    char* s = smem + slot * SLOT;
+    if (i < 2 * MI)
+      copy16(pa + (int64_t)ck * 128, va[i], s + (wave * (16 * MI) + i * 8) * 128);
+    else
+      copy4(g.a_sc + ((int64_t)ck * M + cm0) * 4, vsa, s + C_::S + asw * 256);
+  };
+  auto copy_b = [&](int slot, int i) {
+    char* s = smem + slot * SLOT;
+    if (i < 4)
+      copy16(pb + (int64_t)ck * 64, vb[i], s + C_::B + (wave * 64 + i * 16) * 64);
+    else
+      copy4(g.b_sc + ((int64_t)ck * N + cn0) * 4, vsb, s + C_::S + BM * 4 + wave * 256);
+  };
+  auto advance = [&]() {
+    if (++ck == G) {
+      if (ct + step < t_end) {
+        ct += step;
+        ck = 0;
+        set_tile();
+      } else {
+        ck = G - 1;   // past the last stage: it again, into slots not read
+      }
+    }
+  };
+
+  i32x4_t af[2][MI][2], bf[2][4];
+  uint32_t as[MI], bs[4];
+  typedef uint32_t asv_t __attribute__((ext_vector_type(MI)));
+  asv_t asn;
+  u32x4_t bsn;
+  // read i of a substep: 2 MI half fragments of a, 4 fragments of b, then the
+  // stage's scales
+  auto read_one = [&](int slot, int s, int buf, int i) {
+    const char* p = smem + slot * SLOT;
+    if (i < 2 * MI) {
+      const int c = ((4 * s + 2 * (i & 1) + hi) ^ ((l31 >> 1) & 7)) << 4;
+      af[buf][i / 2][i & 1] = *(const i32x4_t*)(p + (wr * C_::WM + i / 2 * 32 + l31) * 128 + c);
+    } else if (i < 2 * MI + 4) {
+      const int c = ((2 * s + hi) ^ ((l31 >> 2) & 3)) << 4, j = i - 2 * MI;
+      bf[buf][j] = *(const i32x4_t*)(p + C_::B + (wc * 128 + j * 32 + l31) * 64 + c);
+    } else if (i == 2 * MI + 4) {
+      asn = *(const asv_t*)(p + C_::S + (wr * 32 + l31) * (4 * MI));
+    } else {
+      bsn = *(const u32x4_t*)(p + C_::S + BM * 4 + (wc * 32 + l31) * 16);
+    }
+  };
+  // the block of substep s is 2 s + hi: shifted so that byte 2 s is it
+  auto take_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) as[i] = asn[i] >> (8 * hi);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bs[j] = bsn[j] >> (8 * hi);
+  };
+  f32x16_t acc[MI][4];
+
+  // A substep's 8 MI MFMAs (of each block of rows the first part with the four
+  // blocks of columns, then the second) with its R reads and C copies spread
+  // over them, the reads over the first half, the copies evenly.
+  auto substep = [&](auto sub, auto reads, auto copies, auto&& read, auto&& copy) {
+    constexpr int S = decltype(sub)::value, R = decltype(reads)::value,
+                  C = decltype(copies)::value, N_ = 8 * MI;
+    i32x8_t p[2];
+    unroll<N_>([&](auto kk) {
+      constexpr int k = decltype(kk)::value, i = k / 8, q = k / 4 % 2, j = k % 4;
+      constexpr int r0 = k < N_ / 2 ? k * R / (N_ / 2) : R;
+      constexpr int r1 = k + 1 <= N_ / 2 ? (k + 1) * R / (N_ / 2) : R;
+      constexpr int c0 = k * C / N_, c1 = (k + 1) * C / N_;
+      if constexpr (k % 8 == 0) parts(af[S][i][0], af[S][i][1], p[0], p[1]);
+      unroll<r1 - r0>([&](auto x) { read(r0 + decltype(x)::value); });
+      unroll<c1 - c0>([&](auto x) { copy(c0 + decltype(x)::value); });
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          p[q], frag(bf[S][j]), acc[i][j], kFp8, kFp4, 2 * S, (int)as[i], 2 * S, (int)bs[j]);
+      if constexpr (r1 > r0) __builtin_amdgcn_sched_group_barrier(0x100, r1 - r0, 0);
+      if constexpr (c1 > c0) __builtin_amdgcn_sched_group_barrier(0x010, c1 - c0, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    });
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  set_tile();
+#pragma unroll
+  for (int p = 0; p < NS - 1; ++p) {
+#pragma unroll
+    for (int i = 0; i < CA; ++i) copy_a(p, i);
+#pragma unroll
+    for (int i = 0; i < CB; ++i) copy_b(p, i);
+    advance();
+  }
+#pragma unroll
+  for (int i = 0; i < CA; ++i) copy_a(NS - 1, i);
+  int slot = 0, pslot = NS - 1;
+  wait_point<wait_imm((NS - 2) * LPS + CA, 15)>();
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < 2 * MI + 6; ++i) read_one(0, 0, 0, i);
+
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    for (int k = 0; k < G; ++k) {
+      const int next = slot + 1 == NS ? 0 : slot + 1;
+      wait_point<wait_imm(63, 0)>();   // fragments of substep 0, scales
+      take_scales();
+      substep(Int<0>{}, Int<2 * MI + 4>{}, Int<CB>{}, [&](int i) { read_one(slot, 1, 1, i); },
+              [&](int i) { copy_b(pslot, i); });
+      advance();
+      wait_point<wait_imm((NS - 2) * LPS, 0)>();
+      asm volatile("s_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      substep(Int<1>{}, Int<2 * MI + 6>{}, Int<CA>{}, [&](int i) { read_one(next, 0, 0, i); },
+              [&](int i) { copy_a(slot, i); });
+      pslot = slot;
+      slot = next;
+    }
+    settle_sums<MI>();
+    int m0, n0;
+    coords(L, m0, n0);
+    O* out = (O*)g.out + (int64_t)(m0 + wr * C_::WM + 4 * hi) * g.ldo + n0 + wc * 128 + l31;
+    const int mleft = M - (m0 + wr * C_::WM + 4 * hi), nleft = N - (n0 + wc * 128 + l31);
+    if (m0 + BM <= M && n0 + BN <= N) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          O* o = out + (int64_t)(i * 32 + 8 * (e / 4) + e % 4) * g.ldo;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) put(o + j * 32, sum_of<MI>(acc[i][j][e]));
+          __builtin_amdgcn_sched_barrier(0);   // not all accumulators into registers first
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int r = i * 32 + 8 * (e / 4) + e % 4;
+          O* o = out + (int64_t)r * g.ldo;
+          if (r < mleft) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (j * 32 < nleft) put(o + j * 32, sum_of<MI>(acc[i][j][e]));
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    L += step;
+    if (L >= t_end) break;
+  }
+  // no copy may land after the workgroup's LDS is another's
+  wait_point<wait_imm(0, 0)>();
+}
+
 template <typename O>
 hipError_t launch(const MxGemmArgs& g, hipStream_t s) {
-  mx8_mid_kernel<1, O><<<dim3((unsigned)((g.N + 63) / 64), (unsigned)((g.M + 31) / 32)), 256,
-                         Mid<1>::LDS, s>>>(g);
+  const int force = getenv("MX8K") ? atoi(getenv("MX8K")) : 0;
+  const unsigned n64 = (unsigned)((g.N + 63) / 64);
+  int k = force;
+  if (!k) k = ((g.M + 255) / 256) * ((g.N + 255) / 256) >= 128 ? 4 : 1;
+  if (g.K == 0 && k > 2) k = 1;
+  if (k == 1)
+    mx8_mid_kernel<1, O><<<dim3(n64, (unsigned)((g.M + 31) / 32)), 256, Mid<1>::LDS, s>>>(g);
+  else if (k == 2)
+    mx8_mid_kernel<2, O><<<dim3(n64, (unsigned)((g.M + 63) / 64)), 256, Mid<2>::LDS, s>>>(g);
+  else if (k == 3)
+    mx8_big_kernel<2, 3, O><<<kCus, 256, Big<2, 3>::LDS, s>>>(g);
+  else
+    mx8_big_kernel<4, 3, O><<<kCus, 256, Big<4, 3>::LDS, s>>>(g);
   return hipGetLastError();
 }
 

@@ -1,24 +1,10 @@
 // Products of two MXFP4 matrices, out = a b^T, by the scaled matrix
 // instructions: every product of two elements is exact, the block scales
 // enter inside the instruction, and the sums are float32.
-#include "mx.hpp"
+#include "mx_gemm.hpp"
 
 namespace sffn {
 namespace {
-
-typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
-constexpr int kFp4 = 4;   // operand format field of the f8f6f4 instructions
-
-// 16 bytes (32 elements) of an operand; the instruction reads the first
-// four registers of a 4-bit operand.
-__device__ __forceinline__ i32x8_t frag(const i32x4_t v) {
-  return i32x8_t{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
-}
-
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(uint16_t* p, float v) {
-  *p = __builtin_bit_cast(uint16_t, (__bf16)v);   // to nearest even; NaN stays NaN
-}
 
 // ---------------------------------------------------------------- few rows
 
@@ -245,10 +231,6 @@ __global__ __launch_bounds__(256) void mx_mid_kernel(MxGemmArgs g) {
 // frees the slot, whose last fragments are in registers), and substep 1
 // multiplies while the next stage's first fragments are read. Every
 // substep starts half a stage of copies, NSLOT stages ahead.
-constexpr int kNXcd = 8;
-constexpr int kCus = 256;
-constexpr int kGroupM = 4;
-
 template <int MI, int NS>
 struct Big {
   static constexpr int BM = 64 * MI, BN = 256, WM = 32 * MI;
@@ -259,28 +241,6 @@ struct Big {
   static constexpr int LDS = NSLOT * SLOT;
   static constexpr int WGS = LDS > 80 * 1024 ? 1 : 2;   // workgroups a CU
 };
-
-// An accumulator at the point of use. 256 of them are in AGPRs: read there,
-// one by one, or the compiler moves (and converts) them all before the
-// epilogue's branch, which spills. (The compiler adds no wait states between
-// a matrix instruction and inline asm that reads its result: see
-// settle_sums.)
-template <int MI>
-__device__ __forceinline__ float sum_of(float a) {
-  if constexpr (MI < 4) return a;
-  float v;
-  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
-  return v;
-}
-
-// Before the first sum_of after a matrix instruction: its result may be read
-// 18 wait states later at the earliest.
-template <int MI>
-__device__ __forceinline__ void settle_sums() {
-  __builtin_amdgcn_sched_barrier(0);
-  if constexpr (MI == 4) asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
 
 template <int MI, int NS, typename O>
 __global__ __launch_bounds__(256, (Big<MI, NS>::WGS)) void mx_big_kernel(MxGemmArgs g) {

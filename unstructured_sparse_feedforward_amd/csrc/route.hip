@@ -10,7 +10,11 @@
 // not of a rounding. Without a bias experts are compared by their logits,
 // which have the order of the scores.
 //
-// A wave has a token, a lane experts lane, 64 + lane, ..
+// A wave has a token, a lane N consecutive experts, from lane N on. Bytes are
+// few (8192 tokens of 256 experts: 8.9 MB, 2 us); the time is that of the
+// waves' instructions, most of them for the k maxima. So a token is first done in
+// 32 bits, with a check that every comparison that matters was clear of the
+// roundings, and in 64 only where one was not (a few tokens in a hundred).
 #include "route.hpp"
 #include "rowio.hpp"
 
@@ -28,11 +32,68 @@ __device__ __forceinline__ long long order_key(double l) {
   const long long b = __double_as_longlong(l + 0.0);
   return b < 0 ? b ^ 0x7FFFFFFFFFFFFFFFll : b;
 }
-constexpr long long kNone = (long long)0x8000000000000000ull;   // below every value's key
+__device__ __forceinline__ int order_key(float l) {
+  if (l != l) return 0x7FC00000;
+  const int b = __float_as_int(l + 0.0f);
+  return b < 0 ? b ^ 0x7FFFFFFF : b;
+}
+__device__ __forceinline__ float key_value(int k) {
+  return __int_as_float(k < 0 ? k ^ 0x7FFFFFFF : k);
+}
+// below every value's key
+constexpr long long kNone64 = (long long)0x8000000000000000ull;
+constexpr int kNone = (int)0x80000000u;
 
 __device__ __forceinline__ float logit(const RouteArgs& a, int64_t t, int e) {
   return a.bf ? bf16lo(((const uint16_t*)a.logits)[t * a.ldl + e])
               : ((const float*)a.logits)[t * a.ldl + e];
+}
+
+// N consecutive elements of a row, those from `left` on as `fill`
+template <int N, typename E>
+__device__ __forceinline__ void load_run(const E* p, int left, float fill, float (&v)[N]) {
+  if (left >= N) {
+    if constexpr (N == 16) {
+      load8(p, v);
+      load8(p + 8, v + 8);
+    } else if constexpr (N == 8) {
+      load8(p, v);
+    } else if constexpr (N == 4) {
+      load4(p, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = ld(p + i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i < left ? ld(p + i) : fill;
+  }
+}
+template <int N, typename E>
+__device__ __forceinline__ void store_run(E* p, int left, const float (&v)[N]) {
+  if (left >= N) {
+    if constexpr (N == 16) {
+      store8(p, v);
+      store8(p + 8, v + 8);
+    } else if constexpr (N == 8) {
+      store8(p, v);
+    } else if constexpr (N == 4) {
+      store4(p, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) st(p + i, v[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < left) st(p + i, v[i]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, float (&l)[N]) {
+  const int e0 = (threadIdx.x & 63) * N;
+  if (a.bf) load_run<N>((const uint16_t*)a.logits + t * a.ldl + e0, a.E - e0, -INFINITY, l);
+  else load_run<N>((const float*)a.logits + t * a.ldl + e0, a.E - e0, -INFINITY, l);
 }
 
 template <typename T>
@@ -41,145 +102,383 @@ __device__ __forceinline__ T wave_sum(T v) {
   for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
   return v;
 }
+// the sum over the first k lanes (0 in the others), in those
+__device__ __forceinline__ double lanes_sum(double v, int k) {
+#pragma unroll 1
+  for (int o = 1; o < k; o <<= 1) v += __shfl_xor(v, o);
+  return v;
+}
+// the largest of the wave, in all lanes: a scan by lanes of a row, then rows
+// into the next ones; the last lane has it
+__device__ __forceinline__ int wave_max(int v) {
+#define SFFN_STEP(ctrl) v = max(v, __builtin_amdgcn_update_dpp(v, v, ctrl, 0xF, 0xF, false))
+  SFFN_STEP(0x111);    // from the lane 1, 2, 4, 8 before, of the same 16
+  SFFN_STEP(0x112);
+  SFFN_STEP(0x114);
+  SFFN_STEP(0x118);
+  SFFN_STEP(0x142);    // the last of a row of 16 to the next row
+  SFFN_STEP(0x143);    // lane 31 to the upper half
+#undef SFFN_STEP
+  return __builtin_amdgcn_readlane(v, 63);
+}
+// (a NaN is ignored)
 __device__ __forceinline__ float wave_max(float v) {
+  return key_value(wave_max(v != v ? kNone : order_key(v)));
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+// the logit of expert e, by lane
+template <int N>
+__device__ __forceinline__ float value_of(const float (&l)[N], int e) {
+  float v = __shfl(l[0], e / N);
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
+  for (int i = 1; i < N; ++i) {
+    const float o = __shfl(l[i], e / N);
+    v = e % N == i ? o : v;
+  }
   return v;
 }
 
-// The scores of the lane's experts in 64 bits. (Of a row without a logit above
-// -infinity they are 0.)
+// The largest of a row's logits; -infinity of an empty one.
 template <int N>
-__device__ __forceinline__ void scores(const RouteArgs& a, const float (&l)[N], double (&s)[N]) {
-  const int lane = threadIdx.x & 63;
-  if (a.sigmoid) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = 1.0 / (1.0 + exp(-(double)l[i]));
-    return;
-  }
+__device__ __forceinline__ float row_max(const float (&l)[N]) {
   float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);   // (a NaN is ignored here)
+  for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
   m = wave_max(m);
-  double sum = 0.0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    s[i] = i * 64 + lane < a.E && m != -INFINITY ? exp((double)l[i] - (double)m) : 0.0;
-    if (l[i] != l[i]) s[i] = l[i];
-    sum += s[i];
-  }
-  sum = wave_sum(sum);
-#pragma unroll
-  for (int i = 0; i < N; ++i) s[i] = sum == 0.0 ? 0.0 : s[i] / sum;
+  return m != m ? -INFINITY : m;     // (every one a NaN)
 }
 
-template <int N>
+// The two largest of a group's c, in all of its lanes: P = 2^lp lanes have a
+// group, and share out its members in LDS. (NaNs are ignored.)
+template <typename T>
+__device__ __forceinline__ void group_best(const RouteArgs& a, const T* cs, int lp, T& b1, T& b2) {
+  const int lane = threadIdx.x & 63;
+  const int g = lane >> lp, p = lane & ((1 << lp) - 1);
+  b1 = b2 = -INFINITY;
+  if (g < a.groups) {
+    for (int j = p; j < a.per; j += 1 << lp) {
+      const T c = cs[g * a.per + j];
+      b2 = fmax(b2, fmin(b1, c));
+      b1 = fmax(b1, c);
+    }
+  }
+  for (int o = 1; o < 1 << lp; o <<= 1) {
+    const T o1 = __shfl_xor(b1, o), o2 = __shfl_xor(b2, o);
+    b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+    b1 = fmax(b1, o1);
+  }
+}
+
+// e / per, by a product that is exact for e < 2^10
+__device__ __forceinline__ int group_of(const RouteArgs& a, int e) {
+  return (int)(((float)e + 0.5f) * a.inv_per);
+}
+// whether the group of expert e is among those kept (a bit for each lane)
+__device__ __forceinline__ bool kept(const RouteArgs& a, uint64_t keep, int lp, int e) {
+  return (keep >> (group_of(a, e) << lp)) & 1;
+}
+
+// What a token needs in 64 bits where 32 cannot tell: small code, rolled over
+// the row in LDS, since a wave that needs it fetches it first, and alone.
+
+// c of the token's experts, lane, 64 + lane, .. of each lane, into cs; of
+// groups the lanes of those that are kept, a bit for each.
+template <bool BIAS, bool GROUPED>
+__device__ __forceinline__ uint64_t scores64(const RouteArgs& a, int64_t t, float m, double* cs,
+                                             int lp) {
+  const int lane = threadIdx.x & 63;
+  double sum = 1.0;
+  if (!a.sigmoid) {
+    sum = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64) {
+      const float l = logit(a, t, e);
+      if (m != -INFINITY || l != l) sum += exp((double)l - (double)m);
+    }
+    sum = wave_sum(sum);
+  }
+  uint64_t nan = 0;      // the groups of the lane's NaNs
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 64) {
+    const double l = logit(a, t, e);
+    const double x = exp(a.sigmoid ? -l : l - (double)m);
+    // (of a row without a logit above -infinity the scores are 0)
+    double c = a.sigmoid ? 1.0 / (1.0 + x) : sum == 0.0 ? 0.0 : x / sum;
+    if (BIAS) c += (double)a.bias[e];
+    if (c != c) nan |= 1ull << group_of(a, e);
+    cs[e] = c;
+  }
+  if (!GROUPED) return ~0ull;
+  __builtin_amdgcn_wave_barrier();     // (a wave's own part of LDS)
+  double b1, b2;
+  group_best<double>(a, cs, lp, b1, b2);
+  const int mine = lane >> lp;
+#pragma unroll 1
+  for (int o = 1; o < 64; o <<= 1) nan |= __shfl_xor(nan, o);
+  // a group with a NaN is above the others
+  const long long gk = order_key((nan >> mine) & 1 ? (double)NAN : a.best == 2 ? b1 + b2 : b1);
+  int before = 0;
+#pragma unroll 1
+  for (int g = 0; g < a.groups; ++g) {
+    const long long o = __shfl(gk, g << lp);
+    before += o > gk || (o == gk && g < mine);
+  }
+  return __ballot(mine < a.groups && before < a.top_groups);
+}
+
+// The token's experts: lane r returns that of rank r.
+template <bool BIAS, bool GROUPED>
+__device__ __forceinline__ int choose64(const RouteArgs& a, int64_t t, float m, double* cs,
+                                        int lp) {
+  const int lane = threadIdx.x & 63;
+  const uint64_t keep = scores64<BIAS, GROUPED>(a, t, m, cs, lp);
+  long long* key = (long long*)cs;
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 64)
+    key[e] = !GROUPED || kept(a, keep, lp, e)
+                 ? order_key(BIAS ? cs[e] : (double)logit(a, t, e)) : kNone64;
+  int id = 0;
+#pragma unroll 1
+  for (int r = 0; r < a.k; ++r) {
+    long long bk = kNone64;
+    int be = lane;
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64)
+      if (key[e] > bk) {
+        bk = key[e];
+        be = e;
+      }
+    // the largest upper halves, of these the lower halves, of these the expert
+    const int hi = (int)(bk >> 32), top = wave_max(hi);
+    const int lo = hi == top ? (int)((uint32_t)bk ^ 0x80000000u) : kNone, low = wave_max(lo);
+    be = -wave_max(hi == top && lo == low ? -be : kNone);
+    if (lane == (be & 63)) key[be] = kNone64;
+    if (lane == r) id = be;
+  }
+  return id;
+}
+
+// The same from comparisons in 32 bits; *sure: the result is that of 64 bits.
+//
+// With u = 2^-24: the hardware's exponential of x log2 e is off by (2 |x| + 3) u
+// of itself. A sigmoid score is off by s (1 - s) (2 |l| + 3) u, at most 2 u, and
+// a sum and a reciprocal: 4 u. Softmax scores are off by at most 60 u of the
+// largest: (2 |x| + 3) e^x <= 4 for the exponential, x = l - m, u |x| more for
+// the difference; their sum, whose average of |x| is at most log 1024 = 7, by
+// (24 + 16 + 6) u; a reciprocal and a product. c is off by u |c| more. So two c
+// whose difference is more than 2^-20 (2^-16 times the largest score) + 2^-23
+// times their size are in the order of the exact ones, and two sums of two
+// where it is more than twice that and 2^-22 times their size. Without a bias the experts' keys are the
+// logits themselves, which are exact.
+template <int N, bool BIAS, bool GROUPED>
+__device__ __forceinline__ int choose32(const RouteArgs& a, int64_t t, const float (&l)[N],
+                                        float m, double* cs64, int lp, bool* sure) {
+  constexpr float kLog2e = 1.44269504f;
+  const int lane = threadIdx.x & 63, e0 = lane * N;
+  float* cs = (float*)cs64;
+  int key[N];
+  bool clear = true;
+  float room = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) key[i] = e0 + i < a.E ? order_key(l[i]) : kNone;
+  if (BIAS || GROUPED) {
+    float c[N];
+    if (a.sigmoid) {
+      room = 0x1p-20f;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * l[i]));
+    } else {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        c[i] = __builtin_amdgcn_exp2f(kLog2e * (l[i] - m));    // (m = -infinity: NaN)
+        sum += c[i];
+      }
+      const float inv = __builtin_amdgcn_rcpf(wave_sum(sum));
+#pragma unroll
+      for (int i = 0; i < N; ++i) c[i] *= inv;
+      room = 0x1p-16f * inv;
+    }
+    if (BIAS) {
+      float b[N];
+      load_run<N>(a.bias + e0, a.E - e0, 0.0f, b);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        c[i] += b[i];
+        key[i] = e0 + i < a.E ? order_key(c[i]) : kNone;
+      }
+    }
+    if (GROUPED) {
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        cs[e0 + i] = c[i];
+        nan |= c[i] != c[i];
+      }
+      __builtin_amdgcn_wave_barrier();     // (a wave's own part of LDS)
+      float b1, b2;
+      group_best<float>(a, cs, lp, b1, b2);
+      const float score = a.best == 2 ? b1 + b2 : b1;
+      const int gk = order_key(score), mine = lane >> lp;
+      int before = 0;
+#pragma unroll 4
+      for (int g = 0; g < a.groups; ++g) {
+        const int o = __builtin_amdgcn_readlane(gk, g << lp);
+        before += o > gk || (o == gk && g < mine);
+      }
+      const bool valid = mine < a.groups, stays = valid && before < a.top_groups;
+      uint64_t keep = __ballot(stays);
+      // the last that is kept and the first that is not
+      const float low = -wave_max(stays ? -score : -INFINITY);
+      const float high = wave_max(valid && !stays ? score : -INFINITY);
+      if (!(low - high > 2.0f * room + 0x1p-22f * (fabsf(low) + fabsf(high))) ||
+          __ballot(nan) != 0)
+        keep = scores64<BIAS, GROUPED>(a, t, m, cs64, lp);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (!kept(a, keep, lp, e0 + i)) key[i] = kNone;
+    }
+  }
+  // The k largest, one after the other, and with a bias more until one is
+  // clearly less than the last: lane r takes that of rank r. Of equal keys the
+  // lower index is first.
+  constexpr bool SORT = N > 1 && N <= 4;      // the lane's own keys, descending
+  uint32_t at = 0;                            // and whose they are, 2 bits each
+  if constexpr (SORT) {
+    int idx[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) idx[i] = i;
+#pragma unroll
+    for (int p = 0; p < N; ++p)
+#pragma unroll
+      for (int i = p & 1; i + 1 < N; i += 2) {
+        const bool swap = key[i + 1] > key[i];
+        const int k0 = key[i], i0 = idx[i];
+        key[i] = swap ? key[i + 1] : k0;
+        idx[i] = swap ? idx[i + 1] : i0;
+        key[i + 1] = swap ? k0 : key[i + 1];
+        idx[i + 1] = swap ? i0 : idx[i + 1];
+      }
+#pragma unroll
+    for (int i = 0; i < N; ++i) at |= idx[i] << (2 * i);
+  }
+  int id = 0, n = a.k;
+  bool ties = false;
+  float last = INFINITY;
+#pragma unroll 1
+  for (int r = 0;; ++r) {
+    int bk = key[0];
+    if constexpr (!SORT) {
+#pragma unroll
+      for (int i = 1; i < N; ++i) bk = max(bk, key[i]);
+    }
+    if (!BIAS && r == a.k) break;
+    const int best = wave_max(bk);
+    if (BIAS) {
+      const float v = key_value(best);
+      const bool apart = r == 0 || last - v > room + 0x1p-23f * (fabsf(last) + fabsf(v));
+      if (r >= a.k && (apart || best == kNone)) {
+        n = r;
+        break;
+      }
+      if (r == 63) {      // no lane for more
+        clear = false;
+        break;
+      }
+      ties |= !apart;
+      last = v;
+    }
+    const int who = __ffsll((unsigned long long)__ballot(bk == best)) - 1;
+    int j = 0;
+    if constexpr (SORT) {
+      j = at & 3;
+    } else {
+      j = N - 1;
+#pragma unroll
+      for (int i = N - 2; i >= 0; --i) j = key[i] == best ? i : j;
+    }
+    j = __builtin_amdgcn_readlane(j, who);
+    if (lane == r) id = who * N + j;
+    if constexpr (SORT) {
+      const bool mine = lane == who;
+#pragma unroll
+      for (int i = 0; i + 1 < N; ++i) key[i] = mine ? key[i + 1] : key[i];
+      key[N - 1] = mine ? kNone : key[N - 1];
+      at >>= mine ? 2 : 0;
+    } else {
+      const int drop = lane == who ? j : -1;
+#pragma unroll
+      for (int i = 0; i < N; ++i) key[i] = drop == i ? kNone : key[i];
+    }
+  }
+  if (BIAS && ties && clear) {
+    // The n found hold the k, but not for sure in their order: theirs in 64 bits.
+    // (Softmax scores need the sum over the row.)
+    if (!a.sigmoid) {
+      clear = false;
+    } else {
+      const double c = 1.0 / (1.0 + exp(-(double)value_of<N>(l, id))) + (double)a.bias[id];
+      const long long mine = order_key(c);
+      int before = 0;
+#pragma unroll 1
+      for (int q = 0; q < n; ++q) {
+        const uint32_t lo = __builtin_amdgcn_readlane((int)mine, q);
+        const long long hi = __builtin_amdgcn_readlane((int)(mine >> 32), q);
+        const long long o = hi << 32 | lo;
+        before += o > mine || (o == mine && __builtin_amdgcn_readlane(id, q) < id);
+      }
+      id = __builtin_amdgcn_ds_permute((lane < n ? before : lane) << 2, id);
+    }
+  }
+  *sure = clear;
+  return id;
+}
+
+template <int N, bool BIAS, bool GROUPED>
 __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs a) {
-  __shared__ double cs[kWaves][N * 64];
+  __shared__ double cs[kWaves][BIAS || GROUPED ? N * 64 : 1];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
   if (t >= a.T || (a.t_dev && t >= *a.t_dev)) return;
   float l[N];
+  load_logits<N>(a, t, l);
+  const float m = a.sigmoid ? 0.0f : row_max<N>(l);
+  // 2^lp lanes a group
+  const int lp = GROUPED ? __builtin_clz(a.groups - 1) - 26 : 6;
+  bool sure;
+  int id = choose32<N, BIAS, GROUPED>(a, t, l, m, cs[wave], lp, &sure);
+  if (BIAS && !sure) id = choose64<BIAS, GROUPED>(a, t, m, cs[wave], lp);
+  // the weights, of the k experts alone where that is all they depend on
+  double sr = 0.0, sum;
+  const float v = value_of<N>(l, id), lr = lane < a.k ? v : -INFINITY;
+  if (a.sigmoid) {
+    sr = lane < a.k ? 1.0 / (1.0 + exp(-(double)lr)) : 0.0;
+    sum = a.normalize ? lanes_sum(sr, a.k) : 1.0;
+  } else {
+    // normalised: relative to the chosen ones' largest logit, since a bias may
+    // choose experts whose scores are nothing beside the others'
+    const float top = a.normalize ? wave_max(lr) : m;
+    const bool some = top == top && top != -INFINITY;
+    sr = some && lane < a.k ? exp((double)lr - (double)top) : 0.0;
+    if (lr != lr) sr = lr;
+    if (a.normalize) {
+      sum = lanes_sum(sr, a.k);
+    } else {
+      sum = 0.0;
+      const int e0 = lane * N;
 #pragma unroll
-  for (int i = 0; i < N; ++i) l[i] = i * 64 + lane < a.E ? logit(a, t, i * 64 + lane) : -INFINITY;
-  double s[N];
-  scores<N>(a, l, s);
-  long long key[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = i * 64 + lane;
-    key[i] = e < a.E ? order_key(a.bias ? s[i] + (double)a.bias[e] : (double)l[i]) : kNone;
-  }
-  if (a.top_groups < a.groups) {
-    // (a wave's own part of LDS: no barrier)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = i * 64 + lane;
-      cs[wave][e] = a.bias && e < a.E ? s[i] + (double)a.bias[e] : s[i];
+      for (int i = 0; i < N; ++i)
+        if (e0 + i < a.E && (some || l[i] != l[i])) sum += exp((double)l[i] - (double)m);
+      sum = wave_sum(sum);
     }
-    __builtin_amdgcn_wave_barrier();
-    long long gk = kNone;
-    if (lane < a.groups) {
-      double b1 = -INFINITY, b2 = -INFINITY;
-      bool nan = false;
-      for (int j = 0; j < a.per; ++j) {
-        const double c = cs[wave][lane * a.per + j];
-        nan |= c != c;
-        if (c > b1) {
-          b2 = b1;
-          b1 = c;
-        } else if (c > b2) {
-          b2 = c;
-        }
-      }
-      gk = order_key(nan ? NAN : a.best == 2 ? b1 + b2 : b1);
-    }
-    int before = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const long long o = __shfl(gk, g);
-      before += o > gk || (o == gk && g < lane);
-    }
-    const uint64_t keep = __ballot(lane < a.groups && before < a.top_groups);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = i * 64 + lane;
-      if (e < a.E && !((keep >> (e / a.per)) & 1)) key[i] = kNone;
-    }
-  }
-  // the k largest, one after the other; lane r takes that of rank r
-  int id = 0;
-  float lr = -INFINITY;
-  double sr = 0.0;
-  for (int r = 0; r < a.k; ++r) {
-    long long bk = key[0];
-    int bi = 0;
-#pragma unroll
-    for (int i = 1; i < N; ++i)
-      if (key[i] > bk) {
-        bk = key[i];
-        bi = i;
-      }
-    int be = bi * 64 + lane;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const long long ok = __shfl_xor(bk, o);
-      const int oe = __shfl_xor(be, o);
-      if (ok > bk || (ok == bk && oe < be)) {
-        bk = ok;
-        be = oe;
-      }
-    }
-    double sv = 0.0;
-    float lv = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i == be >> 6) {
-        sv = s[i];
-        lv = l[i];
-        if (lane == (be & 63)) key[i] = kNone;
-      }
-    sv = __shfl(sv, be & 63);
-    lv = __shfl(lv, be & 63);
-    if (lane == r) {
-      id = be;
-      sr = sv;
-      lr = lv;
-    }
-  }
-  if (a.normalize) {
-    if (!a.sigmoid) {
-      // relative to the chosen ones' largest logit: a bias may choose experts
-      // whose scores are nothing beside the others'
-      const float m = wave_max(lane < a.k ? lr : -INFINITY);
-      const double ex = lane < a.k && m != -INFINITY ? exp((double)lr - (double)m) : 0.0;
-      sr = lane < a.k && lr != lr ? (double)lr : ex;
-    }
-    const double sum = wave_sum(lane < a.k ? sr : 0.0);
-    sr = sum == 0.0 ? 0.0 : sr / sum;
   }
   if (lane < a.k) {
     a.ids[t * a.k + lane] = id;
-    a.probs[t * a.k + lane] = (float)(sr * (double)a.scale);
+    a.probs[t * a.k + lane] = sum == 0.0 ? 0.0f : (float)(sr / sum * (double)a.scale);
   }
 }
 
@@ -191,9 +490,12 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs a) {
 // dl_r = q_r (g_r - sum g q), nothing for the others.
 template <int N>
 __global__ __launch_bounds__(kWaves * 64) void route_grad_kernel(RouteArgs a) {
-  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int lane = threadIdx.x & 63, wave = wave_id(), e0 = lane * N;
   const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
   if (t >= a.T || (a.t_dev && t >= *a.t_dev)) return;
+  const bool all = !a.sigmoid && !a.normalize;
+  float l[N];
+  if (all) load_logits<N>(a, t, l);
   // lane r: the expert of rank r (none where the index is not one)
   int id = -1;
   float g = 0.0f, lr = -INFINITY;
@@ -205,18 +507,12 @@ __global__ __launch_bounds__(kWaves * 64) void route_grad_kernel(RouteArgs a) {
       lr = logit(a, t, id);
     }
   }
-  const bool all = !a.sigmoid && !a.normalize;
-  float l[N], m = 0.0f, total = 0.0f, dr;
+  float total = 0.0f, dr;
   if (all) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) l[i] = i * 64 + lane < a.E ? logit(a, t, i * 64 + lane) : -INFINITY;
-    m = l[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) m = fmaxf(m, l[i]);
-    m = wave_max(m);
+    const float m = row_max<N>(l);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      l[i] = i * 64 + lane < a.E && m != -INFINITY ? expf(l[i] - m) : 0.0f;
+      l[i] = e0 + i < a.E && m != -INFINITY ? expf(l[i] - m) : 0.0f;
       total += l[i];
     }
     total = wave_sum(total);
@@ -237,27 +533,25 @@ __global__ __launch_bounds__(kWaves * 64) void route_grad_kernel(RouteArgs a) {
     }
     dr *= s * c;
   } else {
-    m = wave_max(lr);
-    const float ex = id >= 0 && m != -INFINITY ? expf(lr - m) : 0.0f;
+    const float m = wave_max(lr);
+    const float ex = id >= 0 && m == m && m != -INFINITY ? expf(lr - m) : 0.0f;
     const float S = wave_sum(ex);
     const float q = S == 0.0f ? 0.0f : ex / S;
     dr = q * (g - wave_sum(g * q));
   }
   float d[N] = {};
   for (int r = 0; r < a.k; ++r) {
-    const int e = __shfl(id, r);
-    const float v = __shfl(dr, r);
+    const int e = __builtin_amdgcn_readlane(id, r) - e0;
+    const float v = lane_value(dr, r);
 #pragma unroll
-    for (int i = 0; i < N; ++i) d[i] += e == i * 64 + lane ? v : 0.0f;
+    for (int i = 0; i < N; ++i) d[i] += e == i ? v : 0.0f;
   }
+  if (all) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = i * 64 + lane;
-    if (e >= a.E) break;
-    const float v = all ? l[i] * (d[i] - total) : d[i];
-    if (a.dl_bf) st((uint16_t*)a.dl + t * a.lddl + e, v);
-    else st((float*)a.dl + t * a.lddl + e, v);
+    for (int i = 0; i < N; ++i) d[i] = l[i] * (d[i] - total);
   }
+  if (a.dl_bf) store_run<N>((uint16_t*)a.dl + t * a.lddl + e0, a.E - e0, d);
+  else store_run<N>((float*)a.dl + t * a.lddl + e0, a.E - e0, d);
 }
 
 template <typename F>
@@ -275,7 +569,12 @@ hipError_t by_experts(int E, F&& f) {
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   const unsigned grid = (unsigned)((a.T + kWaves - 1) / kWaves);
   return by_experts(a.E, [&](auto n) {
-    route_kernel<decltype(n)::value><<<grid, kWaves * 64, 0, s>>>(a);
+    constexpr int N = decltype(n)::value;
+    const bool grouped = a.top_groups < a.groups;
+    if (a.bias && grouped) route_kernel<N, true, true><<<grid, kWaves * 64, 0, s>>>(a);
+    else if (a.bias) route_kernel<N, true, false><<<grid, kWaves * 64, 0, s>>>(a);
+    else if (grouped) route_kernel<N, false, true><<<grid, kWaves * 64, 0, s>>>(a);
+    else route_kernel<N, false, false><<<grid, kWaves * 64, 0, s>>>(a);
   });
 }
 hipError_t launch_route_grad(const RouteArgs& a, hipStream_t s) {

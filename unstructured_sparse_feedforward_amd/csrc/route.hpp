@@ -18,6 +18,7 @@ struct RouteArgs {
   int E, k, groups, per, top_groups, best;   // per: experts a group
   int sigmoid, normalize, bf;
   float scale;
+  float inv_per;             // 1 / per
   int32_t* ids;              // [T, k]
   float* probs;              // [T, k]
   // backward

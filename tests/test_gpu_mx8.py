@@ -99,7 +99,8 @@ SHAPES = [(1, 1, 1), (1, 5, 32), (1, 300, 2048), (3, 33, 129), (15, 64, 96), (16
           (16, 1000, 4224), (17, 65, 257), (32, 64, 640), (33, 130, 1003), (64, 64, 64),
           (65, 257, 300), (100, 1000, 2000), (129, 513, 1999), (256, 256, 256), (300, 900, 1152),
           (512, 2048, 640), (1000, 2100, 512), (1024, 4096, 256), (2100, 4100, 131),
-          (4096, 2304, 1280)]
+          (4096, 2304, 1280), (9, 14400, 4100), (16, 16384, 4200), (7, 14400, 4100),
+          (2600, 4200, 1500), (4000, 3300, 1100), (5000, 5000, 1030)]
 
 
 def _product(a, b):
@@ -125,16 +126,16 @@ def test_product(M, N, K, dtype):
     assert torch.equal(out, sffn.mx_matmul(a, b, dtype=dtype))
 
 
-def _wide(M, K, seed):
-    """Codes of a whose products with +-0.5 .. 6 and their sums are all
+def _wide(M, K, seed, every):
+    """Codes of a whose products with +-0.5 or 1.5 and their sums are all
     multiples of 2^-10 below 2^13: exact in float32 in any order. In every
-    run of 8 one element is 256, the others are at most 2^-4 and go down to
-    the smallest, 2^-9."""
+    (of long rows, every eighth) run of 8 one element is 256, the others are at
+    most 2^-4 and go down to the smallest, 2^-9."""
     g = np.random.default_rng(seed)
     c = g.integers(0, 24, (M, K)).astype(np.uint8)       # 0 .. 15 / 8 2^-5
     big = g.integers(0, 8, (M, -(-K // 8)))
     sign = g.integers(0, 2, (M, K)).astype(np.uint8) << 7
-    for i in range(big.shape[1]):
+    for i in range(0, big.shape[1], every):
         k = np.minimum(i * 8 + big[:, i], K - 1)
         c[np.arange(M), k] = (8 + 7) << 3
     return c | sign
@@ -142,10 +143,11 @@ def _wide(M, K, seed):
 
 @pytest.mark.parametrize("M,N,K", [(1, 64, 128), (5, 100, 128), (16, 33, 250), (33, 64, 128),
                                    (100, 300, 96), (300, 1100, 128), (700, 2100, 160),
-                                   (2304, 4352, 128), (4100, 4100, 100)])
+                                   (2304, 4352, 128), (4100, 4100, 100), (3, 200, 4200),
+                                   (10, 16300, 4200), (4000, 3300, 1100)])
 def test_wide_exponents_lose_nothing(M, N, K):
     """Large and small elements side by side: exact sums come out exactly."""
-    c = _wide(M, K, M + N + K)
+    c = _wide(M, K, M + N + K, 1 if K < 300 else 32 if K > 4000 else 8)
     q = m8.pack(c, np.zeros((M, -(-K // 32)), np.int64))
     a = sffn.MX8Tensor(torch.from_numpy(q[0]).cuda(), torch.from_numpy(q[1]).cuda(), M, K)
     g = np.random.default_rng(N)

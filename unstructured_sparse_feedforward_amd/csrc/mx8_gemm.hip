@@ -17,7 +17,6 @@
 // below the part's largest exponent, e2m1's at most 3 (0.5 under 4), 13 in
 // all, so that nothing is cut and only float32 additions round, as in the
 // rest of the library.
-#include <cstdlib>
 #include "mx_gemm.hpp"
 
 namespace sffn {
@@ -29,42 +28,139 @@ namespace {
 
 // The two parts of an 8-bit operand: the bytes with bit 6 (an exponent field of
 // 8 or more), and the others.
+__device__ __forceinline__ void part(uint32_t x, int32_t& hi, int32_t& lo) {
+  // bit 6 of bytes 1 and 3 to bits 15 and 31, of bytes 0 and 2 as well: the
+  // permutation's selectors 8 to 11 fill a byte with one of those
+  const uint32_t m = __builtin_amdgcn_perm(x << 1, x << 9, 0x0B090A08u);
+  hi = (int32_t)(x & m);
+  lo = (int32_t)(x & ~m);
+}
 __device__ __forceinline__ void parts(const i32x4_t a, const i32x4_t b, i32x8_t& hi, i32x8_t& lo) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t x = (uint32_t)(i < 4 ? a[i & 3] : b[i & 3]);
-    const uint32_t t = x & 0x40404040u;
-    const uint32_t m = (t << 2) - (t >> 6);   // 0xFF in the bytes with bit 6
-    hi[i] = (int32_t)(x & m);
-    lo[i] = (int32_t)(x & ~m);
+    int32_t h, l;
+    part((uint32_t)(i < 4 ? a[i & 3] : b[i & 3]), h, l);
+    hi[i] = h;
+    lo[i] = l;
   }
+}
+
+// ---------------------------------------------------------------- few rows
+
+// M <= 16 rows of a: one workgroup for 16 rows of b, whose W waves share out K
+// by 128-wide groups, each with a ring of its own in LDS, and add their sums
+// in LDS. The rows of b are the instruction's first operand: lane l holds row
+// l % 16 of either, and of the result four consecutive n of row m = l % 16. A
+// slot holds the 16 rows of b and those of a in the pieces of the small tiles,
+// then their scale dwords.
+constexpr int kFewSlots = 2;
+constexpr int kFewA = 1024, kFewS = kFewA + 2048;   // a's rows, the scales
+constexpr int kFewSlot = kFewS + 2 * 256;           // 64 dwords of scales of either
+constexpr int kFewRing = kFewSlots * kFewSlot;
+
+template <int W, typename O>
+__global__ __launch_bounds__(W * 64) void mx8_few_kernel(MxGemmArgs g) {
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kq = lane >> 4, l15 = lane & 15;
+  const int64_t Kp = mx_padded(g.K);
+  const int G = (int)(Kp / 128);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  char* ring = smem + wave * kFewRing;
+
+  // rows past the end repeat the last one
+  const int ar = lane >> 3, br = lane >> 2;
+  const int ma = (int)g.M - 1, nb = (int)min(g.N - 1 - n0, (int64_t)15);
+  uint32_t va[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    va[i] = (uint32_t)min(i * 8 + ar, ma) * (uint32_t)Kp +
+            (((lane & 7) ^ ((4 * i + (ar >> 1)) & 7)) << 4);
+  const uint32_t vb = (uint32_t)min(br, nb) * (uint32_t)(Kp / 2) +
+                      (((lane & 3) ^ ((br >> 2) & 3)) << 4);
+  const uint32_t vsa = (uint32_t)min(l15, ma) * 4, vsb = (uint32_t)min(l15, nb) * 4;
+  const uint8_t* pb = g.b + n0 * (Kp / 2);
+  auto copy = [&](int t, int slot) {
+    char* s = ring + slot * kFewSlot;
+    copy16(pb + (int64_t)t * 64, vb, s);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) copy16(g.a + (int64_t)t * 128, va[i], s + kFewA + i * 1024);
+    copy4(g.b_sc + ((int64_t)t * g.N + n0) * 4, vsb, s + kFewS);
+    copy4(g.a_sc + (int64_t)t * g.M * 4, vsa, s + kFewS + 256);
+  };
+  f32x4_t acc = {};
+  // a wave's groups are wave, wave + W, ..; past the last it copies that
+  // again, so that the number of copies in flight is always the same
+  const int mine = G > wave ? (G - wave + W - 1) / W : 0;
+  const int last = wave + W * (mine - 1);
+  if (mine > 0) {
+#pragma unroll
+    for (int p = 0; p < kFewSlots; ++p) copy(min(wave + W * p, last), p);
+    int slot = 0;
+    for (int q = 0; q < mine; ++q) {
+      // the oldest slot's copies have landed
+      wait_point<wait_imm((kFewSlots - 1) * 5, 15)>();
+      const char* s = ring + slot * kFewSlot;
+      const i32x4_t bv = *(const i32x4_t*)(s + l15 * 64 + ((kq ^ ((l15 >> 2) & 3)) << 4));
+      const char* pa = s + kFewA + l15 * 128;
+      const i32x4_t a0 = *(const i32x4_t*)(pa + ((kq ^ ((l15 >> 1) & 7)) << 4));
+      const i32x4_t a1 = *(const i32x4_t*)(pa + (((4 + kq) ^ ((l15 >> 1) & 7)) << 4));
+      const int bs = *(const uint8_t*)(s + kFewS + l15 * 4 + kq);
+      const int as = *(const uint8_t*)(s + kFewS + 256 + l15 * 4 + kq);
+      // everything read before the slot is written again
+      wait_point<wait_imm(63, 0)>();
+      copy(min(wave + W * (q + kFewSlots), last), slot);
+      i32x8_t p[2];
+      parts(a0, a1, p[0], p[1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(bv), p[i], acc, kFp4, kFp8, 0,
+                                                               bs, 0, as);
+      slot = slot + 1 == kFewSlots ? 0 : slot + 1;
+    }
+  }
+  // a wave's ring takes its sums once its copies have landed
+  wait_point<wait_imm(0, 0)>();
+  *(f32x4_t*)(ring + lane * 16) = acc;
+  __syncthreads();
+  if (threadIdx.x >= 256) return;
+  // output (m, n) is value n % 4 of lane 16 (n / 4) + m
+  const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
+  const char* r = smem + (16 * (n >> 2) + m) * 16 + (n & 3) * 4;
+  float sum = *(const float*)r;
+#pragma unroll
+  for (int w = 1; w < W; ++w) sum += *(const float*)(r + w * kFewRing);
+  if (m < g.M && n <= nb) put((O*)g.out + m * g.ldo + n0 + n, sum);
 }
 
 // ---------------------------------------------------------------- small tiles
 
 // A (32 I) x 64 tile a workgroup, whose four waves share out K by 128-wide
-// groups, each with a ring of its own in LDS, filled by direct copies kMidSlots
-// groups ahead: nothing is shared before the sums, so there is no barrier in
-// the loop, only the wave's wait for its own oldest copies. A slot holds the
-// rows' codes, a's (128 bytes) and then b's (64): 16-byte piece c of row r of a
-// at position c ^ (r / 2) % 8, of b at c ^ (r / 4) % 4 (so that 16 lanes
-// reading one piece of 16 rows meet different banks), then their scale
-// dwords. Lane l holds row l % 32 of a 32-row block of either.
-constexpr int kMidSlots = 2;
-
-template <int I>
+// groups, each with a ring of its own in LDS, filled by direct copies: nothing
+// is shared before the sums, so there is no barrier in the loop, only the
+// wave's wait for its own oldest copies. A slot holds the rows' codes, a's (128
+// bytes) and then b's (64): 16-byte piece c of row r of a at position c ^ (r /
+// 2) % 8, of b at c ^ (r / 4) % 4 (so that 16 lanes reading one piece of 16
+// rows meet different banks), then their scale dwords. Lane l holds row l % 32
+// of a 32-row block of either.
+//
+// A group is multiplied from registers while the next one is read into others;
+// halfway, the next one's slot takes the copies of the group NS after it.
+template <int I, int NS>
 struct Mid {
   static constexpr int TM = 32 * I;
   static constexpr int B = TM * 128, S = B + 64 * 64;   // b's rows, the scales
   static constexpr int SLOT = S + 512;         // 64 dwords of scales of either operand
   static constexpr int LPS = 4 * I + 4 + 2;    // copies a group
-  static constexpr int RING = 4 * kMidSlots * SLOT;
+  static constexpr int RING = 4 * NS * SLOT;
   static constexpr int LDS = RING > 4 * TM * 64 * 4 ? RING : 4 * TM * 64 * 4;
+  static constexpr int WGS = LDS > 80 * 1024 ? 1 : 2;   // workgroups a CU
 };
 
-template <int I, typename O>
-__global__ __launch_bounds__(256) void mx8_mid_kernel(MxGemmArgs g) {
-  typedef Mid<I> C_;
+template <int I, int NS, typename O>
+__global__ __launch_bounds__(256, (Mid<I, NS>::WGS)) void mx8_mid_kernel(MxGemmArgs g) {
+  typedef Mid<I, NS> C_;
   constexpr int TM = C_::TM, SLOT = C_::SLOT, LPS = C_::LPS;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x & 63;
@@ -73,7 +169,7 @@ __global__ __launch_bounds__(256) void mx8_mid_kernel(MxGemmArgs g) {
   const int64_t Kp = mx_padded(g.K);
   const int G = (int)(Kp / 128);
   const int64_t n0 = (int64_t)blockIdx.x * 64, m0 = (int64_t)blockIdx.y * TM;
-  char* ring = smem + wave * (kMidSlots * SLOT);
+  char* ring = smem + wave * (NS * SLOT);
 
   // rows past the end repeat the last one
   const int ar = lane >> 3, br = lane >> 2;
@@ -91,70 +187,109 @@ __global__ __launch_bounds__(256) void mx8_mid_kernel(MxGemmArgs g) {
   const uint32_t vsb = (uint32_t)min(lane, nb) * 4;
   const uint8_t* pa = g.a + m0 * Kp;
   const uint8_t* pb = g.b + n0 * (Kp / 2);
-  // (the scales of TM < 64 rows with repetitions)
-  auto copy = [&](int t, int slot) {
+  i32x4_t av[2][I][4], bv[2][2][2];
+  uint32_t as[2][I], bs[2][2];
+  // read i of a group: 4 I pieces of a (k = 32 c + 16 hi .. + 15), 4 of b (k =
+  // 64 h + 32 hi .. + 31), the scales
+  constexpr int R = 4 * I + 4 + I + 2;
+  auto read_one = [&](auto bb, int slot, auto ii) {
+    constexpr int b = decltype(bb)::value, i = decltype(ii)::value;
+    const char* s = ring + slot * SLOT;
+    if constexpr (i < 4 * I) {
+      av[b][i / 4][i % 4] = *(const i32x4_t*)(s + (i / 4 * 32 + l31) * 128 +
+                                              (((2 * (i % 4) + hi) ^ ((l31 >> 1) & 7)) << 4));
+    } else if constexpr (i < 4 * I + 4) {
+      constexpr int j = (i - 4 * I) / 2, h = (i - 4 * I) % 2;
+      bv[b][j][h] = *(const i32x4_t*)(s + C_::B + (j * 32 + l31) * 64 +
+                                      (((2 * h + hi) ^ ((l31 >> 2) & 3)) << 4));
+    } else if constexpr (i < 5 * I + 4) {
+      as[b][i - 4 * I - 4] = *(const uint32_t*)(s + C_::S + ((i - 4 * I - 4) * 32 + l31) * 4);
+    } else {
+      constexpr int j = i - 5 * I - 4;
+      bs[b][j] = *(const uint32_t*)(s + C_::S + 256 + (j * 32 + l31) * 4);
+    }
+  };
+  // copy i of a group
+  auto copy_one = [&](int t, int slot, auto ii) {
+    constexpr int i = decltype(ii)::value;
     char* s = ring + slot * SLOT;
-#pragma unroll
-    for (int i = 0; i < 4 * I; ++i) copy16(pa + (int64_t)t * 128, va[i], s + i * 1024);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) copy16(pb + (int64_t)t * 64, vb[i], s + C_::B + i * 1024);
-    copy4(g.a_sc + ((int64_t)t * g.M + m0) * 4, vsa, s + C_::S);
-    copy4(g.b_sc + ((int64_t)t * g.N + n0) * 4, vsb, s + C_::S + 256);
+    if constexpr (i < 4 * I)
+      copy16(pa + (int64_t)t * 128, va[i], s + i * 1024);
+    else if constexpr (i < 4 * I + 4)
+      copy16(pb + (int64_t)t * 64, vb[i - 4 * I], s + C_::B + (i - 4 * I) * 1024);
+    else if constexpr (i == 4 * I + 4)   // (the scales of TM < 64 rows with repetitions)
+      copy4(g.a_sc + ((int64_t)t * g.M + m0) * 4, vsa, s + C_::S);
+    else
+      copy4(g.b_sc + ((int64_t)t * g.N + n0) * 4, vsb, s + C_::S + 256);
+  };
+  // the two parts of a's fragments: those multiplied now, the next ones
+  i32x8_t p[2][I][2];
+  auto split = [&](auto bb, auto hh, auto rr) {     // register r of fragments h of group b
+    constexpr int b = decltype(bb)::value, h = decltype(hh)::value, r = decltype(rr)::value;
+    int32_t x, y;
+    part((uint32_t)av[b][r / 8][2 * h + r % 8 / 4][r % 4], x, y);
+    p[h][r / 8][0][r % 8] = x;
+    p[h][r / 8][1][r % 8] = y;
   };
   f32x16_t acc[I][2] = {};
+  // The products of half a group, 4 I of them; between them the next half's
+  // parts are formed (two registers after each) and the R reads or C copies of
+  // other() issued.
+  auto half = [&](auto bb, auto hh, auto nb, auto nh, auto reads, auto copies, auto&& other) {
+    constexpr int b = decltype(bb)::value, h = decltype(hh)::value, N_ = 4 * I;
+    constexpr int RN = decltype(reads)::value, CN = decltype(copies)::value, O_ = RN + CN;
+    unroll<N_>([&](auto kk) {
+      constexpr int k = decltype(kk)::value, i = k / 4, q = k / 2 % 2, j = k % 2;
+      constexpr int o0 = k * O_ / N_, o1 = (k + 1) * O_ / N_;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          p[h][i][q], frag(bv[b][j][h]), acc[i][j], kFp8, kFp4, 2 * h,
+          (int)(as[b][i] >> (8 * hi)), 2 * h, (int)(bs[b][j] >> (8 * hi)));
+      split(nb, nh, Int<2 * k>{});
+      split(nb, nh, Int<2 * k + 1>{});
+      unroll<o1 - o0>([&](auto x) { other(Int<o0 + decltype(x)::value>{}); });
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 10, 0);
+      if constexpr (RN > 0) __builtin_amdgcn_sched_group_barrier(0x100, o1 - o0, 0);
+      if constexpr (CN > 0) __builtin_amdgcn_sched_group_barrier(0x010, o1 - o0, 0);
+    });
+    __builtin_amdgcn_sched_barrier(0);
+  };
   // a wave's groups are wave, wave + 4, ..; past the last it copies that
   // again, so that the number of copies in flight is always the same
   const int mine = G > wave ? (G - wave + 3) / 4 : 0;
   const int last = wave + 4 * (mine - 1);
   if (mine > 0) {
+    auto copy = [&](int t, int slot) {
+      unroll<LPS>([&](auto i) { copy_one(t, slot, i); });
+    };
 #pragma unroll
-    for (int p = 0; p < kMidSlots; ++p) copy(min(wave + 4 * p, last), p);
-    int slot = 0;
-    for (int q = 0; q < mine; ++q) {
-      // the oldest slot's copies have landed
-      wait_point<wait_imm((kMidSlots - 1) * LPS, 15)>();
-      const char* s = ring + slot * SLOT;
-      i32x4_t av[I][4], bv[2][2];
-      uint32_t as[I], bs[2];
-#pragma unroll
-      for (int i = 0; i < I; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)      // k = 32 c + 16 hi .. + 15
-          av[i][c] = *(const i32x4_t*)(s + (i * 32 + l31) * 128 +
-                                       (((2 * c + hi) ^ ((l31 >> 1) & 7)) << 4));
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)      // k = 64 h + 32 hi .. + 31
-          bv[j][h] = *(const i32x4_t*)(s + C_::B + (j * 32 + l31) * 64 +
-                                       (((2 * h + hi) ^ ((l31 >> 2) & 3)) << 4));
-      // the block of substep h is 2 h + hi: shifted so that byte 2 h is it
-#pragma unroll
-      for (int i = 0; i < I; ++i)
-        as[i] = *(const uint32_t*)(s + C_::S + (i * 32 + l31) * 4) >> (8 * hi);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        bs[j] = *(const uint32_t*)(s + C_::S + 256 + (j * 32 + l31) * 4) >> (8 * hi);
-      // everything read before the slot is written again
+    for (int s = 0; s < NS; ++s) copy(min(wave + 4 * s, last), s);
+    wait_point<wait_imm((NS - 1) * LPS, 15)>();
+    unroll<R>([&](auto i) { read_one(Int<0>{}, 0, i); });
+    wait_point<wait_imm(63, 0)>();
+    copy(min(wave + 4 * NS, last), 0);
+    unroll<8 * I>([&](auto r) { split(Int<0>{}, Int<0>{}, r); });
+    order_point();
+    int slot = 1;      // of the next group
+    // (past the last group it is read once more, and not multiplied)
+    auto group = [&](auto bb, int q) {
+      constexpr int b = decltype(bb)::value;
+      wait_point<wait_imm((NS - 1) * LPS, 15)>();
+      half(bb, Int<0>{}, bb, Int<1>{}, Int<R>{}, Int<0>{},
+           [&](auto i) { read_one(Int<1 - b>{}, slot, i); });
+      // the next group is in registers: its slot is written again
       wait_point<wait_imm(63, 0)>();
-      copy(min(wave + 4 * (q + kMidSlots), last), slot);
-      unroll<2>([&](auto hh) {
-        constexpr int h = decltype(hh)::value;
-#pragma unroll
-        for (int i = 0; i < I; ++i) {
-          i32x8_t p[2];
-          parts(av[i][2 * h], av[i][2 * h + 1], p[0], p[1]);
-#pragma unroll
-          for (int q2 = 0; q2 < 2; ++q2)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                  p[q2], frag(bv[j][h]), acc[i][j], kFp8, kFp4, 2 * h, (int)as[i], 2 * h,
-                  (int)bs[j]);
-        }
-      });
-      slot = slot + 1 == kMidSlots ? 0 : slot + 1;
+      const int t = min(wave + 4 * (q + 1 + NS), last);
+      half(bb, Int<1>{}, Int<1 - b>{}, Int<0>{}, Int<0>{}, Int<LPS>{},
+           [&](auto i) { copy_one(t, slot, i); });
+      slot = slot + 1 == NS ? 0 : slot + 1;
+    };
+    int q = 0;
+    for (; q + 1 < mine; q += 2) {
+      group(Int<0>{}, q);
+      group(Int<1>{}, q + 1);
     }
+    if (q < mine) group(Int<0>{}, q);
   }
   // the rings give way to the waves' sums once every copy has landed
   wait_point<wait_imm(0, 0)>();
@@ -177,8 +312,8 @@ __global__ __launch_bounds__(256) void mx8_mid_kernel(MxGemmArgs g) {
 
 // ---------------------------------------------------------------- large tiles
 
-// A (64 MI) x 256 tile a workgroup of 4 waves (2 x 2), a wave (32 MI) x 128
-// of it: MI x 4 blocks of the 32 x 32 x 64 instruction, two of them for the two
+// A (64 MI) x (64 NJ) tile a workgroup of 4 waves (2 x 2), a wave a quarter of
+// it: MI x NJ blocks of the 32 x 32 x 64 instruction, two of them for the two
 // parts of a. Both operands stream through a ring of NS LDS slots filled by
 // direct copies, 128 k (128 bytes of a row of a, 64 of b, and their four scale
 // bytes) a slot. The ring runs on across the tiles of a workgroup. A slot
@@ -192,18 +327,19 @@ __global__ __launch_bounds__(256) void mx8_mid_kernel(MxGemmArgs g) {
 // frees the slot, whose last fragments are in registers), and substep 1
 // multiplies while the next stage's first fragments are read. Every
 // substep starts some of the copies, NS stages ahead.
-template <int MI, int NS>
+template <int MI, int NJ, int NS>
 struct Big {
-  static constexpr int BM = 64 * MI, BN = 256, WM = 32 * MI;
+  static constexpr int BM = 64 * MI, BN = 64 * NJ, WM = 32 * MI, WN = 32 * NJ;
   static constexpr int B = BM * 128, S = B + BN * 64;   // b's rows, the scales
   static constexpr int SLOT = S + (BM + BN) * 4;
-  static constexpr int CA = 2 * MI + 1, CB = 5;   // copies a wave and stage
+  static constexpr int CA = 2 * MI + 1, CB = NJ + 1;   // copies a wave and stage
   static constexpr int LDS = NS * SLOT;
+  static constexpr int WGS = LDS > 80 * 1024 ? 1 : 2;   // workgroups a CU
 };
 
-template <int MI, int NS, typename O>
-__global__ __launch_bounds__(256, 1) void mx8_big_kernel(MxGemmArgs g) {
-  typedef Big<MI, NS> C_;
+template <int MI, int NJ, int NS, typename O>
+__global__ __launch_bounds__(256, (Big<MI, NJ, NS>::WGS)) void mx8_big_kernel(MxGemmArgs g) {
+  typedef Big<MI, NJ, NS> C_;
   constexpr int BM = C_::BM, BN = C_::BN, SLOT = C_::SLOT, CA = C_::CA, CB = C_::CB;
   constexpr int LPS = CA + CB;
   extern __shared__ __align__(16) char smem[];
@@ -236,12 +372,12 @@ __global__ __launch_bounds__(256, 1) void mx8_big_kernel(MxGemmArgs g) {
 
   // copy state: the tile and stage whose copies go out next. A wave copies
   // rows 16 MI wave .. of a, 8 a copy (lane l row l / 8, piece l % 8 of the
-  // slot), 64 wave .. of b, 16 a copy (row l / 4, piece l % 4), and 64 rows'
-  // scales of each (of a, with MI = 2, two waves the same ones). Rows past the
-  // end repeat the last one.
+  // slot), 16 NJ wave .. of b, 16 a copy (row l / 4, piece l % 4), and 64 rows'
+  // scales of each (of 128 rows two waves the same ones). Rows past the end
+  // repeat the last one.
   const int ar = lane >> 3, br = lane >> 2;
-  const int asw = MI == 4 ? wave : (wave & 1);
-  uint32_t va[2 * MI], vb[4], vsa, vsb;
+  const int asw = MI == 4 ? wave : (wave & 1), bsw = NJ == 4 ? wave : (wave & 1);
+  uint32_t va[2 * MI], vb[NJ], vsa, vsb;
   const uint8_t *pa, *pb;
   int cm0, cn0, ct = L, ck = 0;
   auto set_tile = [&]() {
@@ -254,12 +390,12 @@ __global__ __launch_bounds__(256, 1) void mx8_big_kernel(MxGemmArgs g) {
       va[i] = (uint32_t)min(wave * (16 * MI) + i * 8 + ar, ma) * (uint32_t)Kp +
               (((lane & 7) ^ ((4 * i + (ar >> 1)) & 7)) << 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      vb[i] = (uint32_t)min(wave * 64 + i * 16 + br, nb) * (uint32_t)(Kp / 2) +
+    for (int i = 0; i < NJ; ++i)
+      vb[i] = (uint32_t)min(wave * (16 * NJ) + i * 16 + br, nb) * (uint32_t)(Kp / 2) +
               (((lane & 3) ^ ((br >> 2) & 3)) << 4);
-    const int qa = asw * 64 + lane, qb = wave * 64 + lane;
+    const int qa = asw * 64 + lane, qb = bsw * 64 + lane;
     vsa = (uint32_t)min(qa / (32 * MI) * C_::WM + qa % MI * 32 + qa / MI % 32, ma) * 4;
-    vsb = (uint32_t)min(qb / 128 * 128 + qb % 4 * 32 + qb / 4 % 32, nb) * 4;
+    vsb = (uint32_t)min(qb / (32 * NJ) * C_::WN + qb % NJ * 32 + qb / NJ % 32, nb) * 4;
   };
   // copy i of the copy state's stage into a slot: CA of a, CB of b, the scales
   // last
@@ -272,10 +408,10 @@ __global__ __launch_bounds__(256, 1) void mx8_big_kernel(MxGemmArgs g) {
   };
   auto copy_b = [&](int slot, int i) {
     char* s = smem + slot * SLOT;
-    if (i < 4)
-      copy16(pb + (int64_t)ck * 64, vb[i], s + C_::B + (wave * 64 + i * 16) * 64);
+    if (i < NJ)
+      copy16(pb + (int64_t)ck * 64, vb[i], s + C_::B + (wave * (16 * NJ) + i * 16) * 64);
     else
-      copy4(g.b_sc + ((int64_t)ck * N + cn0) * 4, vsb, s + C_::S + BM * 4 + wave * 256);
+      copy4(g.b_sc + ((int64_t)ck * N + cn0) * 4, vsb, s + C_::S + BM * 4 + bsw * 256);
   };
   auto advance = [&]() {
     if (++ck == G) {
@@ -289,25 +425,26 @@ __global__ __launch_bounds__(256, 1) void mx8_big_kernel(MxGemmArgs g) {
     }
   };
 
-  i32x4_t af[2][MI][2], bf[2][4];
-  uint32_t as[MI], bs[4];
+  i32x4_t af[2][MI][2], bf[2][NJ];
+  uint32_t as[MI], bs[NJ];
   typedef uint32_t asv_t __attribute__((ext_vector_type(MI)));
+  typedef uint32_t bsv_t __attribute__((ext_vector_type(NJ)));
   asv_t asn;
-  u32x4_t bsn;
-  // read i of a substep: 2 MI half fragments of a, 4 fragments of b, then the
+  bsv_t bsn;
+  // read i of a substep: 2 MI half fragments of a, NJ fragments of b, then the
   // stage's scales
   auto read_one = [&](int slot, int s, int buf, int i) {
     const char* p = smem + slot * SLOT;
     if (i < 2 * MI) {
       const int c = ((4 * s + 2 * (i & 1) + hi) ^ ((l31 >> 1) & 7)) << 4;
       af[buf][i / 2][i & 1] = *(const i32x4_t*)(p + (wr * C_::WM + i / 2 * 32 + l31) * 128 + c);
-    } else if (i < 2 * MI + 4) {
+    } else if (i < 2 * MI + NJ) {
       const int c = ((2 * s + hi) ^ ((l31 >> 2) & 3)) << 4, j = i - 2 * MI;
-      bf[buf][j] = *(const i32x4_t*)(p + C_::B + (wc * 128 + j * 32 + l31) * 64 + c);
-    } else if (i == 2 * MI + 4) {
+      bf[buf][j] = *(const i32x4_t*)(p + C_::B + (wc * C_::WN + j * 32 + l31) * 64 + c);
+    } else if (i == 2 * MI + NJ) {
       asn = *(const asv_t*)(p + C_::S + (wr * 32 + l31) * (4 * MI));
     } else {
-      bsn = *(const u32x4_t*)(p + C_::S + BM * 4 + (wc * 32 + l31) * 16);
+      bsn = *(const bsv_t*)(p + C_::S + BM * 4 + (wc * 32 + l31) * (4 * NJ));
     }
   };
   // the block of substep s is 2 s + hi: shifted so that byte 2 s is it
@@ -315,30 +452,46 @@ __global__ __launch_bounds__(256, 1) void mx8_big_kernel(MxGemmArgs g) {
 #pragma unroll
     for (int i = 0; i < MI; ++i) as[i] = asn[i] >> (8 * hi);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) bs[j] = bsn[j] >> (8 * hi);
+    for (int j = 0; j < NJ; ++j) bs[j] = bsn[j] >> (8 * hi);
   };
-  f32x16_t acc[MI][4];
+  f32x16_t acc[MI][NJ];
 
-  // A substep's 8 MI MFMAs (of each block of rows the first part with the four
-  // blocks of columns, then the second) with its R reads and C copies spread
-  // over them, the reads over the first half, the copies evenly.
+  // the two parts of the fragment that is multiplied, and of the next one
+  i32x8_t p[2][2];
+  auto split = [&](int buf, int i, int to, int r) {
+    int32_t x, y;
+    part((uint32_t)af[buf][i][r / 4][r % 4], x, y);
+    p[to][0][r] = x;
+    p[to][1][r] = y;
+  };
+  // A substep's 2 MI NJ MFMAs (of each block of rows the first part with the NJ
+  // blocks of columns, then the second) with the next fragment's parts, its R
+  // reads and C copies spread over them, the reads over the first half (the
+  // last block forms the parts of the next substep's first fragment), the
+  // copies evenly: in a run they would hold the wave's issue slot while the
+  // matrix core idles.
   auto substep = [&](auto sub, auto reads, auto copies, auto&& read, auto&& copy) {
     constexpr int S = decltype(sub)::value, R = decltype(reads)::value,
-                  C = decltype(copies)::value, N_ = 8 * MI;
-    i32x8_t p[2];
+                  C = decltype(copies)::value, N_ = 2 * MI * NJ, SP = 4 / NJ;
     unroll<N_>([&](auto kk) {
-      constexpr int k = decltype(kk)::value, i = k / 8, q = k / 4 % 2, j = k % 4;
+      constexpr int k = decltype(kk)::value, i = k / (2 * NJ), q = k / NJ % 2, j = k % NJ;
       constexpr int r0 = k < N_ / 2 ? k * R / (N_ / 2) : R;
       constexpr int r1 = k + 1 <= N_ / 2 ? (k + 1) * R / (N_ / 2) : R;
-      constexpr int c0 = k * C / N_, c1 = (k + 1) * C / N_;
-      if constexpr (k % 8 == 0) parts(af[S][i][0], af[S][i][1], p[0], p[1]);
+      constexpr int CN = NS == 2 && S == 0 ? N_ / 4 : N_;
+      constexpr int c0 = k < CN ? k * C / CN : C, c1 = k + 1 <= CN ? (k + 1) * C / CN : C;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          p[i & 1][q], frag(bf[S][j]), acc[i][j], kFp8, kFp4, 2 * S, (int)as[i], 2 * S,
+          (int)bs[j]);
+      unroll<SP>([&](auto x) {
+        split(i + 1 < MI ? S : 1 - S, i + 1 < MI ? i + 1 : 0, (i + 1) & 1,
+              k % (2 * NJ) * SP + decltype(x)::value);
+      });
       unroll<r1 - r0>([&](auto x) { read(r0 + decltype(x)::value); });
       unroll<c1 - c0>([&](auto x) { copy(c0 + decltype(x)::value); });
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-          p[q], frag(bf[S][j]), acc[i][j], kFp8, kFp4, 2 * S, (int)as[i], 2 * S, (int)bs[j]);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 5 * SP, 0);
       if constexpr (r1 > r0) __builtin_amdgcn_sched_group_barrier(0x100, r1 - r0, 0);
       if constexpr (c1 > c0) __builtin_amdgcn_sched_group_barrier(0x010, c1 - c0, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     });
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -359,35 +512,41 @@ __global__ __launch_bounds__(256, 1) void mx8_big_kernel(MxGemmArgs g) {
   asm volatile("s_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int i = 0; i < 2 * MI + 6; ++i) read_one(0, 0, 0, i);
+  for (int i = 0; i < 2 * MI + NJ + 2; ++i) read_one(0, 0, 0, i);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) split(0, 0, 0, r);
 
   for (;;) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     for (int k = 0; k < G; ++k) {
       const int next = slot + 1 == NS ? 0 : slot + 1;
       wait_point<wait_imm(63, 0)>();   // fragments of substep 0, scales
       take_scales();
-      substep(Int<0>{}, Int<2 * MI + 4>{}, Int<CB>{}, [&](int i) { read_one(slot, 1, 1, i); },
+      substep(Int<0>{}, Int<2 * MI + NJ>{}, Int<CB>{}, [&](int i) { read_one(slot, 1, 1, i); },
               [&](int i) { copy_b(pslot, i); });
       advance();
       wait_point<wait_imm((NS - 2) * LPS, 0)>();
       asm volatile("s_barrier" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      substep(Int<1>{}, Int<2 * MI + 6>{}, Int<CA>{}, [&](int i) { read_one(next, 0, 0, i); },
+      substep(Int<1>{}, Int<2 * MI + NJ + 2>{}, Int<CA>{}, [&](int i) { read_one(next, 0, 0, i); },
               [&](int i) { copy_a(slot, i); });
       pslot = slot;
       slot = next;
     }
-    settle_sums<MI>();
+    settle_sums<MI * NJ / 4>();
     int m0, n0;
     coords(L, m0, n0);
-    O* out = (O*)g.out + (int64_t)(m0 + wr * C_::WM + 4 * hi) * g.ldo + n0 + wc * 128 + l31;
-    const int mleft = M - (m0 + wr * C_::WM + 4 * hi), nleft = N - (n0 + wc * 128 + l31);
+    // (the lane again, by its own instructions: kept over the loop it would be
+    // spilled, with 128 x 256 tiles)
+    const int el = lane_id(), mo = m0 + wr * C_::WM + 4 * (el >> 5);
+    const int no = n0 + wc * C_::WN + (el & 31);
+    O* out = (O*)g.out + (int64_t)mo * g.ldo + no;
+    const int mleft = M - mo, nleft = N - no;
     if (m0 + BM <= M && n0 + BN <= N) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
@@ -395,7 +554,7 @@ __global__ __launch_bounds__(256, 1) void mx8_big_kernel(MxGemmArgs g) {
         for (int e = 0; e < 16; ++e) {
           O* o = out + (int64_t)(i * 32 + 8 * (e / 4) + e % 4) * g.ldo;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) put(o + j * 32, sum_of<MI>(acc[i][j][e]));
+          for (int j = 0; j < NJ; ++j) put(o + j * 32, sum_of<MI * NJ / 4>(acc[i][j][e]));
           __builtin_amdgcn_sched_barrier(0);   // not all accumulators into registers first
         }
     } else {
@@ -407,8 +566,8 @@ __global__ __launch_bounds__(256, 1) void mx8_big_kernel(MxGemmArgs g) {
           O* o = out + (int64_t)r * g.ldo;
           if (r < mleft) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (j * 32 < nleft) put(o + j * 32, sum_of<MI>(acc[i][j][e]));
+            for (int j = 0; j < NJ; ++j)
+              if (j * 32 < nleft) put(o + j * 32, sum_of<MI * NJ / 4>(acc[i][j][e]));
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -420,21 +579,60 @@ __global__ __launch_bounds__(256, 1) void mx8_big_kernel(MxGemmArgs g) {
   wait_point<wait_imm(0, 0)>();
 }
 
+// The kernel by the number of tiles, measured with float32 results (from graphs,
+// on matrices b that the caches do not hold; us, M x N x K; the sides of each
+// border):
+//   few rows:    up to 16: 1 x 5632 x 2048 4.4, 32 x 64 tiles 5.8; 16 x 8192 x
+//                2048 4.65, 5.9. Eight waves for long K and few workgroups (1 x
+//                1024 x 16384 8.7, four 11.2; 16 x 2048 x 4096 4.45, 4.8; 8 x
+//                16384 x 4096 12.8, 11.6)
+//   32 x 64:     for 8 to 16 rows and K from 4096 on where the tiles fill their
+//                rounds of the CUs to 7/8, since their copies of a serve 64 rows
+//                of b, the few rows' 16: 8 x 16384 x 4096 10.4, few rows 11.6; 16
+//                x 16384 x 4096 11.1, 13.0 (16 x 16384 x 2048 7.9, 8.1; 8 x 14336
+//                x 2048 7.3, 7.0). And up to one a CU: 256 x 2048 x 2048 6.4, 64 x
+//                64 8.5; 128 x 2048 x 8192 11.1, 15.5
+//   64 x 64:     up to two a CU: 300 x 3000 x 2048 9.7, 32 x 64 10.9; 512 x 2048 x
+//                5632 15.0, 16.1; 512 x 4096 x 8192 37.7, 128 x 128 50.0; 1024 x
+//                2048 x 2048 16.7, 16.9
+//   128 x 128:   up to 256: 640 x 4096 x 2048 16.6, 64 x 64 22.2; 1024 x 4096 x
+//                2048 19.1, 128 x 256 24.4
+//   128 x 256:   two workgroups a CU, one stores while the other multiplies: 2048
+//                x 4096 x 2048 28.9, 128 x 128 31.4 (2560 x 4096 x 2048 41.3,
+//                38.9); 4096 x 5632 x 2048 69.6, 256 x 256 85.6
+//   256 x 256:   where its tiles fill their rounds of the CUs to 3/4, and K is
+//                longer than 1024 (4096 x 4096 x 1024 32.6, 128 x 256 31.2): 8192
+//                x 5632 x 2048 136, 138; 8192 x 8192 x 8192 643 (1.71 PFLOP/s, two
+//                instructions for every product), 670. Matrix instructions alone,
+//                on random operands, run at 3.4 to 3.7 PFLOP/s here (power).
 template <typename O>
 hipError_t launch(const MxGemmArgs& g, hipStream_t s) {
-  const int force = getenv("MX8K") ? atoi(getenv("MX8K")) : 0;
-  const unsigned n64 = (unsigned)((g.N + 63) / 64);
-  int k = force;
-  if (!k) k = ((g.M + 255) / 256) * ((g.N + 255) / 256) >= 128 ? 4 : 1;
-  if (g.K == 0 && k > 2) k = 1;
-  if (k == 1)
-    mx8_mid_kernel<1, O><<<dim3(n64, (unsigned)((g.M + 31) / 32)), 256, Mid<1>::LDS, s>>>(g);
-  else if (k == 2)
-    mx8_mid_kernel<2, O><<<dim3(n64, (unsigned)((g.M + 63) / 64)), 256, Mid<2>::LDS, s>>>(g);
-  else if (k == 3)
-    mx8_big_kernel<2, 3, O><<<kCus, 256, Big<2, 3>::LDS, s>>>(g);
-  else
-    mx8_big_kernel<4, 3, O><<<kCus, 256, Big<4, 3>::LDS, s>>>(g);
+  const auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+  const auto fill = [](int64_t tiles) {      // of their rounds of the CUs
+    return (double)tiles / (double)((tiles + kCus - 1) / kCus * kCus);
+  };
+  const int64_t n64 = up(g.N, 64), t32 = up(g.M, 32) * n64, t64 = up(g.M, 64) * n64;
+  const int64_t t128 = up(g.M, 128) * up(g.N, 128), t256 = up(g.M, 256) * up(g.N, 256);
+  const bool wide = g.M >= 8 && g.M <= 16 && g.K >= 4096 && fill(n64) >= 0.875;
+  if (g.M <= 16 && !wide) {
+    const unsigned grid = (unsigned)up(g.N, 16);
+    if (g.K >= 4096 && grid <= 2 * kCus)
+      mx8_few_kernel<8, O><<<grid, 512, 8 * kFewRing, s>>>(g);
+    else
+      mx8_few_kernel<4, O><<<grid, 256, 4 * kFewRing, s>>>(g);
+  } else if (wide || t32 <= kCus) {
+    mx8_mid_kernel<1, 2, O><<<dim3((unsigned)n64, (unsigned)up(g.M, 32)), 256, Mid<1, 2>::LDS,
+                              s>>>(g);
+  } else if (t64 <= 2 * kCus || g.K == 0) {   // (no tile of the others is ever empty)
+    mx8_mid_kernel<2, 2, O><<<dim3((unsigned)n64, (unsigned)up(g.M, 64)), 256, Mid<2, 2>::LDS,
+                              s>>>(g);
+  } else if (t128 <= kCus) {
+    mx8_big_kernel<2, 2, 3, O><<<2 * kCus, 256, Big<2, 2, 3>::LDS, s>>>(g);
+  } else if (g.K <= 1024 || fill(t256) < 0.75) {
+    mx8_big_kernel<2, 4, 2, O><<<2 * kCus, 256, Big<2, 4, 2>::LDS, s>>>(g);
+  } else {
+    mx8_big_kernel<4, 4, 3, O><<<kCus, 256, Big<4, 4, 3>::LDS, s>>>(g);
+  }
   return hipGetLastError();
 }
 

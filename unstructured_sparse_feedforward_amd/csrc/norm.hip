@@ -19,27 +19,17 @@ namespace {
 
 // A row is L lanes' (a wave's 64, or a workgroup's), who hold V pieces of CH
 // consecutive elements each: piece v of lane l is at column (v L + l) CH.
+constexpr int CH = 8;
 template <int L>
 struct Row {
-  static constexpr int NT = L < 256 ? 256 : L;     // threads a workgroup
+  static constexpr int NT = L == 64 ? 256 : L;     // threads a workgroup
   static constexpr int ROWS = NT / L;              // rows a workgroup
 };
 
-template <int CH, typename E>
-__device__ __forceinline__ void load_piece(const E* p, int left, float* v) {
-  if (left >= CH) {
-    if constexpr (CH == 8) load8(p, v);
-    else load4(p, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < CH; ++j) v[j] = j < left ? ld(p + j) : 0.0f;
-  }
-}
-template <int CH, typename E>
+template <typename E>
 __device__ __forceinline__ void store_piece(E* p, int left, const float* v) {
   if (left >= CH) {
-    if constexpr (CH == 8) store8(p, v);
-    else store4(p, v);
+    store8(p, v);
   } else {
 #pragma unroll
     for (int j = 0; j < CH; ++j)
@@ -47,47 +37,81 @@ __device__ __forceinline__ void store_piece(E* p, int left, const float* v) {
   }
 }
 
-// the lane's pieces of a row of a matrix of either type
-template <int L, int V, int CH>
+// The lane's pieces of a row of a matrix of either type, as they are in
+// memory (a: float32 0 .. 3 or all of bf16, b: float32 4 .. 7), and their
+// values: apart, so that a load is waited for only where its values are used.
+struct Piece {
+  u32x4_t a, b;
+};
+template <int L, int V>
 __device__ __forceinline__ void load_row(const void* p, int64_t at, int bf, int cols, int l,
-                                         float (&v)[V][CH]) {
-  if (bf) {
+                                         Piece (&v)[V]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (i * L + l) * CH;
-      load_piece<CH>((const uint16_t*)p + at + c, cols - c, v[i]);
-    }
-  } else {
+  for (int i = 0; i < V; ++i) {
+    const int c = (i * L + l) * CH, left = cols - c;
+    if (bf) {
+      const uint16_t* q = (const uint16_t*)p + at + c;
+      if (left >= CH) {
+        v[i].a = *(const u32x4u_t*)q;
+      } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (i * L + l) * CH;
-      load_piece<CH>((const float*)p + at + c, cols - c, v[i]);
+        for (int j = 0; j < 4; ++j)
+          v[i].a[j] = (2 * j < left ? (uint32_t)q[2 * j] : 0u) |
+                      (2 * j + 1 < left ? (uint32_t)q[2 * j + 1] << 16 : 0u);
+      }
+    } else {
+      const uint32_t* q = (const uint32_t*)p + at + c;
+      if (left >= CH) {
+        v[i].a = *(const u32x4w_t*)q;
+        v[i].b = *(const u32x4w_t*)(q + 4);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[i].a[j] = j < left ? q[j] : 0u;
+          v[i].b[j] = 4 + j < left ? q[4 + j] : 0u;
+        }
+      }
     }
   }
 }
-template <int L, int V, int CH>
+template <int V>
+__device__ __forceinline__ void values(const Piece (&v)[V], int bf, float (&o)[V][CH]) {
+  if (bf) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) Vec<uint16_t, 8>::cvt(v[i].a, o[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        o[i][j] = __uint_as_float(v[i].a[j]);
+        o[i][4 + j] = __uint_as_float(v[i].b[j]);
+      }
+  }
+}
+template <int L, int V>
 __device__ __forceinline__ void store_row(void* p, int64_t at, int bf, int cols, int l,
                                           const float (&v)[V][CH]) {
   if (bf) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (i * L + l) * CH;
-      store_piece<CH>((uint16_t*)p + at + c, cols - c, v[i]);
+      store_piece((uint16_t*)p + at + c, cols - c, v[i]);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (i * L + l) * CH;
-      store_piece<CH>((float*)p + at + c, cols - c, v[i]);
+      store_piece((float*)p + at + c, cols - c, v[i]);
     }
   }
 }
 
 // The sum of v over the row's lanes, in all of them, in an order that depends
-// on L alone. share: a float a wave (unused for L = 64). Of a workgroup's
+// on L alone. share: a value a wave (unused for L = 64). Of a workgroup's
 // calls, two in turn need two shares or a barrier between them.
-template <int L>
-__device__ __forceinline__ float row_sum(float v, float* share) {
+template <int L, typename T>
+__device__ __forceinline__ T row_sum(T v, T* share) {
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
   if constexpr (L > 64) {
@@ -102,7 +126,7 @@ __device__ __forceinline__ float row_sum(float v, float* share) {
 
 // The lane's pieces of a row as MXFP8. 32 / CH lanes have a block, 128 / CH
 // the four whose scales are a dword.
-template <int L, int V, int CH>
+template <int L, int V>
 __device__ __forceinline__ void store_mx8(const NormArgs& a, int64_t row, int l,
                                           const float (&v)[V][CH]) {
   const int Kp = (int)mx_padded(a.cols);
@@ -116,10 +140,7 @@ __device__ __forceinline__ void store_mx8(const NormArgs& a, int64_t row, int l,
 #pragma unroll
     for (int o = 1; o < 32 / CH; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
     const uint32_t sb = scale_byte<Fp8>(m);
-    if (c < Kp) {
-      if constexpr (CH == 8) *(u32x2_t*)(codes + c) = Fp8::pack8(v[i], sb);
-      else *(uint32_t*)(codes + c) = Fp8::pack4(v[i], sb);
-    }
+    if (c < Kp) *(u32x2_t*)(codes + c) = Fp8::pack8(v[i], sb);
     uint32_t d = sb << (8 * (l / (32 / CH) % 4));
     d |= (uint32_t)__shfl_xor((int)d, 32 / CH);
     d |= (uint32_t)__shfl_xor((int)d, 64 / CH);
@@ -128,16 +149,26 @@ __device__ __forceinline__ void store_mx8(const NormArgs& a, int64_t row, int l,
   }
 }
 
-template <int L, int V, int CH>
+// WIDE (results in float32 and MXFP8): the sum and the products in 64 bits, y
+// rounded once, so that a result in 8 bits is that of the formula but where y
+// lies within half a step of float32 of a border, and not four of them (8192 x
+// 2048 from bf16, where it costs most, 30.5 us; in 32 bits 29). A bf16 result's
+// own rounding is 2^15 times what that would gain.
+template <int L, int V, bool WIDE>
 __global__ __launch_bounds__(Row<L>::NT) void norm_kernel(NormArgs a) {
-  __shared__ float share[16];
+  typedef std::conditional_t<WIDE, double, float> T;
+  __shared__ T share[16];
   const int l = threadIdx.x % L;
   const int64_t row = (int64_t)blockIdx.x * Row<L>::ROWS + threadIdx.x / L;
   if (row >= a.rows || (a.n_dev && row >= *a.n_dev)) return;   // (all lanes of a row)
+  Piece ps[V], pr[V], pw[V];
   float s[V][CH], t[V][CH];
-  load_row<L, V, CH>(a.x, row * a.ldx, a.x_bf, a.cols, l, s);
+  load_row<L, V>(a.x, row * a.ldx, a.x_bf, a.cols, l, ps);
+  if (a.res) load_row<L, V>(a.res, row * a.ldr, a.r_bf, a.cols, l, pr);
+  if (a.weight) load_row<L, V>(a.weight, 0, a.w_bf, a.cols, l, pw);
+  values(ps, a.x_bf, s);
   if (a.res) {
-    load_row<L, V, CH>(a.res, row * a.ldr, a.r_bf, a.cols, l, t);
+    values(pr, a.r_bf, t);
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -145,76 +176,104 @@ __global__ __launch_bounds__(Row<L>::NT) void norm_kernel(NormArgs a) {
         s[i][j] += t[i][j];
         if (a.r_bf) s[i][j] = bf16lo(bf16_bits(s[i][j]));
       }
-    store_row<L, V, CH>(a.res_out, row * a.ldro, a.r_bf, a.cols, l, s);
+    store_row<L, V>(a.res_out, row * a.ldro, a.r_bf, a.cols, l, s);
   }
-  if (a.weight) load_row<L, V, CH>(a.weight, 0, a.w_bf, a.cols, l, t);
-  float q = 0.0f;
+  T q = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int j = 0; j < CH; ++j) q = fmaf(s[i][j], s[i][j], q);
-  const float r = 1.0f / sqrtf(row_sum<L>(q, share) / (float)a.cols + a.eps);
-  if (a.rstd && l == 0) a.rstd[row] = r;
+    for (int j = 0; j < CH; ++j) q = fma((T)s[i][j], (T)s[i][j], q);
+  const T r = (T)1 / sqrt(row_sum<L>(q, share) / (T)a.cols + (T)a.eps);
+  if (a.rstd && l == 0) a.rstd[row] = (float)r;
+  if (a.weight) values(pw, a.w_bf, t);
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      s[i][j] *= r;
+      s[i][j] = (float)(a.weight ? (T)s[i][j] * r * (T)t[i][j] : (T)s[i][j] * r);
       // (columns past the last are 0 there: s is 0, and r may be infinite)
-      if (a.weight) s[i][j] *= t[i][j];
       if ((i * L + l) * CH + j >= a.cols) s[i][j] = 0.0f;
     }
-  if (a.out_kind == kMx8) store_mx8<L, V, CH>(a, row, l, s);
-  else store_row<L, V, CH>(a.out, row * a.ldo, a.out_kind == kBF16, a.cols, l, s);
+  if (WIDE && a.out_kind == kMx8) store_mx8<L, V>(a, row, l, s);
+  else store_row<L, V>(a.out, row * a.ldo, !WIDE, a.cols, l, s);
 }
 
 // A workgroup's rows are blockIdx.x ROWS + .., and every gridDim.x ROWS from
 // there on: it sums its rows' dy xh in registers, its waves' sums through LDS,
 // and writes one row of the workspace.
-template <int L, int V, int CH>
+template <int L, int V>
 __global__ __launch_bounds__(Row<L>::NT) void norm_grad_kernel(NormGradArgs a) {
   constexpr int ROWS = Row<L>::ROWS;
   __shared__ float share[2][16];
   __shared__ float red[ROWS > 1 ? (ROWS - 1) * L * V * CH : 1];
   const int l = threadIdx.x % L, mine = threadIdx.x / L;
+  // The next row's loads are issued before this row's sum is waited for, and
+  // the weights are kept (of rows over 8192 both would take more registers than
+  // 16 waves have).
+  constexpr bool AHEAD = L * V <= 1024;
   float w[V][CH], dw[V][CH] = {};
-  if (a.weight) {
-    load_row<L, V, CH>(a.weight, 0, a.w_bf, a.cols, l, w);
-  } else {
+  auto load_weight = [&] {
+    if (a.weight) {
+      Piece p[V];
+      load_row<L, V>(a.weight, 0, a.w_bf, a.cols, l, p);
+      values(p, a.w_bf, w);
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+      for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < CH; ++j) w[i][j] = 1.0f;
-  }
+        for (int j = 0; j < CH; ++j) w[i][j] = 1.0f;
+    }
+  };
+  if (AHEAD) load_weight();
+  Piece ps[V], pg[V], pd[V];
+  float r = 0.0f;
+  auto load = [&](int64_t row) {
+    load_row<L, V>(a.s, row * a.lds, a.s_bf, a.cols, l, ps);
+    load_row<L, V>(a.dy, row * a.lddy, a.dy_bf, a.cols, l, pg);
+    if (a.ds_in) load_row<L, V>(a.ds_in, row * a.lddi, a.di_bf, a.cols, l, pd);
+    r = a.rstd[row];
+  };
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t row = (int64_t)blockIdx.x * ROWS + mine;    // (with L > 64 a workgroup has one row)
   int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.rows; r0 += (int64_t)gridDim.x * ROWS) {
-    const int64_t row = r0 + mine;
-    if (L == 64 && row >= a.rows) break;      // (with L > 64 a workgroup has one row)
-    float s[V][CH], g[V][CH], t[V][CH];
-    load_row<L, V, CH>(a.s, row * a.lds, a.s_bf, a.cols, l, s);
-    load_row<L, V, CH>(a.dy, row * a.lddy, a.dy_bf, a.cols, l, g);
-    if (a.ds_in) load_row<L, V, CH>(a.ds_in, row * a.lddi, a.di_bf, a.cols, l, t);
-    const float r = a.rstd[row];
-    float q = 0.0f;
+  if (AHEAD && row < a.rows) load(row);
+  for (; row < a.rows; row += step) {
+    if (!AHEAD) {
+      load(row);
+      load_weight();
+    }
+    float s[V][CH], g[V][CH], q = 0.0f;
+    values(ps, a.s_bf, s);
+    values(pg, a.dy_bf, g);
+    const float r0 = r;
+    Piece p0[AHEAD ? V : 1];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
+      if (AHEAD) p0[i] = pd[i];
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        s[i][j] *= r;
+        s[i][j] *= r0;
         dw[i][j] = fmaf(g[i][j], s[i][j], dw[i][j]);
         g[i][j] *= w[i][j];
         q = fmaf(g[i][j], s[i][j], q);
       }
+    }
+    if (AHEAD && row + step < a.rows) load(row + step);
     const float c = row_sum<L>(q, share[turn]) / (float)a.cols;
     turn ^= 1;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < CH; ++j) {
-        s[i][j] = r * (g[i][j] - s[i][j] * c);
-        if (a.ds_in) s[i][j] += t[i][j];
-      }
-    store_row<L, V, CH>(a.ds, row * a.ldds, a.ds_bf, a.cols, l, s);
+      for (int j = 0; j < CH; ++j) s[i][j] = r0 * (g[i][j] - s[i][j] * c);
+    if (a.ds_in) {
+      if constexpr (AHEAD) values(p0, a.di_bf, g);
+      else values(pd, a.di_bf, g);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < CH; ++j) s[i][j] += g[i][j];
+    }
+    store_row<L, V>(a.ds, row * a.ldds, a.ds_bf, a.cols, l, s);
   }
   if (!a.dw) return;
   if constexpr (ROWS > 1) {
@@ -233,7 +292,7 @@ __global__ __launch_bounds__(Row<L>::NT) void norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
         for (int m = 0; m < ROWS - 1; ++m) dw[i][j] += red[(m * V * CH + i * CH + j) * L + l];
   }
-  store_row<L, V, CH>(a.part, (int64_t)blockIdx.x * a.cols, 0, a.cols, l, dw);
+  store_row<L, V>(a.part, (int64_t)blockIdx.x * a.cols, 0, a.cols, l, dw);
 }
 
 // dw from the workgroups' sums: 64 columns a workgroup, its 16 waves share out
@@ -257,43 +316,55 @@ __global__ __launch_bounds__(kDwWaves * 64) void norm_dw_kernel(NormGradArgs a) 
   }
 }
 
-template <int L, int V, int CH>
+template <int L, int V>
 hipError_t norm(const NormArgs& a, hipStream_t s) {
   const unsigned grid = (unsigned)((a.rows + Row<L>::ROWS - 1) / Row<L>::ROWS);
-  norm_kernel<L, V, CH><<<grid, Row<L>::NT, 0, s>>>(a);
+  if (a.out_kind != kBF16) norm_kernel<L, V, true><<<grid, Row<L>::NT, 0, s>>>(a);
+  else norm_kernel<L, V, false><<<grid, Row<L>::NT, 0, s>>>(a);
   return hipGetLastError();
 }
-template <int L, int V, int CH>
+template <int L, int V>
 hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
-  norm_grad_kernel<L, V, CH><<<a.parts, Row<L>::NT, 0, s>>>(a);
+  norm_grad_kernel<L, V><<<a.parts, Row<L>::NT, 0, s>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
+// Threads for a row by its columns, 8 a thread up to a workgroup's most: the
+// fewer a thread, the more rows a CU has in flight (us, from graphs, out of the
+// caches: 8192 x 2048 bf16 in, out and stream 27.4, by 64 threads of 32 columns
+// 30.5, by 512 of 4 34; 4096 x 4096 27.9, 256 of 16 29.7). A wave or more a
+// row: 64 threads of 16 columns for 777 x 1003 6.5, 128 of 8 5.9.
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
-  if (a.cols <= 512) return norm<64, 1, 8>(a, s);
-  if (a.cols <= 1024) return norm<64, 2, 8>(a, s);
-  if (a.cols <= 2048) return norm<64, 4, 8>(a, s);
-  if (a.cols <= 4096) return norm<256, 2, 8>(a, s);
-  if (a.cols <= 8192) return norm<256, 4, 8>(a, s);
-  return norm<512, 4, 8>(a, s);
+  if (a.cols <= 512) return norm<64, 1>(a, s);
+  if (a.cols <= 1024) return norm<128, 1>(a, s);
+  if (a.cols <= 2048) return norm<256, 1>(a, s);
+  if (a.cols <= 4096) return norm<512, 1>(a, s);
+  if (a.cols <= 8192) return norm<1024, 1>(a, s);
+  return norm<1024, 2>(a, s);
 }
 
+// The gradient's workgroups, each of which writes its sums for dw: as many as
+// keep the memory busy (8192 x 2048: float32 53 us, by 256 52, 1024 56; bf16 31,
+// 40, 33; 4096 x 4096 47, by 512 49; 16384 x 64 13.5, by 512 15.4).
 int norm_grad_parts(int64_t rows, int64_t cols) {
-  const int64_t each = cols <= 2048 ? 4 : 1;      // rows a workgroup at a time
-  return (int)min((rows + each - 1) / each, (int64_t)512);
+  const int64_t each = cols <= 1024 ? 4 : 1;      // rows a workgroup at a time
+  const int64_t most = cols <= 512 ? 768 : cols <= 2048 ? 512 : 256;
+  return (int)min((rows + each - 1) / each, most);
 }
 
+// Its threads: up to 1024 columns a wave has a row, and no barrier (8192 x 1000
+// float32 32.6 us, by 128 threads 36.2; 777 x 1003 9.3, 10.4).
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (a.rows == 0) {}      // (dw is then 0)
-  else if (a.cols <= 512) e = norm_grad<64, 1, 8>(a, s);
-  else if (a.cols <= 1024) e = norm_grad<64, 2, 8>(a, s);
-  else if (a.cols <= 2048) e = norm_grad<64, 4, 8>(a, s);
-  else if (a.cols <= 4096) e = norm_grad<256, 2, 8>(a, s);
-  else if (a.cols <= 8192) e = norm_grad<256, 4, 8>(a, s);
-  else e = norm_grad<512, 4, 8>(a, s);
+  else if (a.cols <= 512) e = norm_grad<64, 1>(a, s);
+  else if (a.cols <= 1024) e = norm_grad<64, 2>(a, s);
+  else if (a.cols <= 2048) e = norm_grad<256, 1>(a, s);
+  else if (a.cols <= 4096) e = norm_grad<512, 1>(a, s);
+  else if (a.cols <= 8192) e = norm_grad<512, 2>(a, s);
+  else e = norm_grad<1024, 2>(a, s);
   if (e != hipSuccess || !a.dw) return e;
   norm_dw_kernel<<<(unsigned)((a.cols + 63) / 64), kDwWaves * 64, 0, s>>>(a);
   return hipGetLastError();

@@ -19,6 +19,7 @@ __device__ __forceinline__ void st(uint16_t* p, float v) { *p = (uint16_t)bf16_b
 // (the hardware's unaligned access)
 typedef f32x4_t f32x4u_t __attribute__((aligned(4)));
 typedef u32x4_t u32x4u_t __attribute__((aligned(2)));
+typedef u32x4_t u32x4w_t __attribute__((aligned(4)));
 typedef u32x2_t u32x2u_t __attribute__((aligned(2)));
 
 // 8 elements

@@ -570,7 +570,7 @@ typedef struct sffn_norm_grad {
 } sffn_norm_grad;
 
 /* The workspace (256-byte aligned; not shared by calls that overlap) is for
- * dweight and may be NULL without it. */
+ * dweight and may be NULL without it, and where its size is 0 (small matrices). */
 sffn_status sffn_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes);
 sffn_status sffn_rms_norm_backward(const sffn_norm_grad* grad, int64_t rows, int64_t cols,
                                    void* ws, size_t ws_bytes, hipStream_t stream);

@@ -12,7 +12,8 @@ ds = r (g - xh c): with E = 50 the mean c is off by E u mean |g xh|, xh and g by
 2 u of themselves; every further operation by half a step of its result. So
   |err| <= u (r (6 |g| + 6 |xh c| + E |xh| mean |g xh|) + 2 |ds|).
 dw sums rows of dy xh, a lane at most ceil(T / 512) of them and up to 3 + 32 + 16
-additions after that: |err| <= (ceil(T / 512) + 54) u sum |dy xh|."""
+additions after that, or (in one launch, T <= 2048) at most 32 rows and 4 + 8:
+|err| <= (ceil(T / 512) + 54) u sum |dy xh|."""
 import numpy as np
 import pytest
 import torch
@@ -201,7 +202,8 @@ def test_gradient(rows, cols):
     _check_grads(*sffn.rms_norm_backward(dy, s, r, w, dstream=d), *a)
 
 
-@pytest.mark.parametrize("rows,cols", [(2, 1), (9, 100), (777, 1003), (2500, 300), (2100, 2048),
+@pytest.mark.parametrize("rows,cols", [(2, 1), (3, 7), (9, 100), (777, 1003), (2047, 8), (2048, 33),
+                                       (2048, 1024), (257, 8191), (2500, 300), (2100, 2048),
                                        (1030, 4096), (600, 6000), (520, 10000)])
 @pytest.mark.parametrize("dd,sd,wd,di,od", [(BF16, BF16, F32, None, BF16),
                                             (BF16, F32, BF16, BF16, F32),
@@ -298,6 +300,37 @@ def test_refusals():
     big = torch.zeros(1, 16385, device="cuda")
     with pytest.raises(sffn.SffnError):
         sffn.rms_norm_backward(big, big, r[:1])
+
+
+def test_aliases():
+    """A result in x's place, the sum in x's place."""
+    x, res, w = _rand((40, 300), 1), _rand((40, 300), 2), _rand((300,), 3)
+    y, s = sffn.rms_norm(x, w, residual=res, dtype=F32)
+    a = x.clone()
+    assert sffn.rms_norm(a, w, residual=res, out=a)[0] is a and torch.equal(a, y)
+    a = x.clone()
+    got = sffn.rms_norm(a, w, residual=res, dtype=F32, residual_out=a)
+    assert got[1] is a and torch.equal(a, s) and torch.equal(got[0], y)
+
+
+def test_two_streams():
+    """Calls that overlap on two streams: nothing is shared."""
+    args = [_grads(n, c, BF16, F32, di=F32, seed=n) for n, c in ((3000, 1500), (300, 900))]
+    want = []
+    for dy, s, r, w, d in args:
+        want.append((*sffn.rms_norm(dy, w, residual=s), *sffn.rms_norm_backward(dy, s, r, w, dstream=d)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    got = [[], []]
+    for _ in range(10):
+        for k, (st, (dy, s, r, w, d)) in enumerate(zip(streams, args)):
+            with torch.cuda.stream(st):
+                got[k].append((*sffn.rms_norm(dy, w, residual=s),
+                               *sffn.rms_norm_backward(dy, s, r, w, dstream=d)))
+    torch.cuda.synchronize()
+    for g, ref in zip(got, want):
+        for one in g:
+            assert all(torch.equal(a, b) for a, b in zip(one, ref))
 
 
 def test_graphs_share_nothing():

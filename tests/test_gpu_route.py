@@ -75,6 +75,10 @@ def test_ties(scores, biased):
     bias = torch.zeros(96, device="cuda") if biased else None
     for c in ((96, 20, 1, 1, 1), (96, 8, 12, 5, 2), (96, 8, 12, 5, 1)):
         _check(c, scores, True, 1.0, logits, bias)
+    # more equal ones than a wave has lanes
+    even = torch.full((3, 300), 0.25, device="cuda")
+    _check((300, 7, 1, 1, 1), scores, True, 1.0, even,
+           torch.full((300,), 0.5, device="cuda") if biased else None)
     z = torch.zeros(2, 96, device="cuda")
     r, _ = _router((96, 5, 4, 2, 2), scores, True)
     assert r.forward(z, bias)[0].tolist() == [[0, 1, 2, 3, 4]] * 2

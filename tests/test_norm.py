@@ -94,13 +94,14 @@ def test_limits_and_empty():
     dict(ds=None), dict(ds=P + 2), dict(dstream=P + 1), dict(weight=None), dict(weight=P + 2),
     dict(dweight=P + 2), dict(lddy=63), dict(lds=63), dict(lddstream=63), dict(ldds=63),
     dict(dy_dtype=2), dict(s_dtype=-1), dict(dstream_dtype=3), dict(weight_dtype=2),
-    dict(ds_dtype=3), dict(rows=-1), dict(cols=-1), dict(ws=None), dict(ws=P + 16),
-    dict(ws_bytes=255), dict(rows=0, weight=None), dict(rows=0, weight=P + 2)])
+    dict(ds_dtype=3), dict(rows=-1), dict(cols=-1), dict(rows=1 << 20, ws=None),
+    dict(rows=1 << 20, ws=P + 16), dict(rows=1 << 20, ws_bytes=512 * 64 * 4 - 1),
+    dict(rows=0, weight=None), dict(rows=0, weight=P + 2)])
 def test_backward_refusals(kw):
     a = dict(dy=P, s=P, dstream=P, weight=P, rstd=P, ds=P, dweight=P, lddy=64, lds=64,
              lddstream=64, ldds=64, dy_dtype=0, s_dtype=1, dstream_dtype=1, weight_dtype=0,
              ds_dtype=0)
-    b = dict(rows=1, cols=64, ws=P, ws_bytes=256)
+    b = dict(rows=1, cols=64, ws=P, ws_bytes=1 << 30)
     for k, v in kw.items():
         (a if k in a else b)[k] = v
     assert B.load_library().sffn_rms_norm_backward(

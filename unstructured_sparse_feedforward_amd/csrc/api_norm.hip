@@ -98,8 +98,8 @@ sffn_status sffn_rms_norm_backward(const sffn_norm_grad* n, int64_t rows, int64_
       return SFFN_E_ARG;
     if (n->lddy < cols || n->lds < cols || n->ldds < cols || (n->dstream && n->lddstream < cols))
       return SFFN_E_ARG;
-    if (n->dweight && (!aligned(ws, kAlign) || ws_bytes < workspace(rows, cols)))
-      return SFFN_E_ARG;
+    const size_t need = n->dweight ? workspace(rows, cols) : 0;
+    if (need > 0 && (!aligned(ws, kAlign) || ws_bytes < need)) return SFFN_E_ARG;
   }
   NormGradArgs a = {};
   a.dy = n->dy;
@@ -122,6 +122,7 @@ sffn_status sffn_rms_norm_backward(const sffn_norm_grad* n, int64_t rows, int64_
   a.w_bf = n->weight && n->weight_dtype == SFFN_BF16;
   a.ds_bf = n->ds_dtype == SFFN_BF16;
   a.parts = norm_grad_parts(rows, cols);
+  a.slabs = a.parts == 0 && n->dweight ? norm_grad_slabs(cols) : 0;
   return done(launch_norm_grad(a, stream));
 }
 

@@ -198,15 +198,75 @@ __global__ __launch_bounds__(Row<L>::NT) void norm_kernel(NormArgs a) {
   else store_row<L, V>(a.out, row * a.ldo, !WIDE, a.cols, l, s);
 }
 
+// dw of kSlab columns over all rows, by a workgroup of NT threads: four lanes
+// have 8 columns each of a row (of cols >= 8; the last ones' run is moved to end
+// with the row), so a wave 16 rows; 8 rows of a lane are loaded at a time.
+constexpr int kSlab = 32;
+template <int NT>
+__device__ __forceinline__ void columns_dw(const NormGradArgs& a, int slab, float* red) {
+  constexpr int STEP = NT / 4, U = 8;
+  const int c = slab * kSlab + (threadIdx.x & 3) * CH, c0 = min(c, a.cols - CH);
+  float dw[CH] = {};
+  for (int64_t r0 = threadIdx.x >> 2; r0 < a.rows; r0 += STEP * U) {
+    Piece s[U][1], g[U][1];
+    float r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = min(r0 + u * STEP, a.rows - 1);
+      load_row<1, 1>(a.s, row * a.lds + c0, a.s_bf, CH, 0, s[u]);
+      load_row<1, 1>(a.dy, row * a.lddy + c0, a.dy_bf, CH, 0, g[u]);
+      r[u] = a.rstd[row];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (r0 + u * STEP >= a.rows) break;
+      float sv[1][CH], gv[1][CH];
+      values(s[u], a.s_bf, sv);
+      values(g[u], a.dy_bf, gv);
+#pragma unroll
+      for (int j = 0; j < CH; ++j) dw[j] = fmaf(gv[0][j], sv[0][j] * r[u], dw[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+#pragma unroll
+    for (int o = 4; o < 64; o <<= 1) dw[j] += __shfl_xor(dw[j], o);
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (lane < 4) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+      if (c0 + j >= c) red[wave * kSlab + c0 + j - slab * kSlab] = dw[j];
+  }
+  __syncthreads();
+  const int col = slab * kSlab + threadIdx.x;
+  if (threadIdx.x < kSlab && col < a.cols) {
+    float v = red[threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) v += red[w * kSlab + threadIdx.x];
+    a.dw[col] = v;
+  }
+}
+
 // A workgroup's rows are blockIdx.x ROWS + .., and every gridDim.x ROWS from
 // there on: it sums its rows' dy xh in registers, its waves' sums through LDS,
 // and writes one row of the workspace.
-template <int L, int V>
+//
+// ONE: little enough to be read a second time: the first a.slabs workgroups
+// form dw, which needs no row's sum, from columns of their own, the others ds
+// of a row each, and there is no second launch (777 x 1003 bf16: a call 14.5
+// us, 10 so).
+template <int L, int V, bool ONE>
 __global__ __launch_bounds__(Row<L>::NT) void norm_grad_kernel(NormGradArgs a) {
-  constexpr int ROWS = Row<L>::ROWS;
+  constexpr int ROWS = Row<L>::ROWS, NT = Row<L>::NT;
   __shared__ float share[2][16];
-  __shared__ float red[ROWS > 1 ? (ROWS - 1) * L * V * CH : 1];
+  __shared__ float red[ONE ? NT / 64 * kSlab : ROWS > 1 ? (ROWS - 1) * L * V * CH : 1];
   const int l = threadIdx.x % L, mine = threadIdx.x / L;
+  const int block = ONE ? (int)blockIdx.x - a.slabs : (int)blockIdx.x;
+  if (ONE && block < 0) {
+    columns_dw<NT>(a, blockIdx.x, red);
+    return;
+  }
   // The next row's loads are issued before this row's sum is waited for, and
   // the weights are kept (of rows over 8192 both would take more registers than
   // 16 waves have).
@@ -233,8 +293,8 @@ __global__ __launch_bounds__(Row<L>::NT) void norm_grad_kernel(NormGradArgs a) {
     if (a.ds_in) load_row<L, V>(a.ds_in, row * a.lddi, a.di_bf, a.cols, l, pd);
     r = a.rstd[row];
   };
-  const int64_t step = (int64_t)gridDim.x * ROWS;
-  int64_t row = (int64_t)blockIdx.x * ROWS + mine;    // (with L > 64 a workgroup has one row)
+  const int64_t step = (int64_t)(ONE ? gridDim.x - a.slabs : gridDim.x) * ROWS;
+  int64_t row = (int64_t)block * ROWS + mine;    // (with L > 64 a workgroup has one row)
   int turn = 0;
   if (AHEAD && row < a.rows) load(row);
   for (; row < a.rows; row += step) {
@@ -275,7 +335,7 @@ __global__ __launch_bounds__(Row<L>::NT) void norm_grad_kernel(NormGradArgs a) {
     }
     store_row<L, V>(a.ds, row * a.ldds, a.ds_bf, a.cols, l, s);
   }
-  if (!a.dw) return;
+  if (ONE || !a.dw) return;
   if constexpr (ROWS > 1) {
     if (mine > 0) {
 #pragma unroll
@@ -325,7 +385,14 @@ hipError_t norm(const NormArgs& a, hipStream_t s) {
 }
 template <int L, int V>
 hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
-  norm_grad_kernel<L, V><<<a.parts, Row<L>::NT, 0, s>>>(a);
+  if constexpr (L * V * CH <= 8192) {
+    if (a.parts == 0) {
+      const unsigned rows = (unsigned)((a.rows + Row<L>::ROWS - 1) / Row<L>::ROWS);
+      norm_grad_kernel<L, V, true><<<a.slabs + rows, Row<L>::NT, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  }
+  norm_grad_kernel<L, V, false><<<a.parts, Row<L>::NT, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -345,10 +412,21 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   return norm<1024, 2>(a, s);
 }
 
+// Whether one launch forms ds and dw: up to 2^21 elements, whose second reading
+// is from the caches, and 2048 rows, which a workgroup sums in little time (us,
+// from graphs: 777 x 1003 bf16 7.3, two launches 9.3; 1024 x 2048 float32 11.5,
+// 13.4; 2000 x 256 10.4, 9.3, where the second launch costs the host 4 more; 4096
+// x 512 25.6, 12.9; 2048 x 2048 bf16 14.7, 13.6).
+static bool norm_grad_one(int64_t rows, int64_t cols) {
+  return cols >= CH && cols <= 8192 && rows <= 2048 && rows * cols <= (int64_t)1 << 21;
+}
+int norm_grad_slabs(int64_t cols) { return (int)((cols + kSlab - 1) / kSlab); }
+
 // The gradient's workgroups, each of which writes its sums for dw: as many as
 // keep the memory busy (8192 x 2048: float32 53 us, by 256 52, 1024 56; bf16 31,
 // 40, 33; 4096 x 4096 47, by 512 49; 16384 x 64 13.5, by 512 15.4).
 int norm_grad_parts(int64_t rows, int64_t cols) {
+  if (norm_grad_one(rows, cols)) return 0;
   const int64_t each = cols <= 1024 ? 4 : 1;      // rows a workgroup at a time
   const int64_t most = cols <= 512 ? 768 : cols <= 2048 ? 512 : 256;
   return (int)min((rows + each - 1) / each, most);
@@ -365,7 +443,7 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
   else if (a.cols <= 4096) e = norm_grad<512, 1>(a, s);
   else if (a.cols <= 8192) e = norm_grad<512, 2>(a, s);
   else e = norm_grad<1024, 2>(a, s);
-  if (e != hipSuccess || !a.dw) return e;
+  if (e != hipSuccess || !a.dw || (a.parts == 0 && a.rows > 0)) return e;
   norm_dw_kernel<<<(unsigned)((a.cols + 63) / 64), kDwWaves * 64, 0, s>>>(a);
   return hipGetLastError();
 }

@@ -42,10 +42,13 @@ struct NormGradArgs {
   int64_t rows;
   int cols;
   int dy_bf, s_bf, di_bf, w_bf, ds_bf;
-  int parts;
+  int parts;                // rows of the workspace
+  int slabs;                // of columns, where dw needs no workspace (else 0)
 };
-// rows of the workspace (and workgroups of the first kernel)
+// rows of the workspace, and workgroups of the first kernel; 0: one launch does
+// without
 int norm_grad_parts(int64_t rows, int64_t cols);
+int norm_grad_slabs(int64_t cols);
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s);
 
 }  // namespace sffn

@@ -137,9 +137,10 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, rstd: torch.Tensor,
         else:
             pdw, _ = _vector(dweight, cols, dev, "dweight", f32=True)
         nb = _workspace_bytes(rows, cols)
-        # torch's allocations are 512-byte aligned
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-        pws = ws.data_ptr()
+        if nb > 0:
+            # torch's allocations are 512-byte aligned
+            ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+            pws = ws.data_ptr()
     elif dweight is not None:
         raise ValueError("dweight is given without a weight")
     out, ldo, od = _result(out, rows, cols, dtype, dev)

@@ -268,16 +268,67 @@ def test_views_out_n_tokens():
         assert (buf == 7).all()
 
 
-def test_many_tokens():
-    """Beyond one grid's worth of workgroups a CU; against sorting."""
-    T, E, k = 20001, 96, 5
-    l = _rand((T, E), 6)
-    r, _ = _router((E, k, 1, 1, 1), "softmax", True)
-    ids, p = r.forward(l)
-    top = l.sort(dim=1, descending=True, stable=True)
-    assert torch.equal(ids.long(), top.indices[:, :k])
-    ref = torch.softmax(top.values[:, :k].double(), dim=1)
-    assert ((p.double() - ref).abs() <= 1.01 * U * ref).all()
+def _plain(l, c, scores, bias, normalize):
+    """The definition in float64 torch operations."""
+    E, k, G, tg, gb = c
+    l = l.double()
+    s = torch.softmax(l, 1) if scores == "softmax" else torch.sigmoid(l)
+    ch = s if bias is None else s + bias.double()
+    key = l if bias is None else ch
+    if tg < G:
+        g = ch.view(-1, G, E // G).sort(dim=2, descending=True).values[:, :, :gb].sum(2)
+        kept = g.sort(dim=1, descending=True, stable=True).indices[:, :tg]
+        keep = torch.zeros_like(g, dtype=torch.bool).scatter_(1, kept, True)
+        key = key.masked_fill(~keep.repeat_interleave(E // G, 1), -float("inf"))
+    ids = key.sort(dim=1, descending=True, stable=True).indices[:, :k]
+    p = s.gather(1, ids)
+    return ids, p / p.sum(1, keepdim=True) if normalize else p
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("c", [(64, 6, 1, 1, 1), (64, 15, 16, 5, 2), (60, 8, 4, 2, 2), (5, 2, 1, 1, 1),
+                               (64, 16, 1, 1, 1), (96, 5, 1, 1, 1), (128, 31, 32, 11, 2),
+                               (128, 8, 4, 2, 1), (256, 8, 8, 4, 2)])
+def test_many_tokens(c, scores, biased):
+    """Several tokens a wave, the last wave's not all there; against sorting,
+    bfloat16 logits (with ties, of groups too) as well."""
+    for T, dt, normalize in ((20001, F32, True), (9003, BF16, False), (5000, BF16, True)):
+        l = _rand((T, c[0]), 6, dt)
+        bias = _rand((c[0],), 7, scale=0.2) if biased else None
+        r, _ = _router(c, scores, normalize)
+        ids, p = r.forward(l, bias)
+        oi, op = _plain(l, c, scores, bias, normalize)
+        assert torch.equal(ids.long(), oi)
+        assert ((p.double() - op).abs() <= 1.01 * U * op).all()
+
+
+def test_many_tokens_masked_and_counted():
+    """Several tokens a wave with masked experts, rows without any, equal ones
+    throughout, and fewer tokens than rows."""
+    for c in ((64, 6, 1, 1, 1), (64, 6, 8, 3, 2), (128, 8, 1, 1, 1)):
+        T, E, k = 9000, c[0], c[1]
+        l = _rand((T, E), 3)
+        l[::7] = -float("inf")
+        l[1::7, k - 2:] = -float("inf")
+        l[2::7] = 0.5
+        l[3::7, 5] = float("nan")
+        bias = _rand((E,), 4, scale=0.2)
+        bias[::3] = 0
+        for scores in ("softmax", "sigmoid"):
+            for b in (None, bias, torch.zeros_like(bias)):
+                r, kw = _router(c, scores, True)
+                ids, p = r.forward(l, b)
+                for rows in (slice(0, 28), slice(T - 28, T)):
+                    keep = [i for i in range(28) if (i + (0 if rows.start == 0 else T - 28)) % 7 != 3]
+                    oi, op = ro.forward(_np(l[rows])[keep], k, bias=_np(b), **kw)
+                    assert np.array_equal(ids[rows].cpu().numpy()[keep], oi)
+                    assert (np.abs(_np(p[rows])[keep] - op) <= 1.01 * U * op + 1e-45).all()
+                n = torch.full((1,), 4097, dtype=torch.int32, device="cuda")
+                out = (torch.full_like(ids, 77), torch.full_like(p, 7.0))
+                r.forward(l, b, n_tokens=n, out=out)
+                assert torch.equal(out[0][:4097], ids[:4097]) and (out[0][4097:] == 77).all()
+                assert (out[1][4097:] == 7).all()
 
 
 def test_empty_and_refusals():

@@ -10,11 +10,12 @@
 // not of a rounding. Without a bias experts are compared by their logits,
 // which have the order of the scores.
 //
-// A wave has a token, a lane N consecutive experts, from lane N on. Bytes are
-// few (8192 tokens of 256 experts: 8.9 MB, 2 us); the time is that of the
-// waves' instructions, most of them for the k maxima. So a token is first done in
-// 32 bits, with a check that every comparison that matters was clear of the
-// roundings, and in 64 only where one was not (a few tokens in a hundred).
+// A wave has a token, or, of many, LPT of its lanes have one, a lane N
+// consecutive experts. Bytes are few (8192 tokens of 256 experts: 8.9 MB, 2 us);
+// the time is that of the waves' instructions, most of them for the k maxima. So
+// a token is first done in 32 bits, with a check that every comparison that
+// matters was clear of the roundings, and in 64 only where one was not (a few
+// tokens in a thousand).
 #include "route.hpp"
 #include "rowio.hpp"
 
@@ -89,74 +90,98 @@ __device__ __forceinline__ void store_run(E* p, int left, const float (&v)[N]) {
       if (i < left) st(p + i, v[i]);
   }
 }
+// A lane's place: seg the first lane of its token's, pos its own among them.
+template <int LPT>
+__device__ __forceinline__ int seg_of(int lane) { return LPT == 64 ? 0 : lane & -LPT; }
+template <int LPT>
+__device__ __forceinline__ int pos_of(int lane) { return LPT == 64 ? lane : lane & (LPT - 1); }
+
 template <int N>
-__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, float (&l)[N]) {
-  const int e0 = (threadIdx.x & 63) * N;
-  if (a.bf) load_run<N>((const uint16_t*)a.logits + t * a.ldl + e0, a.E - e0, -INFINITY, l);
-  else load_run<N>((const float*)a.logits + t * a.ldl + e0, a.E - e0, -INFINITY, l);
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, int e0, int left,
+                                            float (&l)[N]) {
+  if (a.bf) load_run<N>((const uint16_t*)a.logits + t * a.ldl + e0, left, -INFINITY, l);
+  else load_run<N>((const float*)a.logits + t * a.ldl + e0, left, -INFINITY, l);
 }
 
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
+// sums and maxima over a token's lanes, in all of them
+template <int LPT, typename T>
+__device__ __forceinline__ T seg_sum(T v) {
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  for (int o = 1; o < LPT; o <<= 1) v += __shfl_xor(v, o);
   return v;
 }
-// the sum over the first k lanes (0 in the others), in those
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) { return seg_sum<64>(v); }
+// the sum over the token's first k lanes (the others have 0), in those
 __device__ __forceinline__ double lanes_sum(double v, int k) {
 #pragma unroll 1
   for (int o = 1; o < k; o <<= 1) v += __shfl_xor(v, o);
   return v;
 }
-// the largest of the wave, in all lanes: a scan by lanes of a row, then rows
-// into the next ones; the last lane has it
+#define SFFN_DPP(ctrl) v = max(v, __builtin_amdgcn_update_dpp(v, v, ctrl, 0xF, 0xF, false))
+// a scan by lanes of a row of 16, then rows into the next ones; the last lane
+// has it
 __device__ __forceinline__ int wave_max(int v) {
-#define SFFN_STEP(ctrl) v = max(v, __builtin_amdgcn_update_dpp(v, v, ctrl, 0xF, 0xF, false))
-  SFFN_STEP(0x111);    // from the lane 1, 2, 4, 8 before, of the same 16
-  SFFN_STEP(0x112);
-  SFFN_STEP(0x114);
-  SFFN_STEP(0x118);
-  SFFN_STEP(0x142);    // the last of a row of 16 to the next row
-  SFFN_STEP(0x143);    // lane 31 to the upper half
-#undef SFFN_STEP
+  SFFN_DPP(0x111);    // from the lane 1, 2, 4, 8 before, of the same 16
+  SFFN_DPP(0x112);
+  SFFN_DPP(0x114);
+  SFFN_DPP(0x118);
+  SFFN_DPP(0x142);    // the last of a row of 16 to the next row
+  SFFN_DPP(0x143);    // lane 31 to the upper half
   return __builtin_amdgcn_readlane(v, 63);
 }
-// (a NaN is ignored)
-__device__ __forceinline__ float wave_max(float v) {
-  return key_value(wave_max(v != v ? kNone : order_key(v)));
+template <int LPT>
+__device__ __forceinline__ int seg_max(int v) {
+  if constexpr (LPT == 64) return wave_max(v);
+  SFFN_DPP(0xB1);     // neighbours, pairs, halves and wholes of a row of 16
+  SFFN_DPP(0x4E);
+  SFFN_DPP(0x141);
+  SFFN_DPP(0x140);
+  if constexpr (LPT == 32) {
+    const auto o = __builtin_amdgcn_permlane16_swap(v, v, false, false);   // and of two rows
+    v = max((int)o[0], (int)o[1]);
+  }
+  return v;
 }
+#undef SFFN_DPP
+// (a NaN is ignored)
+template <int LPT>
+__device__ __forceinline__ float seg_max(float v) {
+  return key_value(seg_max<LPT>(v != v ? kNone : order_key(v)));
+}
+__device__ __forceinline__ float wave_max(float v) { return seg_max<64>(v); }
 __device__ __forceinline__ float lane_value(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
 
-// the logit of expert e, by lane
+// the logit of the token's expert e, by lane
 template <int N>
-__device__ __forceinline__ float value_of(const float (&l)[N], int e) {
-  float v = __shfl(l[0], e / N);
+__device__ __forceinline__ float value_of(const float (&l)[N], int seg, int e) {
+  float v = __shfl(l[0], seg + e / N);
 #pragma unroll
   for (int i = 1; i < N; ++i) {
-    const float o = __shfl(l[i], e / N);
+    const float o = __shfl(l[i], seg + e / N);
     v = e % N == i ? o : v;
   }
   return v;
 }
 
 // The largest of a row's logits; -infinity of an empty one.
-template <int N>
+template <int N, int LPT>
 __device__ __forceinline__ float row_max(const float (&l)[N]) {
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
-  m = wave_max(m);
+  m = seg_max<LPT>(m);
   return m != m ? -INFINITY : m;     // (every one a NaN)
 }
 
 // The two largest of a group's c, in all of its lanes: P = 2^lp lanes have a
 // group, and share out its members in LDS. (NaNs are ignored.)
 template <typename T>
-__device__ __forceinline__ void group_best(const RouteArgs& a, const T* cs, int lp, T& b1, T& b2) {
-  const int lane = threadIdx.x & 63;
-  const int g = lane >> lp, p = lane & ((1 << lp) - 1);
+__device__ __forceinline__ void group_best(const RouteArgs& a, const T* cs, int pos, int lp, T& b1,
+                                           T& b2) {
+  const int g = pos >> lp, p = pos & ((1 << lp) - 1);
   b1 = b2 = -INFINITY;
   if (g < a.groups) {
     for (int j = p; j < a.per; j += 1 << lp) {
@@ -176,16 +201,17 @@ __device__ __forceinline__ void group_best(const RouteArgs& a, const T* cs, int 
 __device__ __forceinline__ int group_of(const RouteArgs& a, int e) {
   return (int)(((float)e + 0.5f) * a.inv_per);
 }
-// whether the group of expert e is among those kept (a bit for each lane)
-__device__ __forceinline__ bool kept(const RouteArgs& a, uint64_t keep, int lp, int e) {
-  return (keep >> (group_of(a, e) << lp)) & 1;
+// whether the group of expert e is among those kept (a bit for each lane, the
+// token's from seg on)
+__device__ __forceinline__ bool kept(const RouteArgs& a, uint64_t keep, int seg, int lp, int e) {
+  return (keep >> (seg + (group_of(a, e) << lp))) & 1;
 }
 
 // What a token needs in 64 bits where 32 cannot tell: small code, rolled over
 // the row in LDS, since a wave that needs it fetches it first, and alone.
 
-// c of the token's experts, lane, 64 + lane, .. of each lane, into cs; of
-// groups the lanes of those that are kept, a bit for each.
+// c of the token's experts, lane, 64 + lane, .. of each lane of the wave, into
+// cs; of groups, 2^lp lanes each, the lanes of those that are kept.
 template <bool BIAS, bool GROUPED>
 __device__ __forceinline__ uint64_t scores64(const RouteArgs& a, int64_t t, float m, double* cs,
                                              int lp) {
@@ -214,7 +240,7 @@ __device__ __forceinline__ uint64_t scores64(const RouteArgs& a, int64_t t, floa
   if (!GROUPED) return ~0ull;
   __builtin_amdgcn_wave_barrier();     // (a wave's own part of LDS)
   double b1, b2;
-  group_best<double>(a, cs, lp, b1, b2);
+  group_best<double>(a, cs, lane, lp, b1, b2);
   const int mine = lane >> lp;
 #pragma unroll 1
   for (int o = 1; o < 64; o <<= 1) nan |= __shfl_xor(nan, o);
@@ -238,7 +264,7 @@ __device__ __forceinline__ int choose64(const RouteArgs& a, int64_t t, float m, 
   long long* key = (long long*)cs;
 #pragma unroll 1
   for (int e = lane; e < a.E; e += 64)
-    key[e] = !GROUPED || kept(a, keep, lp, e)
+    key[e] = !GROUPED || kept(a, keep, 0, lp, e)
                  ? order_key(BIAS ? cs[e] : (double)logit(a, t, e)) : kNone64;
   int id = 0;
 #pragma unroll 1
@@ -273,12 +299,13 @@ __device__ __forceinline__ int choose64(const RouteArgs& a, int64_t t, float m, 
 // times their size are in the order of the exact ones, and two sums of two
 // where it is more than twice that and 2^-22 times their size. Without a bias the experts' keys are the
 // logits themselves, which are exact.
-template <int N, bool BIAS, bool GROUPED>
+template <int N, int LPT, bool BIAS, bool GROUPED>
 __device__ __forceinline__ int choose32(const RouteArgs& a, int64_t t, const float (&l)[N],
-                                        float m, double* cs64, int lp, bool* sure) {
+                                        float m, double* cs64, int* ids, bool* sure) {
   constexpr float kLog2e = 1.44269504f;
-  const int lane = threadIdx.x & 63, e0 = lane * N;
-  float* cs = (float*)cs64;
+  const int lane = threadIdx.x & 63, seg = seg_of<LPT>(lane), pos = pos_of<LPT>(lane);
+  const int e0 = pos * N;
+  float* cs = (float*)cs64 + seg * N;
   int key[N];
   bool clear = true;
   float room = 0.0f;
@@ -298,7 +325,7 @@ __device__ __forceinline__ int choose32(const RouteArgs& a, int64_t t, const flo
         c[i] = __builtin_amdgcn_exp2f(kLog2e * (l[i] - m));    // (m = -infinity: NaN)
         sum += c[i];
       }
-      const float inv = __builtin_amdgcn_rcpf(wave_sum(sum));
+      const float inv = __builtin_amdgcn_rcpf(seg_sum<LPT>(sum));
 #pragma unroll
       for (int i = 0; i < N; ++i) c[i] *= inv;
       room = 0x1p-16f * inv;
@@ -320,34 +347,39 @@ __device__ __forceinline__ int choose32(const RouteArgs& a, int64_t t, const flo
         nan |= c[i] != c[i];
       }
       __builtin_amdgcn_wave_barrier();     // (a wave's own part of LDS)
+      const int lp = a.lp[LPT == 64 ? 0 : LPT == 32 ? 1 : 2];
       float b1, b2;
-      group_best<float>(a, cs, lp, b1, b2);
+      group_best<float>(a, cs, pos, lp, b1, b2);
       const float score = a.best == 2 ? b1 + b2 : b1;
-      const int gk = order_key(score), mine = lane >> lp;
+      const int gk = order_key(score), mine = pos >> lp;
       int before = 0;
 #pragma unroll 4
       for (int g = 0; g < a.groups; ++g) {
-        const int o = __builtin_amdgcn_readlane(gk, g << lp);
+        const int o = LPT == 64 ? __builtin_amdgcn_readlane(gk, g << lp)
+                                : __shfl(gk, seg + (g << lp));
         before += o > gk || (o == gk && g < mine);
       }
       const bool valid = mine < a.groups, stays = valid && before < a.top_groups;
       uint64_t keep = __ballot(stays);
       // the last that is kept and the first that is not
-      const float low = -wave_max(stays ? -score : -INFINITY);
-      const float high = wave_max(valid && !stays ? score : -INFINITY);
-      if (!(low - high > 2.0f * room + 0x1p-22f * (fabsf(low) + fabsf(high))) ||
-          __ballot(nan) != 0)
-        keep = scores64<BIAS, GROUPED>(a, t, m, cs64, lp);
+      const float low = -seg_max<LPT>(stays ? -score : -INFINITY);
+      const float high = seg_max<LPT>(valid && !stays ? score : -INFINITY);
+      clear = low - high > 2.0f * room + 0x1p-22f * (fabsf(low) + fabsf(high));
+      clear = clear && seg_max<LPT>((int)nan) == 0;
+      if constexpr (LPT == 64) {
+        if (!clear) keep = scores64<BIAS, GROUPED>(a, t, m, cs64, lp);
+        clear = true;
+      }
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (!kept(a, keep, lp, e0 + i)) key[i] = kNone;
+        if (!kept(a, keep, seg, lp, e0 + i)) key[i] = kNone;
     }
   }
   // The k largest, one after the other, and with a bias more until one is
-  // clearly less than the last: lane r takes that of rank r. Of equal keys the
-  // lower index is first.
-  constexpr bool SORT = N > 1 && N <= 4;      // the lane's own keys, descending
-  uint32_t at = 0;                            // and whose they are, 2 bits each
+  // clearly less than the last: lane r takes that of rank r (of several tokens a
+  // wave by way of LDS). Of equal keys the lower index is first.
+  constexpr bool SORT = N > 1 && N <= 8;      // the lane's own keys, descending
+  uint32_t at = 0;                            // and whose they are, 3 bits each
   if constexpr (SORT) {
     int idx[N];
 #pragma unroll
@@ -364,121 +396,149 @@ __device__ __forceinline__ int choose32(const RouteArgs& a, int64_t t, const flo
         idx[i + 1] = swap ? i0 : idx[i + 1];
       }
 #pragma unroll
-    for (int i = 0; i < N; ++i) at |= idx[i] << (2 * i);
+    for (int i = 0; i < N; ++i) at |= (uint32_t)idx[i] << (3 * i);
   }
-  int id = 0, n = a.k;
-  bool ties = false;
+  const auto drop = [&](bool mine, int j) {
+    if constexpr (SORT) {
+#pragma unroll
+      for (int i = 0; i + 1 < N; ++i) key[i] = mine ? key[i + 1] : key[i];
+      key[N - 1] = mine ? kNone : key[N - 1];
+      at >>= mine ? 3 : 0;
+    } else {
+      const int d = mine ? j : -1;
+#pragma unroll
+      for (int i = 0; i < N; ++i) key[i] = d == i ? kNone : key[i];
+    }
+  };
+  const auto place = [&](int best) {      // of the lane's largest
+    if constexpr (SORT) return (int)(at & 7);
+    int j = N - 1;
+#pragma unroll
+    for (int i = N - 2; i >= 0; --i) j = key[i] == best ? i : j;
+    return j;
+  };
+  int id = 0, n = a.k;          // n: found that may be among the k
+  bool ties = false, done = false;
   float last = INFINITY;
+  int r = 0;
 #pragma unroll 1
-  for (int r = 0;; ++r) {
+  for (;; ++r) {
+    if (!BIAS && r == a.k) break;
     int bk = key[0];
     if constexpr (!SORT) {
 #pragma unroll
       for (int i = 1; i < N; ++i) bk = max(bk, key[i]);
     }
-    if (!BIAS && r == a.k) break;
-    const int best = wave_max(bk);
+    const int best = seg_max<LPT>(bk);
     if (BIAS) {
       const float v = key_value(best);
       const bool apart = r == 0 || last - v > room + 0x1p-23f * (fabsf(last) + fabsf(v));
-      if (r >= a.k && (apart || best == kNone)) {
+      if (!done && r >= a.k && (apart || best == kNone)) {
+        done = true;
         n = r;
-        break;
       }
-      if (r == 63) {      // no lane for more
-        clear = false;
-        break;
-      }
-      ties |= !apart;
+      ties |= !done && !apart;
       last = v;
+      if (LPT == 64 ? done : __ballot(!done) == 0) break;
+      if (r == LPT - 1) {      // no lane for more
+        clear = clear && done;
+        break;
+      }
     }
-    const int who = __ffsll((unsigned long long)__ballot(bk == best)) - 1;
-    int j = 0;
-    if constexpr (SORT) {
-      j = at & 3;
+    const uint64_t has = __ballot(bk == best);
+    if constexpr (LPT == 64) {
+      const int who = __ffsll((unsigned long long)has) - 1;
+      const int j = __builtin_amdgcn_readlane(place(best), who);
+      if (lane == r) id = who * N + j;
+      drop(lane == who, j);
     } else {
-      j = N - 1;
-#pragma unroll
-      for (int i = N - 2; i >= 0; --i) j = key[i] == best ? i : j;
-    }
-    j = __builtin_amdgcn_readlane(j, who);
-    if (lane == r) id = who * N + j;
-    if constexpr (SORT) {
-      const bool mine = lane == who;
-#pragma unroll
-      for (int i = 0; i + 1 < N; ++i) key[i] = mine ? key[i + 1] : key[i];
-      key[N - 1] = mine ? kNone : key[N - 1];
-      at >>= mine ? 2 : 0;
-    } else {
-      const int drop = lane == who ? j : -1;
-#pragma unroll
-      for (int i = 0; i < N; ++i) key[i] = drop == i ? kNone : key[i];
+      const bool mine = pos == __builtin_ctz((uint32_t)(has >> seg));
+      const int j = place(best);
+      if (mine) ids[seg + r] = e0 + j;
+      drop(mine, j);
     }
   }
-  if (BIAS && ties && clear) {
-    // The n found hold the k, but not for sure in their order: theirs in 64 bits.
-    // (Softmax scores need the sum over the row.)
-    if (!a.sigmoid) {
-      clear = false;
-    } else {
-      const double c = 1.0 / (1.0 + exp(-(double)value_of<N>(l, id))) + (double)a.bias[id];
+  if constexpr (LPT < 64) {
+    __builtin_amdgcn_wave_barrier();
+    id = ids[lane];
+  }
+  if (BIAS) {
+    if (pos >= n) id = 0;
+    const bool resolve = ties && clear && a.sigmoid;
+    if (ties && !a.sigmoid) clear = false;      // (the scores need the sum over the row)
+    if (__ballot(resolve) != 0) {
+      // The n found hold the k, but not for sure in their order: theirs in 64 bits.
+      const double c = 1.0 / (1.0 + exp(-(double)value_of<N>(l, seg, id))) + (double)a.bias[id];
       const long long mine = order_key(c);
       int before = 0;
 #pragma unroll 1
-      for (int q = 0; q < n; ++q) {
-        const uint32_t lo = __builtin_amdgcn_readlane((int)mine, q);
-        const long long hi = __builtin_amdgcn_readlane((int)(mine >> 32), q);
-        const long long o = hi << 32 | lo;
-        before += o > mine || (o == mine && __builtin_amdgcn_readlane(id, q) < id);
+      for (int q = 0; q < r; ++q) {
+        const long long o = __shfl(mine, seg + q);
+        const int oi = __shfl(id, seg + q);
+        before += q < n && (o > mine || (o == mine && oi < id));
       }
-      id = __builtin_amdgcn_ds_permute((lane < n ? before : lane) << 2, id);
+      const int to = resolve && pos < n ? before : pos;
+      id = __builtin_amdgcn_ds_permute((seg + to) << 2, id);
     }
   }
   *sure = clear;
   return id;
 }
 
-template <int N, bool BIAS, bool GROUPED>
+template <int N, int LPT, bool BIAS, bool GROUPED>
 __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs a) {
+  constexpr int TOKENS = 64 / LPT;
   __shared__ double cs[kWaves][BIAS || GROUPED ? N * 64 : 1];
+  __shared__ int ids[kWaves][LPT < 64 ? 64 : 1];
   const int lane = threadIdx.x & 63, wave = wave_id();
-  const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
-  if (t >= a.T || (a.t_dev && t >= *a.t_dev)) return;
+  const int seg = seg_of<LPT>(lane), pos = pos_of<LPT>(lane), e0 = pos * N;
+  const int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * TOKENS;
+  const int64_t T = a.t_dev ? min(a.T, (int64_t)*a.t_dev) : a.T;
+  if (t0 >= T) return;
+  const int64_t t = t0 + seg / LPT;
+  const bool valid = t < T;      // (the lanes of tokens past the last go along)
   float l[N];
-  load_logits<N>(a, t, l);
-  const float m = a.sigmoid ? 0.0f : row_max<N>(l);
-  // 2^lp lanes a group
-  const int lp = GROUPED ? __builtin_clz(a.groups - 1) - 26 : 6;
+  load_logits<N>(a, t, e0, valid ? a.E - e0 : 0, l);
+  const float m = a.sigmoid ? 0.0f : row_max<N, LPT>(l);
   bool sure;
-  int id = choose32<N, BIAS, GROUPED>(a, t, l, m, cs[wave], lp, &sure);
-  if (BIAS && !sure) id = choose64<BIAS, GROUPED>(a, t, m, cs[wave], lp);
+  int id = choose32<N, LPT, BIAS, GROUPED>(a, t, l, m, cs[wave], ids[wave], &sure);
+  if (BIAS || (GROUPED && LPT < 64)) {
+    // the tokens of the wave one after the other, by all of it
+    for (uint64_t left = __ballot(valid && !sure && pos == 0); left; left &= left - 1) {
+      const int s = __ffsll((unsigned long long)left) - 1;
+      const int one = choose64<BIAS, GROUPED>(a, t0 + s / LPT, lane_value(m, s), cs[wave], a.lp[0]);
+      // (lane r has that of rank r: to the token's lanes)
+      const int moved = __shfl(one, pos);
+      if (seg == s) id = moved;
+    }
+  }
   // the weights, of the k experts alone where that is all they depend on
+  const bool chosen = pos < a.k;
   double sr = 0.0, sum;
-  const float v = value_of<N>(l, id), lr = lane < a.k ? v : -INFINITY;
+  const float v = value_of<N>(l, seg, id), lr = chosen ? v : -INFINITY;
   if (a.sigmoid) {
-    sr = lane < a.k ? 1.0 / (1.0 + exp(-(double)lr)) : 0.0;
+    sr = chosen ? 1.0 / (1.0 + exp(-(double)lr)) : 0.0;
     sum = a.normalize ? lanes_sum(sr, a.k) : 1.0;
   } else {
     // normalised: relative to the chosen ones' largest logit, since a bias may
     // choose experts whose scores are nothing beside the others'
-    const float top = a.normalize ? wave_max(lr) : m;
+    const float top = a.normalize ? seg_max<LPT>(lr) : m;
     const bool some = top == top && top != -INFINITY;
-    sr = some && lane < a.k ? exp((double)lr - (double)top) : 0.0;
+    sr = some && chosen ? exp((double)lr - (double)top) : 0.0;
     if (lr != lr) sr = lr;
     if (a.normalize) {
       sum = lanes_sum(sr, a.k);
     } else {
       sum = 0.0;
-      const int e0 = lane * N;
 #pragma unroll
       for (int i = 0; i < N; ++i)
         if (e0 + i < a.E && (some || l[i] != l[i])) sum += exp((double)l[i] - (double)m);
-      sum = wave_sum(sum);
+      sum = seg_sum<LPT>(sum);
     }
   }
-  if (lane < a.k) {
-    a.ids[t * a.k + lane] = id;
-    a.probs[t * a.k + lane] = sum == 0.0 ? 0.0f : (float)(sr / sum * (double)a.scale);
+  if (chosen && valid) {
+    a.ids[t * a.k + pos] = id;
+    a.probs[t * a.k + pos] = sum == 0.0 ? 0.0f : (float)(sr / sum * (double)a.scale);
   }
 }
 
@@ -495,7 +555,7 @@ __global__ __launch_bounds__(kWaves * 64) void route_grad_kernel(RouteArgs a) {
   if (t >= a.T || (a.t_dev && t >= *a.t_dev)) return;
   const bool all = !a.sigmoid && !a.normalize;
   float l[N];
-  if (all) load_logits<N>(a, t, l);
+  if (all) load_logits<N>(a, t, e0, a.E - e0, l);
   // lane r: the expert of rank r (none where the index is not one)
   int id = -1;
   float g = 0.0f, lr = -INFINITY;
@@ -509,7 +569,7 @@ __global__ __launch_bounds__(kWaves * 64) void route_grad_kernel(RouteArgs a) {
   }
   float total = 0.0f, dr;
   if (all) {
-    const float m = row_max<N>(l);
+    const float m = row_max<N, 64>(l);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       l[i] = e0 + i < a.E && m != -INFINITY ? expf(l[i] - m) : 0.0f;
@@ -566,16 +626,32 @@ hipError_t by_experts(int E, F&& f) {
 
 }  // namespace
 
-hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
-  const unsigned grid = (unsigned)((a.T + kWaves - 1) / kWaves);
-  return by_experts(a.E, [&](auto n) {
-    constexpr int N = decltype(n)::value;
-    const bool grouped = a.top_groups < a.groups;
-    if (a.bias && grouped) route_kernel<N, true, true><<<grid, kWaves * 64, 0, s>>>(a);
-    else if (a.bias) route_kernel<N, true, false><<<grid, kWaves * 64, 0, s>>>(a);
-    else if (grouped) route_kernel<N, false, true><<<grid, kWaves * 64, 0, s>>>(a);
-    else route_kernel<N, false, false><<<grid, kWaves * 64, 0, s>>>(a);
-  });
+hipError_t launch_route(const RouteArgs& in, hipStream_t s) {
+  RouteArgs a = in;
+  const bool grouped = a.top_groups < a.groups;
+  int lg = 0;      // lanes a group, a power of two
+  while ((1 << lg) < a.groups) ++lg;
+  for (int i = 0; i < 3; ++i) a.lp[i] = grouped ? max(6 - i - lg, 0) : 6 - i;
+  const auto go = [&](auto n, auto lpt) {
+    constexpr int N = decltype(n)::value, LPT = decltype(lpt)::value;
+    const int64_t each = kWaves * 64 / LPT;
+    const unsigned grid = (unsigned)((a.T + each - 1) / each);
+    if (a.bias && grouped) route_kernel<N, LPT, true, true><<<grid, kWaves * 64, 0, s>>>(a);
+    else if (a.bias) route_kernel<N, LPT, true, false><<<grid, kWaves * 64, 0, s>>>(a);
+    else if (grouped) route_kernel<N, LPT, false, true><<<grid, kWaves * 64, 0, s>>>(a);
+    else route_kernel<N, LPT, false, false><<<grid, kWaves * 64, 0, s>>>(a);
+    return hipGetLastError();
+  };
+  // Several tokens a wave where there are many and their experts few: they share
+  // its instructions, and it takes longer (us, from graphs: 16384 tokens of 64
+  // experts, top 6, 6.3, a wave a token 10.2, in groups 11.3, 22.2; 4096 4.3, 4.7;
+  // 2048 in groups 6.9, 6.5; 8192 of 128 7.1, 8.0, in groups 12.5, 16.1; 2048 4.5,
+  // 4.4; 8192 of 256 by two a wave 12.8, 10.7).
+  if (a.E <= 64 && a.k < 16 && a.groups <= 16 && a.T >= 4096)
+    return go(std::integral_constant<int, 4>{}, std::integral_constant<int, 16>{});
+  if (a.E <= 128 && a.k < 32 && a.groups <= 32 && a.T >= 8192)
+    return go(std::integral_constant<int, 4>{}, std::integral_constant<int, 32>{});
+  return by_experts(a.E, [&](auto n) { go(n, std::integral_constant<int, 64>{}); });
 }
 hipError_t launch_route_grad(const RouteArgs& a, hipStream_t s) {
   const unsigned grid = (unsigned)((a.T + kWaves - 1) / kWaves);

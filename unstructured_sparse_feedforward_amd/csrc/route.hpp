@@ -19,6 +19,7 @@ struct RouteArgs {
   int sigmoid, normalize, bf;
   float scale;
   float inv_per;             // 1 / per
+  int lp[3];                 // log2 of a group's lanes, of 64, 32 and 16 a token
   int32_t* ids;              // [T, k]
   float* probs;              // [T, k]
   // backward

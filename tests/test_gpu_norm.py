@@ -260,6 +260,29 @@ def test_gradient_places():
     assert ds.shape == (0, 500) and (dw == 0).all()
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 8), (2, 64), (777, 1003), (1024, 2048), (2048, 1024),
+                                       (2048, 512), (512, 4096), (256, 8192), (2048, 2048),
+                                       (2000, 7)])
+@pytest.mark.parametrize("dd,sd,od", [(F32, F32, F32), (BF16, BF16, BF16), (BF16, F32, F32)])
+def test_gradient_in_place(rows, cols, dd, sd, od):
+    """ds in the place of dy or of s: dw, which reads every row of both, is the same."""
+    dy, s, r, w, d = _grads(rows, cols, dd, sd, di=F32)
+    ref, rdw = sffn.rms_norm_backward(dy, s, r, w, dstream=d, dtype=od)
+    for i in range(2):
+        if (dd, sd)[i] != od:
+            continue
+        for _ in range(3):
+            t = [dy.clone(), s.clone()]
+            got, dw = sffn.rms_norm_backward(t[0], t[1], r, w, dstream=d, out=t[i])
+            assert got is t[i] and torch.equal(got, ref) and torch.equal(dw, rdw)
+    # halves of the same rows: nothing in common but the span
+    wide = torch.empty(rows, 2 * cols, dtype=sd, device="cuda")
+    wide[:, :cols] = s
+    if sd == od:
+        got, dw = sffn.rms_norm_backward(dy, wide[:, :cols], r, w, dstream=d, out=wide[:, cols:])
+        assert torch.equal(got, ref) and torch.equal(dw, rdw) and torch.equal(wide[:, :cols], s)
+
+
 def test_empty():
     e = torch.empty(0, 500, device="cuda")
     y, s = sffn.rms_norm(e, residual=e, dtype=F32)

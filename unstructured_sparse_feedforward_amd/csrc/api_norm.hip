@@ -25,6 +25,13 @@ sffn_status sizes(int64_t rows, int64_t cols) {
   return rows > kMaxRows || cols > kNormMaxCols ? SFFN_E_UNSUPPORTED : SFFN_OK;
 }
 
+// Whether the memory that two matrices span has a byte in common.
+bool meet(const void* p, int64_t ldp, int pe, const void* q, int64_t ldq, int qe, int64_t rows,
+          int64_t cols) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return a < b + ((rows - 1) * ldq + cols) * qe && b < a + ((rows - 1) * ldp + cols) * pe;
+}
+
 size_t workspace(int64_t rows, int64_t cols) {
   return ((size_t)norm_grad_parts(rows, cols) * cols * 4 + kAlign - 1) / kAlign * kAlign;
 }
@@ -123,6 +130,10 @@ sffn_status sffn_rms_norm_backward(const sffn_norm_grad* n, int64_t rows, int64_
   a.ds_bf = n->ds_dtype == SFFN_BF16;
   a.parts = norm_grad_parts(rows, cols);
   a.slabs = a.parts == 0 && n->dweight ? norm_grad_slabs(cols) : 0;
+  a.in_place = rows > 0 && (meet(n->ds, n->ldds, elem(n->ds_dtype), n->dy, n->lddy,
+                                 elem(n->dy_dtype), rows, cols) ||
+                            meet(n->ds, n->ldds, elem(n->ds_dtype), n->s, n->lds,
+                                 elem(n->s_dtype), rows, cols));
   return done(launch_norm_grad(a, stream));
 }
 

@@ -388,7 +388,18 @@ hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
   if constexpr (L * V * CH <= 8192) {
     if (a.parts == 0) {
       const unsigned rows = (unsigned)((a.rows + Row<L>::ROWS - 1) / Row<L>::ROWS);
-      norm_grad_kernel<L, V, true><<<a.slabs + rows, Row<L>::NT, 0, s>>>(a);
+      if (a.slabs == 0 || !a.in_place) {
+        norm_grad_kernel<L, V, true><<<a.slabs + rows, Row<L>::NT, 0, s>>>(a);
+        return hipGetLastError();
+      }
+      // The slabs read every row of dy and s, which ds would overwrite under
+      // them: all of dw first, then the rows, in launches of their own.
+      norm_grad_kernel<L, V, true><<<a.slabs, Row<L>::NT, 0, s>>>(a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      NormGradArgs b = a;
+      b.slabs = 0;
+      norm_grad_kernel<L, V, true><<<rows, Row<L>::NT, 0, s>>>(b);
       return hipGetLastError();
     }
   }

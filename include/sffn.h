@@ -481,7 +481,7 @@ sffn_status sffn_mx8_dequantize(const uint8_t* codes, const uint8_t* scales, int
                                 hipStream_t stream);
 
 /* sffn_mx_matmul for a in MXFP8 (tokens) and b in MXFP4 (weights). Products
- * are exact, sums float32. Codes of a must not be NaN (0x7F, 0xFF). */
+ * are exact, sums float32. A NaN code of a (0x7F, 0xFF) makes its row NaN. */
 sffn_status sffn_mx8_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
                             const uint8_t* b_codes, const uint8_t* b_scales, int64_t N, int64_t K,
                             void* out, int32_t out_dtype, int64_t ldo, hipStream_t stream);
@@ -492,7 +492,8 @@ sffn_status sffn_mx8_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int
  *   s = x + residual (rounded to the residual's type),
  *   r = 1 / sqrt(mean(s^2) + eps),   y = s r w,
  * over rows of up to 16384 columns (SFFN_E_UNSUPPORTED above, and above 2^27
- * rows). Sums are float32 (a row's squares must not overflow); the same call
+ * rows). The result is formed in float32 where it is bf16, in 64 bits where it
+ * is float32 or MXFP8 (a row's squares must not overflow float32); the same call
  * repeats bit for bit, and a row's result does not depend on the other rows.
  * Every matrix is float32 or bf16 with contiguous rows, its own row stride
  * (>= cols elements) and no more than its elements' alignment.

@@ -1,6 +1,6 @@
-// MXFP4 matrices, shared by the quantiser (mx.hip), the products
-// (mx_gemm.hip, mx8_gemm.hip) and the expert layer (moe.hip), and the copies into LDS of
-// the last two.
+// MXFP4 matrices, shared by the quantiser (mx.hip), the products (mx_gemm.hip,
+// mx8_gemm.hip) and the expert layer (moe.hip), and the copies into LDS of the
+// products and the layer.
 //
 // A matrix [R, K] (blocks of 32 along K) is kept as
 //   codes  [R, Kp / 2] bytes, Kp = K rounded up to 128: element k of a row

@@ -37,8 +37,8 @@ __device__ __forceinline__ float sum_of(float a) {
   return v;
 }
 
-// Before the first sum_of after a matrix instruction: its result may be read
-// 18 wait states later at the earliest.
+// Before the first sum_of after a matrix instruction: its result may be read 20
+// wait states later (with an 8-bit operand, 16 passes) at the earliest; 24 here.
 template <int MI>
 __device__ __forceinline__ void settle_sums() {
   __builtin_amdgcn_sched_barrier(0);

@@ -491,8 +491,9 @@ sffn_status sffn_mx8_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int
  * root-mean-square norm of the sum,
  *   s = x + residual (rounded to the residual's type),
  *   r = 1 / sqrt(mean(s^2) + eps),   y = s r w,
- * over rows of up to 16384 columns (SFFN_E_UNSUPPORTED above, and above 2^27
- * rows). The result is formed in float32 where it is bf16, in 64 bits where it
+ * over rows of up to 16384 columns (SFFN_E_UNSUPPORTED above, and above 2^25
+ * rows of up to 512 columns, 2^31 / n of more, n an eighth of the columns rounded
+ * up to a power of two, at most 1024; the gradient's limit is 2^27 rows). The result is formed in float32 where it is bf16, in 64 bits where it
  * is float32 or MXFP8 (a row's squares must not overflow float32); the same call
  * repeats bit for bit, and a row's result does not depend on the other rows.
  * Every matrix is float32 or bf16 with contiguous rows, its own row stride
@@ -612,8 +613,8 @@ typedef struct sffn_route_desc {
 } sffn_route_desc;
 
 /* logits [T, E] of dtype with row stride ldl >= E, ids [T, k] int32, probs
- * [T, k] float32; T up to 2^27. n_tokens as in sffn_moe_forward. No handle,
- * no workspace, no state. */
+ * [T, k] float32; T up to 2^25 (SFFN_E_UNSUPPORTED above). n_tokens as in
+ * sffn_moe_forward. No handle, no workspace, no state. */
 sffn_status sffn_route(const sffn_route_desc* desc, const void* logits, int32_t dtype, int64_t T,
                        int64_t ldl, const float* bias, const int32_t* n_tokens, int32_t* ids,
                        float* probs, hipStream_t stream);

@@ -340,6 +340,14 @@ def test_aliases():
     assert got[1] is a and torch.equal(a, s) and torch.equal(got[0], y)
 
 
+def test_most_rows():
+    """2^25 rows of up to 512 columns, the most of a call."""
+    x = torch.ones(1 << 25, 8, dtype=BF16, device="cuda")
+    y = torch.full_like(x, 7)
+    sffn.rms_norm(x, eps=0.0, out=y)
+    assert (y == 1).all()
+
+
 def test_two_streams():
     """Calls that overlap on two streams: nothing is shared."""
     args = [_grads(n, c, BF16, F32, di=F32, seed=n) for n, c in ((3000, 1500), (300, 900))]

@@ -370,3 +370,24 @@ def test_graph():
         i2, p2 = r.forward(buf, b)
         assert torch.equal(ids, i2) and torch.equal(p, p2)
         assert torch.equal(d, r.backward(dp, buf, i2))
+
+
+def test_most_tokens():
+    """2^25 tokens, the most of a call: a window at each end and in the middle against
+    the same window alone, and nothing left out."""
+    T, E, k = 1 << 25, 8, 2
+    logits = torch.randn(T, E, generator=torch.Generator(device="cuda").manual_seed(1),
+                         device="cuda", dtype=torch.float32)
+    r = sffn.MoERouter(E, k)
+    out = (torch.full((T, k), -7, dtype=torch.int32, device="cuda"),
+           torch.full((T, k), float("nan"), device="cuda"))
+    ids, probs = r.forward(logits, out=out)
+    assert (ids >= 0).all() and not probs.isnan().any()
+    dl = r.backward(torch.ones_like(probs), logits, ids, out=torch.full_like(logits, float("nan")))
+    assert not dl.isnan().any()
+    for a in (0, T // 2 - 500, T - 1000):
+        i, p = r.forward(logits[a:a + 1000])
+        assert torch.equal(i, ids[a:a + 1000])
+        # (so few tokens take a kernel of other lanes, whose sums have another order: E + k
+        # roundings and an exponential's at each side)
+        assert torch.allclose(p, probs[a:a + 1000], rtol=2 * (E + k + 4) * 2.0 ** -24, atol=0)

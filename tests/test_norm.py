@@ -77,6 +77,11 @@ def test_refusals(kw):
 def test_limits_and_empty():
     assert _norm(dict(cols=16385, ldx=20000, ldr=20000, ldro=20000, ldo=20000)) == B.SFFN_E_UNSUPPORTED
     assert _norm(dict(rows=(1 << 27) + 1)) == B.SFFN_E_UNSUPPORTED
+    for cols, rows in ((64, 25), (512, 25), (513, 24), (2048, 23), (2049, 22), (4097, 21),
+                       (16384, 21)):
+        ld = dict(cols=cols, ldx=cols, ldr=cols, ldro=cols, ldo=cols)
+        assert _norm(dict(rows=(1 << rows) + 1, **ld)) == B.SFFN_E_UNSUPPORTED
+        assert _norm(dict(rows=1 << rows, x=None, **ld)) == B.SFFN_E_ARG
     assert _norm(dict(rows=0, x=None, out=None)) == B.SFFN_OK
     assert _norm(dict(cols=0, x=None, out=None)) == B.SFFN_OK
     lib = B.load_library()

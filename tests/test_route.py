@@ -84,8 +84,10 @@ def test_refusals():
                dict(n=P + 1), dict(dl=None), dict(dl=P + 2), dict(dl_dtype=2), dict(lddl=63)):
         assert lib.sffn_route_backward(ctypes.byref(D), *{**g, **kw}.values(), None) == B.SFFN_E_ARG
     assert lib.sffn_route(None, *f.values(), None) == B.SFFN_E_ARG
-    assert lib.sffn_route(ctypes.byref(D), *{**f, "T": (1 << 27) + 1}.values(),
-                          None) == B.SFFN_E_UNSUPPORTED
+    for T, st in (((1 << 25) + 1, B.SFFN_E_UNSUPPORTED), (1 << 25, B.SFFN_E_ARG)):
+        assert lib.sffn_route(ctypes.byref(D), *{**f, "T": T, "logits": None}.values(), None) == st
+        assert lib.sffn_route_backward(ctypes.byref(D), *{**g, "T": T, "dl": None}.values(),
+                                       None) == st
 
 
 def test_python_refusals():

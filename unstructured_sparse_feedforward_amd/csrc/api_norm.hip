@@ -45,6 +45,8 @@ sffn_status sffn_rms_norm(const sffn_norm* n, int64_t rows, int64_t cols, float 
   if (!n) return SFFN_E_ARG;
   const sffn_status st = sizes(rows, cols);
   if (st != SFFN_OK) return st;
+  // (a launch has fewer than 2^32 threads)
+  if (rows * norm_threads(cols) > (int64_t)1 << 31) return SFFN_E_UNSUPPORTED;
   if (!(eps >= 0.0f) || !std::isfinite(eps)) return SFFN_E_ARG;
   const bool mx8 = n->out_dtype == SFFN_MXFP8;
   if (!mx8 && !float_type(n->out_dtype)) return SFFN_E_ARG;

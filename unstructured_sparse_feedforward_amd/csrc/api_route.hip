@@ -9,7 +9,7 @@ namespace {
 
 using namespace sffn;
 
-constexpr int64_t kMaxTokens = (int64_t)1 << 27;
+constexpr int64_t kMaxTokens = (int64_t)1 << 25;    // 64 threads each, below 2^32 a launch
 
 bool aligned(const void* p, size_t a) { return p != nullptr && (uintptr_t)p % a == 0; }
 bool floats(const void* p, int32_t dt) {

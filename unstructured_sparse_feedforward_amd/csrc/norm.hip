@@ -415,13 +415,17 @@ hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
 // caches: 8192 x 2048 bf16 in, out and stream 27.4, by 64 threads of 32 columns
 // 30.5, by 512 of 4 34; 4096 x 4096 27.9, 256 of 16 29.7). A wave or more a
 // row: 64 threads of 16 columns for 777 x 1003 6.5, 128 of 8 5.9.
+int norm_threads(int64_t cols) {
+  return cols <= 512 ? 64 : cols <= 1024 ? 128 : cols <= 2048 ? 256 : cols <= 4096 ? 512 : 1024;
+}
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
-  if (a.cols <= 512) return norm<64, 1>(a, s);
-  if (a.cols <= 1024) return norm<128, 1>(a, s);
-  if (a.cols <= 2048) return norm<256, 1>(a, s);
-  if (a.cols <= 4096) return norm<512, 1>(a, s);
-  if (a.cols <= 8192) return norm<1024, 1>(a, s);
-  return norm<1024, 2>(a, s);
+  switch (norm_threads(a.cols)) {
+    case 64: return norm<64, 1>(a, s);
+    case 128: return norm<128, 1>(a, s);
+    case 256: return norm<256, 1>(a, s);
+    case 512: return norm<512, 1>(a, s);
+    default: return a.cols <= 8192 ? norm<1024, 1>(a, s) : norm<1024, 2>(a, s);
+  }
 }
 
 // Whether one launch forms ds and dw: up to 2^21 elements, whose second reading

@@ -50,6 +50,8 @@ struct NormGradArgs {
 // without
 int norm_grad_parts(int64_t rows, int64_t cols);
 int norm_grad_slabs(int64_t cols);
+// threads for a row of the norm
+int norm_threads(int64_t cols);
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s);
 
 }  // namespace sffn

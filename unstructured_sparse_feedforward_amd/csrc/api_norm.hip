@@ -78,6 +78,7 @@ sffn_status sffn_rms_norm(const sffn_norm* n, int64_t rows, int64_t cols, float 
   a.rows = rows;
   a.cols = (int)cols;
   a.eps = eps;
+  a.inv_cols = 1.0 / (double)cols;
   a.x_bf = n->x_dtype == SFFN_BF16;
   a.r_bf = n->residual && n->residual_dtype == SFFN_BF16;
   a.w_bf = n->weight && n->weight_dtype == SFFN_BF16;

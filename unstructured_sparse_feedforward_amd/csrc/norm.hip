@@ -152,9 +152,11 @@ __device__ __forceinline__ void store_mx8(const NormArgs& a, int64_t row, int l,
 // WIDE (results in float32 and MXFP8): the sum and the products in 64 bits, y
 // rounded once, so that a result in 8 bits is that of the formula but where y
 // lies within half a step of float32 of a border, and not four of them. It costs
-// most for MXFP8 from bf16 (8192 x 2048 32.2 us, in 32 bits 28.4; without a
-// residual 24.0, 19.2; from float32 45.8, 45.1). A bf16 result's own rounding is
-// 2^15 times what that would gain.
+// most for MXFP8 from bf16, which is bound by its instructions (8192 x 2048 29.9
+// us, in 32 bits 28.0; without a residual 20.9, 18.4; from float32 45.5, 45.5).
+// r by quotients and a root in 64 bits, in place of 1 / cols from the host and
+// rsqrt, took 33.2 and 23.7 us (31.1 and 21.7 otherwise the same). A bf16
+// result's own rounding is 2^15 times what 64 bits would gain.
 template <int L, int V, bool WIDE>
 __global__ __launch_bounds__(Row<L>::NT) void norm_kernel(NormArgs a) {
   typedef std::conditional_t<WIDE, double, float> T;
@@ -184,17 +186,24 @@ __global__ __launch_bounds__(Row<L>::NT) void norm_kernel(NormArgs a) {
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < CH; ++j) q = fma((T)s[i][j], (T)s[i][j], q);
-  const T r = (T)1 / sqrt(row_sum<L>(q, share) / (T)a.cols + (T)a.eps);
+  T r = row_sum<L>(q, share);
+  if constexpr (WIDE) r = rsqrt(fma(r, a.inv_cols, (double)a.eps));
+  else r = 1.0f / sqrtf(r / (float)a.cols + a.eps);
   if (a.rstd && l == 0) a.rstd[row] = (float)r;
   if (a.weight) values(pw, a.w_bf, t);
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i) {
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
+    for (int j = 0; j < CH; ++j)
       s[i][j] = (float)(a.weight ? (T)s[i][j] * r * (T)t[i][j] : (T)s[i][j] * r);
-      // (columns past the last are 0 there: s is 0, and r may be infinite)
-      if ((i * L + l) * CH + j >= a.cols) s[i][j] = 0.0f;
+    // columns past the last are 0 in MXFP8: s is 0, but r may be infinite
+    const int left = a.cols - (i * L + l) * CH;
+    if (WIDE && left < CH) {
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+        if (j >= left) s[i][j] = 0.0f;
     }
+  }
   if (WIDE && a.out_kind == kMx8) store_mx8<L, V>(a, row, l, s);
   else store_row<L, V>(a.out, row * a.ldo, !WIDE, a.cols, l, s);
 }

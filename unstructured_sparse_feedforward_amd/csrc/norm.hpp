@@ -24,6 +24,7 @@ struct NormArgs {
   int64_t rows;
   int cols;
   float eps;
+  double inv_cols;          // 1 / cols
   int x_bf, r_bf, w_bf;     // bf16, else float32
   int out_kind;
 };

@@ -12,7 +12,7 @@ some 6 roundings: y is off by at most (D / 2 + 7) u of itself, taken here as
 ds = r (g - xh c): with E = 50 the mean c is off by E u mean |g xh|, xh and g by
 2 u of themselves; every further operation by half a step of its result. So
   |err| <= u (r (6 |g| + 6 |xh c| + E |xh| mean |g xh|) + 2 |ds|).
-dw sums rows of dy xh, by columns: up to 512, ceil(T / 3072) rows a lane, then 3
+dw sums rows of dy xh, by columns: up to 512, ceil(T / (4 x 768)) rows a lane, then 3
 additions over a workgroup's waves, 48 of workgroups and 15 of their sums; up to
 2048, ceil(T / 512) rows (or a quarter), 3 + 32 + 15; above, ceil(T / 256) and 16 +
 15; in one launch (T <= 2048) fewer. With fewer rows there are fewer workgroups, each

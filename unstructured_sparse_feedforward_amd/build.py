@@ -27,6 +27,8 @@ ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
          # keep the compiler from forming packed fp32 VALU ops
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+         # a launch's status that nothing looks at
+         "-Werror=unused-value",
          "-I", INCLUDE, "-I", CSRC]
 
 

@@ -614,14 +614,14 @@ __global__ __launch_bounds__(kWaves * 64) void route_grad_kernel(RouteArgs a) {
   else store_run<N>((float*)a.dl + t * a.lddl + e0, a.E - e0, d);
 }
 
+// f launches, and returns that launch's status
 template <typename F>
 hipError_t by_experts(int E, F&& f) {
-  if (E <= 64) f(std::integral_constant<int, 1>{});
-  else if (E <= 128) f(std::integral_constant<int, 2>{});
-  else if (E <= 256) f(std::integral_constant<int, 4>{});
-  else if (E <= 512) f(std::integral_constant<int, 8>{});
-  else f(std::integral_constant<int, 16>{});
-  return hipGetLastError();
+  if (E <= 64) return f(std::integral_constant<int, 1>{});
+  if (E <= 128) return f(std::integral_constant<int, 2>{});
+  if (E <= 256) return f(std::integral_constant<int, 4>{});
+  if (E <= 512) return f(std::integral_constant<int, 8>{});
+  return f(std::integral_constant<int, 16>{});
 }
 
 }  // namespace
@@ -651,12 +651,13 @@ hipError_t launch_route(const RouteArgs& in, hipStream_t s) {
     return go(std::integral_constant<int, 4>{}, std::integral_constant<int, 16>{});
   if (a.E <= 128 && a.k < 32 && a.groups <= 32 && a.T >= 8192)
     return go(std::integral_constant<int, 4>{}, std::integral_constant<int, 32>{});
-  return by_experts(a.E, [&](auto n) { go(n, std::integral_constant<int, 64>{}); });
+  return by_experts(a.E, [&](auto n) { return go(n, std::integral_constant<int, 64>{}); });
 }
 hipError_t launch_route_grad(const RouteArgs& a, hipStream_t s) {
   const unsigned grid = (unsigned)((a.T + kWaves - 1) / kWaves);
   return by_experts(a.E, [&](auto n) {
     route_grad_kernel<decltype(n)::value><<<grid, kWaves * 64, 0, s>>>(a);
+    return hipGetLastError();
   });
 }
 

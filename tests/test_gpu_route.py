@@ -9,6 +9,8 @@ Gradients, with u = 2^-24: exponentials, quotients and products are off by at
 most 8 u of themselves, sums over n terms by (7 + n / 64) u of the terms'
 magnitudes; a difference g - t of such values and the product with q <= 1 then
 by at most 16 (|g| + sum |g| q) q u, E <= 1024 in the sums: taken as 40 u."""
+import decimal
+
 import numpy as np
 import pytest
 import torch
@@ -391,3 +393,62 @@ def test_most_tokens():
         # (so few tokens take a kernel of other lanes, whose sums have another order: E + k
         # roundings and an exponential's at each side)
         assert torch.allclose(p, probs[a:a + 1000], rtol=2 * (E + k + 4) * 2.0 ** -24, atol=0)
+
+
+def _sigmoid_gradient(dp, l, ids, scale):
+    """(the gradient of normalised sigmoid weights, its bound) of one token, from
+    the definition with 60 digits. Bound: q = s / S is the 64-bit one rounded, the
+    scores' gradient and sums as in the head of this file, 40 u q (1 - s) (|g| +
+    sum |g| q); a q below float32's smallest normal is off by 2^-150 itself."""
+    D = decimal.Decimal
+    with decimal.localcontext() as c:
+        c.prec = 60
+        s = [1 / (1 + (-D(float(v))).exp()) for v in l]
+        g = [D(float(v)) * D(scale) for v in dp]
+        S = sum(s[e] for e in ids)
+        t = sum(gr * s[e] for gr, e in zip(g, ids)) / S
+        ta = sum(abs(gr) * s[e] for gr, e in zip(g, ids)) / S
+        d, b = np.zeros(len(l)), np.zeros(len(l))
+        for gr, e in zip(g, ids):
+            d[e] = float((gr - t) / S * s[e] * (1 - s[e]))
+            b[e] = float((abs(gr) + ta) * (D(40 * U) * s[e] / S * (1 - s[e]) + D(2) ** -148))
+    return d, b
+
+
+@pytest.mark.parametrize("top", [-30.0, -80.0, -86.0, -87.2, -88.0, -88.5, -90.0, -100.0, -103.5, -300.0,
+                                 -700.0])
+@pytest.mark.parametrize("by", [1.0, 65536.0])
+def test_backward_of_far_logits(top, by):
+    """Normalised sigmoid weights of experts whose scores float32 cannot hold, as
+    the forward pass forms them; beside ordinary ones; loss scaling."""
+    E, k, scale = 40, 4, 2.5
+    l = _rand((6, E), 3, scale=0.5) + top
+    l[4, 7:9] = torch.tensor([0.5, -1.0])          # ordinary ones, and others with them
+    l[5, 3] = 90.0
+    r, _ = _router((E, k, 1, 1, 1), "sigmoid", True, scale)
+    ids, p = r.forward(l)
+    assert (torch.abs(p.sum(1) - scale) < 1e-5).all()
+    dp = by * _rand((6, k), 4)
+    d = _np(r.backward(dp, l, ids))
+    for t in range(6):
+        ref, bound = _sigmoid_gradient(_np(dp)[t], _np(l)[t], ids[t].tolist(), scale)
+        assert (np.abs(d[t] - ref) <= bound).all(), (t, d[t][ids[t].tolist()], ref[ids[t].tolist()])
+    # weights that are not normalised: s (1 - s) g, as far as float32 holds it
+    r, _ = _router((E, k, 1, 1, 1), "sigmoid", False, scale)
+    d = _np(r.backward(dp, l, ids))
+    for t in range(6):
+        for g, e in zip(_np(dp)[t], ids[t].tolist()):
+            v = _np(l)[t, e]
+            ref = scale * g * np.exp(-abs(v)) / (1 + np.exp(-abs(v))) ** 2
+            assert abs(d[t, e] - ref) <= 40 * U * abs(ref) + 2.0 ** -149
+
+
+def test_backward_where_every_score_is_0():
+    """Logits whose scores are 0 in 64 bits too: the weights are, and their gradient."""
+    r, _ = _router((8, 2, 1, 1, 1), "sigmoid", True)
+    l = torch.tensor([[-709.78], [-709.79], [-800.0], [-float("inf")]], device="cuda").repeat(1, 8)
+    ids, p = r.forward(l)
+    d = r.backward(torch.tensor([[1.0, -2.0]] * 4, device="cuda"), l, ids)
+    assert (p[0] == 0.5).all() and (p[1:] == 0).all()
+    # q = 1/2 each, g - sum g q = 1.5 and -1.5
+    assert d[0, :2].tolist() == [0.75, -0.75] and (d[0, 2:] == 0).all() and (d[1:] == 0).all()

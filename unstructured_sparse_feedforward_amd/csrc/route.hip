@@ -547,7 +547,8 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs a) {
 //   sum of the chosen s, else ds_r = g_r; 0 for the others
 //   softmax: dl = s (ds - sum ds s), sigmoid: dl = ds s (1 - s).
 // Normalised softmax weights are the softmax q over the chosen experts alone:
-// dl_r = q_r (g_r - sum g q), nothing for the others.
+// dl_r = q_r (g_r - sum g q), nothing for the others; sigmoid ones, with q_r = s_r
+// / S, have dl_r = q_r (1 - s_r) (g_r - sum g q).
 template <int N>
 __global__ __launch_bounds__(kWaves * 64) void route_grad_kernel(RouteArgs a) {
   const int lane = threadIdx.x & 63, wave = wave_id(), e0 = lane * N;
@@ -583,15 +584,23 @@ __global__ __launch_bounds__(kWaves * 64) void route_grad_kernel(RouteArgs a) {
     total = wave_sum(g * s);     // sum ds s
     dr = g;
   } else if (a.sigmoid) {
-    const float s = id >= 0 ? 1.0f / (1.0f + expf(-lr)) : 0.0f;
-    const float c = id >= 0 ? 1.0f / (1.0f + expf(lr)) : 0.0f;    // 1 - s
-    dr = g;
+    // s and 1 - s are z = 1 / (1 + e) and e z with e = exp(-|l|), in one order or
+    // the other; e by its root, which float32 holds down to |l| = 174. (The
+    // hardware's reciprocal is within a step, of values from 1/2 to 32.)
+    const float root = expf(-0.5f * fabsf(lr)), e = root * root;
+    const float z = __builtin_amdgcn_rcpf(1.0f + e);
     if (a.normalize) {
-      const float S = wave_sum(s);
-      const float inv = S == 0.0f ? 0.0f : 1.0f / S;
-      dr = (g - wave_sum(g * s) * inv) * inv;
+      // q relative to the largest score: of logits far below -87 float32 has
+      // neither s nor 1 / S (of logits below -709.78 the forward pass' 64 bits have
+      // none either, and its weights are 0)
+      const float m = wave_max(lr), h = fminf(m, 0.0f);
+      float q = id >= 0 && m > -709.7827f ? (lr > 0.0f ? z : expf(lr - h) * z) : 0.0f;
+      const float S = wave_sum(q);
+      q *= S == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(S);
+      dr = q * (lr > 0.0f ? e * z : z) * (g - wave_sum(g * q));
+    } else {
+      dr = root * g * (root * (z * z));
     }
-    dr *= s * c;
   } else {
     const float m = wave_max(lr);
     const float ex = id >= 0 && m == m && m != -INFINITY ? expf(lr - m) : 0.0f;

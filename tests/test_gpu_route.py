@@ -452,3 +452,34 @@ def test_backward_where_every_score_is_0():
     assert (p[0] == 0.5).all() and (p[1:] == 0).all()
     # q = 1/2 each, g - sum g q = 1.5 and -1.5
     assert d[0, :2].tolist() == [0.75, -0.75] and (d[0, 2:] == 0).all() and (d[1:] == 0).all()
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("c,T", [((64, 6, 1, 1, 1), 5000), ((64, 6, 8, 3, 2), 5000), ((60, 15, 4, 2, 1), 5003),
+                                 ((128, 8, 1, 1, 1), 9000), ((128, 9, 16, 5, 2), 9001),
+                                 ((256, 8, 8, 4, 2), 700), ((1000, 20, 1, 1, 1), 90)])
+def test_many_near_ties(c, T, scores):
+    """Scores plus bias that 32 bits cannot tell apart, of all experts of every
+    other token: tokens of one wave need 64 bits one after the other."""
+    E = c[0]
+    g = torch.Generator().manual_seed(E + T)
+    u, noise = torch.rand(E, generator=g).double(), torch.rand(T, E, generator=g).double()
+    if scores == "sigmoid":
+        bias = (0.5 * u).float()
+        s = 0.9 - bias.double() + 1e-7 * noise
+        l = torch.log(s / (1 - s)).float()
+    else:
+        bias = (0.5 / E * u).float()
+        s = (1 + bias.double().sum()) / E - bias.double() + 1e-9 * noise
+        l = torch.log(s).float()
+    l[1::4] = torch.randn(l[1::4].shape, generator=g)
+    l[3::4] = torch.randn(l[3::4].shape, generator=g)
+    l, bias = l.cuda(), bias.cuda()
+    near = (torch.softmax(l[:1].double(), 1) if scores == "softmax" else torch.sigmoid(l[:1].double())) + bias
+    assert len(set(near[0].tolist())) == E and near.max() - near.min() < 2.0 ** -20
+    r, _ = _router(c, scores, True)
+    for b in (bias, None):
+        ids, p = r.forward(l, b)
+        oi, op = _plain(l, c, scores, b, True)
+        assert torch.equal(ids.long(), oi)
+        assert ((p.double() - op).abs() <= 1.01 * U * op).all()

@@ -176,16 +176,36 @@ __device__ __forceinline__ float row_max(const float (&l)[N]) {
   return m != m ? -INFINITY : m;     // (every one a NaN)
 }
 
+// A wave's own part of LDS holds 32-bit scores, then 64-bit ones, then their
+// keys, for one token after the other: bytes, accessed as one type or another.
+template <typename T>
+__device__ __forceinline__ T lds_get(const char* p, int i) {
+  T v;
+  __builtin_memcpy(&v, __builtin_assume_aligned(p + i * sizeof(T), sizeof(T)), sizeof(T));
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void lds_put(char* p, int i, T v) {
+  __builtin_memcpy(__builtin_assume_aligned(p + i * sizeof(T), sizeof(T)), &v, sizeof(T));
+}
+// Between a lane's accesses there and those of others: the hardware has a wave's
+// in their order, and the compiler is to keep it.
+__device__ __forceinline__ void lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The two largest of a group's c, in all of its lanes: P = 2^lp lanes have a
 // group, and share out its members in LDS. (NaNs are ignored.)
 template <typename T>
-__device__ __forceinline__ void group_best(const RouteArgs& a, const T* cs, int pos, int lp, T& b1,
-                                           T& b2) {
+__device__ __forceinline__ void group_best(const RouteArgs& a, const char* cs, int pos, int lp,
+                                           T& b1, T& b2) {
   const int g = pos >> lp, p = pos & ((1 << lp) - 1);
   b1 = b2 = -INFINITY;
   if (g < a.groups) {
     for (int j = p; j < a.per; j += 1 << lp) {
-      const T c = cs[g * a.per + j];
+      const T c = lds_get<T>(cs, g * a.per + j);
       b2 = fmax(b2, fmin(b1, c));
       b1 = fmax(b1, c);
     }
@@ -213,7 +233,7 @@ __device__ __forceinline__ bool kept(const RouteArgs& a, uint64_t keep, int seg,
 // c of the token's experts, lane, 64 + lane, .. of each lane of the wave, into
 // cs; of groups, 2^lp lanes each, the lanes of those that are kept.
 template <bool BIAS, bool GROUPED>
-__device__ __forceinline__ uint64_t scores64(const RouteArgs& a, int64_t t, float m, double* cs,
+__device__ __forceinline__ uint64_t scores64(const RouteArgs& a, int64_t t, float m, char* cs,
                                              int lp) {
   const int lane = threadIdx.x & 63;
   double sum = 1.0;
@@ -227,6 +247,7 @@ __device__ __forceinline__ uint64_t scores64(const RouteArgs& a, int64_t t, floa
     sum = wave_sum(sum);
   }
   uint64_t nan = 0;      // the groups of the lane's NaNs
+  lds_order();
 #pragma unroll 1
   for (int e = lane; e < a.E; e += 64) {
     const double l = logit(a, t, e);
@@ -235,10 +256,10 @@ __device__ __forceinline__ uint64_t scores64(const RouteArgs& a, int64_t t, floa
     double c = a.sigmoid ? 1.0 / (1.0 + x) : sum == 0.0 ? 0.0 : x / sum;
     if (BIAS) c += (double)a.bias[e];
     if (c != c) nan |= 1ull << group_of(a, e);
-    cs[e] = c;
+    lds_put(cs, e, c);
   }
   if (!GROUPED) return ~0ull;
-  __builtin_amdgcn_wave_barrier();     // (a wave's own part of LDS)
+  lds_order();
   double b1, b2;
   group_best<double>(a, cs, lane, lp, b1, b2);
   const int mine = lane >> lp;
@@ -257,31 +278,33 @@ __device__ __forceinline__ uint64_t scores64(const RouteArgs& a, int64_t t, floa
 
 // The token's experts: lane r returns that of rank r.
 template <bool BIAS, bool GROUPED>
-__device__ __forceinline__ int choose64(const RouteArgs& a, int64_t t, float m, double* cs,
-                                        int lp) {
+__device__ __forceinline__ int choose64(const RouteArgs& a, int64_t t, float m, char* cs, int lp) {
   const int lane = threadIdx.x & 63;
   const uint64_t keep = scores64<BIAS, GROUPED>(a, t, m, cs, lp);
-  long long* key = (long long*)cs;
+  lds_order();
 #pragma unroll 1
-  for (int e = lane; e < a.E; e += 64)
-    key[e] = !GROUPED || kept(a, keep, 0, lp, e)
-                 ? order_key(BIAS ? cs[e] : (double)logit(a, t, e)) : kNone64;
+  for (int e = lane; e < a.E; e += 64) {
+    const double c = BIAS ? lds_get<double>(cs, e) : (double)logit(a, t, e);
+    lds_put(cs, e, !GROUPED || kept(a, keep, 0, lp, e) ? order_key(c) : kNone64);
+  }
   int id = 0;
 #pragma unroll 1
   for (int r = 0; r < a.k; ++r) {
     long long bk = kNone64;
     int be = lane;
 #pragma unroll 1
-    for (int e = lane; e < a.E; e += 64)
-      if (key[e] > bk) {
-        bk = key[e];
+    for (int e = lane; e < a.E; e += 64) {
+      const long long key = lds_get<long long>(cs, e);
+      if (key > bk) {
+        bk = key;
         be = e;
       }
+    }
     // the largest upper halves, of these the lower halves, of these the expert
     const int hi = (int)(bk >> 32), top = wave_max(hi);
     const int lo = hi == top ? (int)((uint32_t)bk ^ 0x80000000u) : kNone, low = wave_max(lo);
     be = -wave_max(hi == top && lo == low ? -be : kNone);
-    if (lane == (be & 63)) key[be] = kNone64;
+    if (lane == (be & 63)) lds_put(cs, be, kNone64);
     if (lane == r) id = be;
   }
   return id;
@@ -301,11 +324,11 @@ __device__ __forceinline__ int choose64(const RouteArgs& a, int64_t t, float m, 
 // logits themselves, which are exact.
 template <int N, int LPT, bool BIAS, bool GROUPED>
 __device__ __forceinline__ int choose32(const RouteArgs& a, int64_t t, const float (&l)[N],
-                                        float m, double* cs64, int* ids, bool* sure) {
+                                        float m, char* cs64, int* ids, bool* sure) {
   constexpr float kLog2e = 1.44269504f;
   const int lane = threadIdx.x & 63, seg = seg_of<LPT>(lane), pos = pos_of<LPT>(lane);
   const int e0 = pos * N;
-  float* cs = (float*)cs64 + seg * N;
+  char* cs = cs64 + seg * N * sizeof(float);
   int key[N];
   bool clear = true;
   float room = 0.0f;
@@ -343,10 +366,10 @@ __device__ __forceinline__ int choose32(const RouteArgs& a, int64_t t, const flo
       bool nan = false;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        cs[e0 + i] = c[i];
+        lds_put(cs, e0 + i, c[i]);
         nan |= c[i] != c[i];
       }
-      __builtin_amdgcn_wave_barrier();     // (a wave's own part of LDS)
+      lds_order();
       const int lp = a.lp[LPT == 64 ? 0 : LPT == 32 ? 1 : 2];
       float b1, b2;
       group_best<float>(a, cs, pos, lp, b1, b2);
@@ -459,7 +482,7 @@ __device__ __forceinline__ int choose32(const RouteArgs& a, int64_t t, const flo
     }
   }
   if constexpr (LPT < 64) {
-    __builtin_amdgcn_wave_barrier();
+    lds_order();
     id = ids[lane];
   }
   if (BIAS) {
@@ -488,7 +511,7 @@ __device__ __forceinline__ int choose32(const RouteArgs& a, int64_t t, const flo
 template <int N, int LPT, bool BIAS, bool GROUPED>
 __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs a) {
   constexpr int TOKENS = 64 / LPT;
-  __shared__ double cs[kWaves][BIAS || GROUPED ? N * 64 : 1];
+  __shared__ __align__(16) char cs[kWaves][BIAS || GROUPED ? N * 64 * sizeof(double) : 16];
   __shared__ int ids[kWaves][LPT < 64 ? 64 : 1];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int seg = seg_of<LPT>(lane), pos = pos_of<LPT>(lane), e0 = pos * N;

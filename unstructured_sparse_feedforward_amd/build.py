@@ -27,8 +27,9 @@ ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
          # keep the compiler from forming packed fp32 VALU ops
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-         # a launch's status that nothing looks at
-         "-Werror=unused-value",
+         # a launch's status that nothing looks at, an address said to have more
+         # alignment than it has
+         "-Werror=unused-value", "-Werror=align-mismatch",
          "-I", INCLUDE, "-I", CSRC]
 
 

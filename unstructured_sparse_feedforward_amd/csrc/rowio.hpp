@@ -29,7 +29,8 @@ __device__ __forceinline__ void load8(const float* p, float* v) {
   for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
 }
 __device__ __forceinline__ void load8(const uint16_t* p, float* v) {
-  Vec<uint16_t, 8>::cvt(*(const u32x4u_t*)p, v);
+  const u32x4_t a = *(const u32x4u_t*)p;     // (a reference would claim its own alignment)
+  Vec<uint16_t, 8>::cvt(a, v);
 }
 __device__ __forceinline__ void store8(float* p, const float* v) {
   *(f32x4u_t*)p = f32x4_t{v[0], v[1], v[2], v[3]};
@@ -49,7 +50,8 @@ __device__ __forceinline__ void load4(const float* p, float* v) {
   for (int i = 0; i < 4; ++i) v[i] = a[i];
 }
 __device__ __forceinline__ void load4(const uint16_t* p, float* v) {
-  Vec<uint16_t, 4>::cvt(*(const u32x2u_t*)p, v);
+  const u32x2_t a = *(const u32x2u_t*)p;
+  Vec<uint16_t, 4>::cvt(a, v);
 }
 __device__ __forceinline__ void store4(float* p, const float* v) {
   *(f32x4u_t*)p = f32x4_t{v[0], v[1], v[2], v[3]};

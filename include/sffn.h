@@ -501,9 +501,10 @@ sffn_status sffn_mx8_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int
  *   x             [rows, cols]
  *   residual      nullable: then s = x
  *   residual_out  [rows, cols] of residual_dtype: s (NULL iff residual is).
- *                 May be residual itself, or x where the types agree; apart
- *                 from that, and from out = x, no result may overlap an
- *                 operand.
+ *                 May be residual itself, or x; out may be x. In the place
+ *                 of an operand a result has its type and, of more than one
+ *                 row, its row stride; otherwise they have no byte in common
+ *                 (SFFN_E_ARG), nor have the results.
  *   weight        w [cols], nullable: 1
  *   out           y: float32, bf16 (rounded once), or MXFP8 codes (16-byte
  *                 aligned; SFFN_MXFP8, ldo is not used) of the [rows, cols]
@@ -547,7 +548,9 @@ sffn_status sffn_rms_norm(const sffn_norm* norm, int64_t rows, int64_t cols, flo
  *   dstream  nullable: the gradient that reaches s beside the norm's
  *   weight   nullable: 1
  *   rstd     [rows] float32 of the forward pass
- *   ds       [rows, cols], may be dy, s or dstream where the types agree
+ *   ds       [rows, cols], may be dy, s or dstream, then of the same type and,
+ *            of more than one row, row stride; has no byte in common with any
+ *            otherwise (SFFN_E_ARG)
  *   dweight  [cols] float32, nullable (NULL without a weight); written by
  *            rows == 0 too (zeros)
  * Sums are float32, of rows in an order that depends on the sizes alone.

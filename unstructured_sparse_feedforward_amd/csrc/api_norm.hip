@@ -3,6 +3,8 @@
 #include <cmath>
 
 #include "norm.hpp"
+#include "mx.hpp"
+#include "place.hpp"
 #include "sffn.h"
 
 namespace {
@@ -25,11 +27,10 @@ sffn_status sizes(int64_t rows, int64_t cols) {
   return rows > kMaxRows || cols > kNormMaxCols ? SFFN_E_UNSUPPORTED : SFFN_OK;
 }
 
-// Whether the memory that two matrices span has a byte in common.
-bool meet(const void* p, int64_t ldp, int pe, const void* q, int64_t ldq, int qe, int64_t rows,
-          int64_t cols) {
-  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  return a < b + ((rows - 1) * ldq + cols) * qe && b < a + ((rows - 1) * ldp + cols) * pe;
+// of a matrix of a float type; of none (p is null), no bytes
+Place place(const void* p, int32_t dt, int64_t ld, int64_t rows, int64_t cols) {
+  const int e = (int)elem(dt);
+  return {p, p ? rows : 0, ld * e, cols * e, e};
 }
 
 size_t workspace(int64_t rows, int64_t cols) {
@@ -62,6 +63,17 @@ sffn_status sffn_rms_norm(const sffn_norm* n, int64_t rows, int64_t cols, float 
           : !aligned(n->out, elem(n->out_dtype)) || n->out_scales != nullptr || n->ldo < cols)
     return SFFN_E_ARG;
   if ((n->rstd && !aligned(n->rstd, 4)) || (n_rows && !aligned(n_rows, 4))) return SFFN_E_ARG;
+  // in the place of an operand, or apart from it
+  const Place x = place(n->x, n->x_dtype, n->ldx, rows, cols);
+  const Place r = place(n->residual, n->residual_dtype, n->ldr, rows, cols);
+  const Place ro = place(n->residual_out, n->residual_dtype, n->ldro, rows, cols);
+  const int64_t Kp = mx_padded(cols);
+  const Place y = mx8 ? Place{n->out, rows, Kp, Kp, 1}
+                      : place(n->out, n->out_dtype, n->ldo, rows, cols);
+  if (meeting(y, x) == kMixed) return SFFN_E_ARG;
+  if (n->residual && (meeting(ro, x) == kMixed || meeting(ro, r) == kMixed ||
+                      meeting(y, r) == kMixed || meeting(y, ro) != kApart))
+    return SFFN_E_ARG;
   NormArgs a = {};
   a.x = n->x;
   a.res = n->residual;
@@ -111,6 +123,13 @@ sffn_status sffn_rms_norm_backward(const sffn_norm_grad* n, int64_t rows, int64_
     const size_t need = n->dweight ? workspace(rows, cols) : 0;
     if (need > 0 && (!aligned(ws, kAlign) || ws_bytes < need)) return SFFN_E_ARG;
   }
+  // ds in the place of an operand, or apart from it
+  const Place ds = place(n->ds, n->ds_dtype, n->ldds, rows, cols);
+  const Meeting dy_ds = meeting(ds, place(n->dy, n->dy_dtype, n->lddy, rows, cols));
+  const Meeting s_ds = meeting(ds, place(n->s, n->s_dtype, n->lds, rows, cols));
+  if (dy_ds == kMixed || s_ds == kMixed ||
+      meeting(ds, place(n->dstream, n->dstream_dtype, n->lddstream, rows, cols)) == kMixed)
+    return SFFN_E_ARG;
   NormGradArgs a = {};
   a.dy = n->dy;
   a.s = n->s;
@@ -133,10 +152,7 @@ sffn_status sffn_rms_norm_backward(const sffn_norm_grad* n, int64_t rows, int64_
   a.ds_bf = n->ds_dtype == SFFN_BF16;
   a.parts = norm_grad_parts(rows, cols);
   a.slabs = a.parts == 0 && n->dweight ? norm_grad_slabs(cols) : 0;
-  a.in_place = rows > 0 && (meet(n->ds, n->ldds, elem(n->ds_dtype), n->dy, n->lddy,
-                                 elem(n->dy_dtype), rows, cols) ||
-                            meet(n->ds, n->ldds, elem(n->ds_dtype), n->s, n->lds,
-                                 elem(n->s_dtype), rows, cols));
+  a.in_place = dy_ds == kSame || s_ds == kSame;
   return done(launch_norm_grad(a, stream));
 }
 

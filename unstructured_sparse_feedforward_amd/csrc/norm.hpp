@@ -45,7 +45,7 @@ struct NormGradArgs {
   int dy_bf, s_bf, di_bf, w_bf, ds_bf;
   int parts;                // rows of the workspace
   int slabs;                // of columns, where dw needs no workspace (else 0)
-  int in_place;             // ds shares memory with dy or s
+  int in_place;             // ds is in the place of dy or s
 };
 // rows of the workspace, and workgroups of the first kernel; 0: one launch does
 // without

@@ -623,8 +623,9 @@ sffn_status sffn_route(const sffn_route_desc* desc, const void* logits, int32_t 
                        float* probs, hipStream_t stream);
 
 /* The gradient of the logits [T, E] (dl_dtype, row stride lddl >= E, every
- * element written) from that of the weights, dprobs [T, k] float32; the choice
- * itself, and with it the bias, has none. logits and ids are the forward
+ * element written; it may be logits itself, of the same type and row stride, and
+ * shares no byte with it otherwise: SFFN_E_ARG) from that of the weights, dprobs
+ * [T, k] float32; the choice itself, and with it the bias, has none. logits and ids are the forward
  * pass's; an index outside 0 .. E - 1 counts as an expert that was not
  * chosen. */
 sffn_status sffn_route_backward(const sffn_route_desc* desc, const float* dprobs,

@@ -483,3 +483,14 @@ def test_many_near_ties(c, T, scores):
         oi, op = _plain(l, c, scores, b, True)
         assert torch.equal(ids.long(), oi)
         assert ((p.double() - op).abs() <= 1.01 * U * op).all()
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_backward_in_place(scores, normalize):
+    for (E, k), dt in (((64, 6), F32), ((300, 8), BF16), ((1000, 20), F32)):
+        r, _ = _router((E, k, 1, 1, 1), scores, normalize)
+        l, dp = _rand((700, E + 5), 1, dt)[:, 2:2 + E], _rand((700, k), 2)
+        ids, _ = r.forward(l)
+        d = r.backward(dp, l, ids, dtype=dt)
+        assert r.backward(dp, l, ids, out=l) is l and torch.equal(d, l)

@@ -82,7 +82,13 @@ for n in range(20000):
     bad = any(p is not None and ds.meets(p) == 2 for p in (dy, s, di))
     check("norm grad", lib.sffn_rms_norm_backward(R(a), rows, cols, P << 14, 1 << 20, None), bad, dy, s,
           di, ds)
-for what in ("norm", "norm grad"):
+
+    l = near(rows, cols, [])
+    dl = near(rows, cols, [l])
+    D = B.SffnRouteDesc(cols, 1, 1, 1, 1, 0, 1, 1.0)
+    check("route grad", lib.sffn_route_backward(R(D), P << 11, l.at, l.dtype, rows, l.ld, P << 12, None,
+                                                dl.at, dl.dtype, dl.ld, None), dl.meets(l) == 2, l, dl)
+for what in ("norm", "norm grad", "route grad"):
     for bad in (False, True):
         assert seen[what, bad] > 1000, seen
 """

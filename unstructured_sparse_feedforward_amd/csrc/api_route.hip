@@ -2,6 +2,7 @@
 // launches. See include/sffn.h for the contract.
 #include <cmath>
 
+#include "place.hpp"
 #include "route.hpp"
 #include "sffn.h"
 
@@ -12,8 +13,9 @@ using namespace sffn;
 constexpr int64_t kMaxTokens = (int64_t)1 << 25;    // 64 threads each, below 2^32 a launch
 
 bool aligned(const void* p, size_t a) { return p != nullptr && (uintptr_t)p % a == 0; }
+int elem(int32_t dt) { return dt == SFFN_BF16 ? 2 : 4; }
 bool floats(const void* p, int32_t dt) {
-  return (dt == SFFN_F32 || dt == SFFN_BF16) && aligned(p, dt == SFFN_BF16 ? 2 : 4);
+  return (dt == SFFN_F32 || dt == SFFN_BF16) && aligned(p, elem(dt));
 }
 
 sffn_status validate(const sffn_route_desc* D, RouteArgs* a) {
@@ -83,6 +85,10 @@ sffn_status sffn_route_backward(const sffn_route_desc* desc, const float* dprobs
   if (T == 0) return SFFN_OK;
   if (!floats(logits, dtype) || ldl < a.E || !aligned(dprobs, 4) || !aligned(ids, 4) ||
       !floats(dlogits, dl_dtype) || lddl < a.E)
+    return SFFN_E_ARG;
+  const int e = elem(dtype), de = elem(dl_dtype);
+  if (meeting({logits, T, ldl * e, (int64_t)a.E * e, e},
+              {dlogits, T, lddl * de, (int64_t)a.E * de, de}) == kMixed)
     return SFFN_E_ARG;
   a.logits = logits;
   a.bf = dtype == SFFN_BF16;

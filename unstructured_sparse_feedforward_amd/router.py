@@ -84,7 +84,8 @@ class MoERouter:
                  dtype: torch.dtype = torch.float32, n_tokens: Optional[torch.Tensor] = None,
                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """The gradient of the logits [T, n_experts], of ``dtype`` (or in
-        ``out``), from ``dprobs`` [T, k] float32, that of the weights.
+        ``out``, which may be ``logits``), from ``dprobs`` [T, k] float32, that of
+        the weights.
         ``logits`` and ``ids`` are the forward call's. (The bias takes part in
         the choice alone and has no gradient.)"""
         T, ld, dt = self._logits(logits)

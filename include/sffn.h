@@ -493,9 +493,10 @@ sffn_status sffn_mx8_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int
  *   r = 1 / sqrt(mean(s^2) + eps),   y = s r w,
  * over rows of up to 16384 columns (SFFN_E_UNSUPPORTED above, and above 2^25
  * rows of up to 512 columns, 2^31 / n of more, n an eighth of the columns rounded
- * up to a power of two, at most 1024; the gradient's limit is 2^27 rows). The result is formed in float32 where it is bf16, in 64 bits where it
- * is float32 or MXFP8 (a row's squares must not overflow float32); the same call
- * repeats bit for bit, and a row's result does not depend on the other rows.
+ * up to a power of two, at most 1024; the gradient's limit is 2^27 rows). The
+ * result is formed in float32 where it is bf16 (whose range a row's squares may
+ * leave), in 64 bits where it is float32 or MXFP8; the same call repeats bit for
+ * bit, and a row's result does not depend on the other rows.
  * Every matrix is float32 or bf16 with contiguous rows, its own row stride
  * (>= cols elements) and no more than its elements' alignment.
  *   x             [rows, cols]
@@ -510,7 +511,8 @@ sffn_status sffn_mx8_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int
  *                 aligned; SFFN_MXFP8, ldo is not used) of the [rows, cols]
  *                 matrix, quantised from the float32 y
  *   out_scales    their scales (SFFN_MXFP8; else NULL)
- *   rstd          r [rows], nullable: the backward pass takes it
+ *   rstd          r [rows], nullable: the backward pass takes it (infinite
+ *                 where r is above float32: a root mean square below 2^-128)
  */
 typedef struct sffn_norm {
   const void* x;

@@ -402,3 +402,39 @@ def test_graphs_share_nothing():
             want = (*y, *sffn.rms_norm_backward(dy, y[1], rs, w, dstream=d))
             for a, b in zip(outs[k], want):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cols", [1, 8, 500, 1000, 2000, 4000, 8000, 16000])
+@pytest.mark.parametrize("eps", [0.0, 1e-42, 1e-33, 1e-6, 1e30])
+def test_squares_beyond_float32(cols, eps):
+    """Rows whose squares float32 cannot hold, of any result type; ordinary rows
+    between them as without them. Bounds as above, and r, which may be below
+    float32's normals but not below 2^-128, is off by 2^-150 at most, 4 u of itself;
+    below bfloat16's (float32's) normals a result by 2^-134 (2^-150) more."""
+    eps = float(np.float32(eps))
+    sizes = [1e-44, 1e-40, 1e-38, 1e-30, 1e-23, 1e-19, 1e-15, 1e-12, 1.0, 1e15, 1e19, 1e25, 1e30, 8e37]
+    x = torch.stack([_rand((cols,), i).clamp(-4, 4) * s for i, s in enumerate(sizes)])
+    x = torch.where(x == 0, torch.full_like(x, 1e-44), x)
+    x = torch.cat([x, x[-3:]])
+    x[-3:, ::2] *= 1e-30                          # large and small ones in one row
+    x[-3:, 0] = torch.tensor([1e25, 1e30, 3e38], device="cuda")
+    w = _rand((cols,), 99)
+    for xd in (F32, BF16):
+        xt = x.to(xd)
+        if eps == 0:
+            xt = xt[(xt != 0).any(1)]              # (a row of zeros has no norm)
+        ref, r = no.forward(_np(xt), _np(w), eps)
+        for dt in (BF16, F32):
+            rs = torch.empty(len(xt), device="cuda")
+            y = sffn.rms_norm(xt, w, eps=eps, dtype=dt, rstd=rs)
+            tol = 36 * U * np.abs(ref) + (2.0 ** -8 * np.abs(ref) * (1 + 36 * U) if dt == BF16 else 0)
+            assert (np.abs(_np(y) - ref) <= tol + 2.0 ** (-133 if dt == BF16 else -148)).all()
+            fits = r < 3.4e38
+            assert (np.abs(_np(rs) - r) <= 36 * U * r + 2.0 ** -148)[fits].all()
+            assert torch.isinf(rs[~torch.from_numpy(fits).cuda()]).all()
+        # a residual's sum, the norm in place of it
+        y, s = sffn.rms_norm(torch.zeros_like(xt), w, residual=xt, eps=eps)
+        assert torch.equal(s, xt) and torch.equal(y, sffn.rms_norm(xt, w, eps=eps))
+    mixed = torch.cat([x, _rand((9, cols), 5)])[torch.randperm(len(x) + 9, generator=torch.Generator().manual_seed(1))]
+    alone = torch.cat([sffn.rms_norm(row[None], w, eps=eps) for row in mixed])
+    assert torch.equal(sffn.rms_norm(mixed, w, eps=eps), alone)

@@ -9,7 +9,8 @@
 //   ds = r (g - xh mean(g xh)) + ds_in,    dw = sum over rows of dy xh.
 //
 // A row is read once and stays in registers between the sum of its squares
-// and the result. Sums are float32.
+// and the result. Sums are float32, those of results in float32 and MXFP8
+// float64.
 #include "mx.hpp"
 #include "norm.hpp"
 #include "rowio.hpp"
@@ -160,7 +161,7 @@ __device__ __forceinline__ void store_mx8(const NormArgs& a, int64_t row, int l,
 template <int L, int V, bool WIDE>
 __global__ __launch_bounds__(Row<L>::NT) void norm_kernel(NormArgs a) {
   typedef std::conditional_t<WIDE, double, float> T;
-  __shared__ T share[16];
+  __shared__ T share[WIDE ? 1 : 2][16];
   const int l = threadIdx.x % L;
   const int64_t row = (int64_t)blockIdx.x * Row<L>::ROWS + threadIdx.x / L;
   if (row >= a.rows || (a.n_dev && row >= *a.n_dev)) return;   // (all lanes of a row)
@@ -186,10 +187,41 @@ __global__ __launch_bounds__(Row<L>::NT) void norm_kernel(NormArgs a) {
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < CH; ++j) q = fma((T)s[i][j], (T)s[i][j], q);
-  T r = row_sum<L>(q, share);
-  if constexpr (WIDE) r = rsqrt(fma(r, a.inv_cols, (double)a.eps));
-  else r = 1.0f / sqrtf(r / (float)a.cols + a.eps);
-  if (a.rstd && l == 0) a.rstd[row] = (float)r;
+  T r = row_sum<L>(q, share[0]);
+  float rstd;
+  if constexpr (WIDE) {
+    r = rsqrt(fma(r, a.inv_cols, (double)a.eps));
+    rstd = (float)r;
+  } else {
+    r = r / (float)a.cols + a.eps;
+    // (a wave's lanes have one r; as bits, 2^-100 to infinity)
+    const uint32_t bits = __builtin_amdgcn_readfirstlane(__float_as_uint(r));
+    if (__builtin_expect(bits - 0x0D800000u >= 0x7F800000u - 0x0D800000u, 0)) {
+      // Squares that float32 does not hold: again those of s m. (Any other mean is
+      // off by at most 2^-150, half of float32's smallest step, of each square.)
+      // m of small ones stays with s, since r may be above float32; m of large ones
+      // goes to r, since s m would lose the row's smallest. (No other row's result
+      // changes; us with and without this, 8192 x 2048 bf16 26.1, 26.0, 1024 x
+      // 16384 33.7, 33.1.)
+      const bool small = r < 1.0f;
+      const float m = small ? 0x1p100f : 0x1p-100f;
+      q = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          q = fmaf(s[i][j] * m, s[i][j] * m, q);
+          if (small) s[i][j] *= m;
+        }
+      r = 1.0f / sqrtf(row_sum<L>(q, share[1]) / (float)a.cols + a.eps * m * m);
+      rstd = r * m;
+      if (!small) r = rstd;
+    } else {
+      r = 1.0f / sqrtf(r);
+      rstd = r;
+    }
+  }
+  if (a.rstd && l == 0) a.rstd[row] = rstd;
   if (a.weight) values(pw, a.w_bf, t);
 #pragma unroll
   for (int i = 0; i < V; ++i) {

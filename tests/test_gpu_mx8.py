@@ -275,3 +275,59 @@ def test_graph_and_streams():
         torch.cuda.synchronize()
         assert torch.equal(out, ref)
         assert torch.equal(sffn.mx_matmul(sffn.mx8_quantize(buf), w), ref)
+
+
+# one size for each kernel: few rows by 4 and by 8 waves, 32 x 64 and 64 x 64 tiles, 128 x 128,
+# 128 x 256 and 256 x 256 ones
+KERNELS = [(16, 500, 160), (16, 500, 4128), (256, 300, 160), (700, 2100, 160), (1000, 2100, 160),
+           (2100, 4100, 160), (4096, 3328, 1056)]
+
+
+def _device(mx, pack, codes, exps):
+    return mx(*(torch.from_numpy(v).cuda() for v in pack(codes, exps)), *codes.shape)
+
+
+@pytest.mark.parametrize("M,N,K", KERNELS)
+def test_wide_exponents_in_every_kernel(M, N, K):
+    """As test_wide_exponents_lose_nothing: multiples of 2^-10 below 2^13, of long
+    rows with 256 in some runs of 8 only."""
+    e = np.zeros((M, -(-K // 32)), np.int64)
+    c = _wide(M, K, M + N + K, 1 if K < 300 else 32 if K > 4000 else 8)
+    g = np.random.default_rng(N)
+    w = np.where(g.integers(0, 2, (N, K)) == 1, 0.5, 1.5) * g.choice([-1.0, 1.0], (N, K))
+    ref = torch.from_numpy(m8.values(c, e)).cuda() @ torch.from_numpy(w).cuda().t()
+    assert torch.equal(ref.float().double(), ref)        # the pin's own claim
+    out = sffn.mx_matmul(_device(sffn.MX8Tensor, m8.pack, c, e), sffn.mx_quantize(torch.from_numpy(w).float().cuda()))
+    assert torch.equal(out.double(), ref)
+
+
+@pytest.mark.parametrize("M,N,K", KERNELS)
+def test_every_code_in_every_kernel(M, N, K):
+    """Every e4m3 value against every e2m1 value, at several places of k; the NaN
+    codes make their rows NaN."""
+    va = np.array([m8.e4m3(i) for i in range(256)])
+    vb = m4.values(np.arange(16, dtype=np.uint8)[:, None], np.zeros((16, 1), np.int64))[:, 0]
+    for k in (0, 77, K - 1):
+        for first in range(0, 256, min(M, 256)):
+            ca, cb = np.zeros((M, K), np.uint8), np.zeros((N, K), np.uint8)
+            ca[:, k], cb[:, k] = (first + np.arange(M)) % 256, np.arange(N) % 16
+            out = sffn.mx_matmul(_device(sffn.MX8Tensor, m8.pack, ca, np.zeros((M, -(-K // 32)), np.int64)),
+                                 _device(sffn.MXTensor, m4.pack, cb, np.zeros((N, -(-K // 32)), np.int64)))
+            ref = torch.from_numpy(va[ca[:, k]][:, None] * vb[cb[:, k]][None]).cuda()
+            assert torch.equal(torch.isnan(out), torch.isnan(ref))
+            assert torch.equal(out.double().nan_to_num(), ref.nan_to_num())
+
+
+@pytest.mark.parametrize("M,N,K", KERNELS)
+def test_scales_in_every_kernel(M, N, K):
+    """Each block of k has its own scale in either operand, in every row."""
+    g = np.random.default_rng(1)
+    n = -(-K // 32)
+    ea, eb = g.integers(-20, 20, (M, n)), g.integers(-20, 20, (N, n))
+    for b in sorted({0, 1, 2, 3, 4, n // 2, n - 2, n - 1}):
+        ca, cb = np.zeros((M, K), np.uint8), np.zeros((N, K), np.uint8)
+        ca[:, 32 * b + b % 32] = 56          # 1
+        cb[:, 32 * b + b % 32] = 2           # 1
+        out = sffn.mx_matmul(_device(sffn.MX8Tensor, m8.pack, ca, ea), _device(sffn.MXTensor, m4.pack, cb, eb))
+        ref = torch.from_numpy(2.0 ** ea[:, b]).cuda()[:, None] * torch.from_numpy(2.0 ** eb[:, b]).cuda()[None]
+        assert torch.equal(out.double(), ref), b

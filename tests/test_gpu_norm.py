@@ -438,3 +438,16 @@ def test_squares_beyond_float32(cols, eps):
     mixed = torch.cat([x, _rand((9, cols), 5)])[torch.randperm(len(x) + 9, generator=torch.Generator().manual_seed(1))]
     alone = torch.cat([sffn.rms_norm(row[None], w, eps=eps) for row in mixed])
     assert torch.equal(sffn.rms_norm(mixed, w, eps=eps), alone)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 8193), (40, 16384), (600, 10000), (3, 5), (3000, 300), (2100, 2048),
+                                       (1100, 4096), (700, 6000)])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_gradient_in_place_by_rows(rows, cols, dt):
+    """ds in the place of each operand in the kernels that form ds and dw together."""
+    dy, s, r, w, d = _grads(rows, cols, dt, dt, di=dt)
+    ref, rdw = sffn.rms_norm_backward(dy, s, r, w, dstream=d, dtype=dt)
+    for i in range(3):
+        t = [dy.clone(), s.clone(), d.clone()]
+        got, dw = sffn.rms_norm_backward(t[0], t[1], r, w, dstream=t[2], out=t[i])
+        assert got is t[i] and torch.equal(got, ref) and torch.equal(dw, rdw)

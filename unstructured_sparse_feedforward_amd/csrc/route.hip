@@ -565,6 +565,12 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs a) {
   }
 }
 
+// 1 / v of a normal v, to a step: the hardware's, and one of Newton's steps
+__device__ __forceinline__ float reciprocal(float v) {
+  const float r = __builtin_amdgcn_rcpf(v);
+  return fmaf(fmaf(-v, r, 1.0f), r, r);
+}
+
 // The logits' gradient. With g_r = scale dp_r of the chosen experts,
 //   scores' gradient: normalised ds_r = (g_r - sum_q g_q s_q / S) / S, S the
 //   sum of the chosen s, else ds_r = g_r; 0 for the others
@@ -608,10 +614,8 @@ __global__ __launch_bounds__(kWaves * 64) void route_grad_kernel(RouteArgs a) {
     dr = g;
   } else if (a.sigmoid) {
     // s and 1 - s are z = 1 / (1 + e) and e z with e = exp(-|l|), in one order or
-    // the other; e by its root, which float32 holds down to |l| = 174. (The
-    // hardware's reciprocal is within a step, of values from 1/2 to 32.)
-    const float root = expf(-0.5f * fabsf(lr)), e = root * root;
-    const float z = __builtin_amdgcn_rcpf(1.0f + e);
+    // the other
+    const float e = expf(-fabsf(lr)), z = reciprocal(1.0f + e);
     if (a.normalize) {
       // q relative to the largest score: of logits far below -87 float32 has
       // neither s nor 1 / S (of logits below -709.78 the forward pass' 64 bits have
@@ -619,10 +623,14 @@ __global__ __launch_bounds__(kWaves * 64) void route_grad_kernel(RouteArgs a) {
       const float m = wave_max(lr), h = fminf(m, 0.0f);
       float q = id >= 0 && m > -709.7827f ? (lr > 0.0f ? z : expf(lr - h) * z) : 0.0f;
       const float S = wave_sum(q);
-      q *= S == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(S);
+      q *= S == 0.0f ? 0.0f : reciprocal(S);
       dr = q * (lr > 0.0f ? e * z : z) * (g - wave_sum(g * q));
     } else {
-      dr = root * g * (root * (z * z));
+      dr = g * (e * (z * z));
+      if (fabsf(lr) > 80.0f) {      // e below float32's normals, but g e need not be
+        const float root = expf(-0.5f * fabsf(lr));
+        dr = root * g * (root * (z * z));
+      }
     }
   } else {
     const float m = wave_max(lr);

@@ -554,7 +554,8 @@ sffn_status sffn_rms_norm(const sffn_norm* norm, int64_t rows, int64_t cols, flo
  *            of more than one row, row stride; has no byte in common with any
  *            otherwise (SFFN_E_ARG)
  *   dweight  [cols] float32, nullable (NULL without a weight); written by
- *            rows == 0 too (zeros)
+ *            rows == 0 too (zeros); not the weight's memory (SFFN_E_ARG), nor any
+ *            other operand's
  * Sums are float32, of rows in an order that depends on the sizes alone.
  */
 typedef struct sffn_norm_grad {

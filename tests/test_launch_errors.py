@@ -51,7 +51,7 @@ elif which == "norm":
     for rows, cols, out in itertools.product((1, 700, 9000), COLS, (0, 1, 3)):
         a = B.SffnNorm(P, P, P, P, P << 20, P if out == 3 else None, P, cols, cols, cols, cols, 0, 0, 0, out)
         check(("norm", rows, cols, out), lambda: lib.sffn_rms_norm(R(a), rows, cols, 1e-6, None, None))
-    for rows, cols, ds, dw in itertools.product((0, 1, 700, 9000), COLS, (P, P << 20), (None, P)):
+    for rows, cols, ds, dw in itertools.product((0, 1, 700, 9000), COLS, (P, P << 20), (None, P << 21)):
         if rows == 0 and dw is None:
             continue
         a = B.SffnNormGrad(P, P << 10, None, P, P, ds, dw, cols, cols, cols, cols, 0, 0, 0, 0, 0)

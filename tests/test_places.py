@@ -80,6 +80,10 @@ for n in range(20000):
     a = B.SffnNormGrad(dy.at, s.at, di and di.at, P << 11, P << 12, ds.at, P << 13, dy.ld, s.ld,
                        di.ld if di else 0, ds.ld, dy.dtype, s.dtype, di.dtype if di else 0, 0, ds.dtype)
     bad = any(p is not None and ds.meets(p) == 2 for p in (dy, s, di))
+    if rng.random() < 0.2:       # the weight and its gradient, float32 or bfloat16 and float32
+        wd = rng.randrange(2)
+        a.weight, a.weight_dtype, a.dweight = P << 13, wd, (P << 13) + 4 * rng.randrange(-12, 13)
+        bad = bad or a.weight < a.dweight + 4 * cols and a.dweight < a.weight + cols * SIZE[wd]
     check("norm grad", lib.sffn_rms_norm_backward(R(a), rows, cols, P << 14, 1 << 20, None), bad, dy, s,
           di, ds)
 

@@ -128,7 +128,9 @@ sffn_status sffn_rms_norm_backward(const sffn_norm_grad* n, int64_t rows, int64_
   const Meeting dy_ds = meeting(ds, place(n->dy, n->dy_dtype, n->lddy, rows, cols));
   const Meeting s_ds = meeting(ds, place(n->s, n->s_dtype, n->lds, rows, cols));
   if (dy_ds == kMixed || s_ds == kMixed ||
-      meeting(ds, place(n->dstream, n->dstream_dtype, n->lddstream, rows, cols)) == kMixed)
+      meeting(ds, place(n->dstream, n->dstream_dtype, n->lddstream, rows, cols)) == kMixed ||
+      meeting(place(n->dweight, SFFN_F32, cols, 1, cols),
+              place(n->weight, n->weight_dtype, cols, 1, cols)) != kApart)
     return SFFN_E_ARG;
   NormGradArgs a = {};
   a.dy = n->dy;

@@ -73,6 +73,7 @@ typedef int32_t sffn_status;
 #define SFFN_BF16 1
 /* element type of an expert layer's weights (microscaled 4-bit, below) */
 #define SFFN_MXFP4 2
+/* a form of the norm's result (microscaled 8-bit, below) */
 #define SFFN_MXFP8 3
 
 /* forward modes */
@@ -556,7 +557,9 @@ sffn_status sffn_rms_norm(const sffn_norm* norm, int64_t rows, int64_t cols, flo
  *   dweight  [cols] float32, nullable (NULL without a weight); written by
  *            rows == 0 too (zeros); not the weight's memory (SFFN_E_ARG), nor any
  *            other operand's
- * Sums are float32, of rows in an order that depends on the sizes alone.
+ * Sums are float32, of rows in an order that depends on the sizes alone. Every one
+ * of the `rows` rows counts: after a forward pass with n_rows, whose s and rstd of
+ * the other rows are left as they were, rows is that number.
  */
 typedef struct sffn_norm_grad {
   const void* dy;

@@ -590,11 +590,12 @@ __global__ __launch_bounds__(256, (Big<MI, NJ, NS>::WGS)) void mx8_big_kernel(Mx
 //                rounds of the CUs to 7/8, since their copies of a serve 64 rows
 //                of b, the few rows' 16: 8 x 16384 x 4096 10.4, few rows 11.6; 16
 //                x 16384 x 4096 11.1, 13.0 (16 x 16384 x 2048 7.9, 8.1; 8 x 14336
-//                x 2048 7.3, 7.0). And up to one a CU: 256 x 2048 x 2048 6.4, 64 x
+//                x 2048 7.3, 7.0). And up to 256 tiles: 256 x 2048 x 2048 6.4, 64 x
 //                64 8.5; 128 x 2048 x 8192 11.1, 15.5
-//   64 x 64:     up to two a CU: 300 x 3000 x 2048 9.7, 32 x 64 10.9; 512 x 2048 x
-//                5632 15.0, 16.1; 512 x 4096 x 8192 37.7, 128 x 128 50.0; 1024 x
-//                2048 x 2048 16.7, 16.9
+//   64 x 64:     up to 512 tiles, two rounds of the CUs (a workgroup fills one):
+//                300 x 3000 x 2048 9.7, 32 x 64 10.9; 512 x 2048 x 5632 15.0, 16.1;
+//                512 x 4096 x 8192 37.7, 128 x 128 50.0; 1024 x 2048 x 2048 16.7,
+//                16.9
 //   128 x 128:   up to 256: 640 x 4096 x 2048 16.6, 64 x 64 22.2; 1024 x 4096 x
 //                2048 19.1, 128 x 256 24.4
 //   128 x 256:   two workgroups a CU, one stores while the other multiplies: 2048
@@ -604,7 +605,7 @@ __global__ __launch_bounds__(256, (Big<MI, NJ, NS>::WGS)) void mx8_big_kernel(Mx
 //                longer than 1024 (4096 x 4096 x 1024 32.6, 128 x 256 31.2): 8192
 //                x 5632 x 2048 136, 138; 8192 x 8192 x 8192 643 (1.71 PFLOP/s, two
 //                instructions for every product), 670. Matrix instructions alone,
-//                on random operands, run at 3.4 to 3.7 PFLOP/s here (power).
+//                on random operands, run at 3.3 to 3.8 PFLOP/s here (power).
 template <typename O>
 hipError_t launch(const MxGemmArgs& g, hipStream_t s) {
   const auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };

@@ -320,8 +320,8 @@ __device__ __forceinline__ int choose64(const RouteArgs& a, int64_t t, float m, 
 // (24 + 16 + 6) u; a reciprocal and a product. c is off by u |c| more. So two c
 // whose difference is more than 2^-20 (2^-16 times the largest score) + 2^-23
 // times their size are in the order of the exact ones, and two sums of two
-// where it is more than twice that and 2^-22 times their size. Without a bias the experts' keys are the
-// logits themselves, which are exact.
+// where it is more than twice that and 2^-22 times their size. Without a bias
+// the experts' keys are the logits themselves, which are exact.
 template <int N, int LPT, bool BIAS, bool GROUPED>
 __device__ __forceinline__ int choose32(const RouteArgs& a, int64_t t, const float (&l)[N],
                                         float m, char* cs64, int* ids, bool* sure) {

@@ -56,8 +56,8 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     type. With a residual (result, s) is returned, s rounded to the residual's
     type, the norm being that of the rounded sum; it is made here or is
     ``residual_out``, which may be the residual itself (``out`` and
-    ``residual_out`` either are an operand, rows in the same places, or share no
-    memory with one). ``rstd`` [rows] float32
+    ``residual_out`` are either an operand, rows in the same places, or share no
+    memory with any). ``rstd`` [rows] float32
     receives 1 / sqrt(mean(s^2) + eps) for :func:`rms_norm_backward`.
     ``n_rows``, an int32 tensor of one element on the GPU, says how many of the
     rows count: the results of the others are left as they were."""
@@ -119,8 +119,8 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, rstd: torch.Tensor,
     and ``rstd`` what the forward call wrote. ds, the gradient of x and of the
     residual alike, has ``dstream`` added, the gradient that reaches s from
     elsewhere; it is of ``dtype``, or ``out`` (which may be dy, s or dstream, and
-    shares no memory with them otherwise).
-    dweight [cols] float32 (``dweight`` when given) is None without a
+    shares no memory with them otherwise). Every row counts: after a forward call
+    with ``n_rows`` pass the valid ones alone. dweight [cols] float32 (``dweight`` when given) is None without a
     weight."""
     rows, cols, lddy, yd = _matrix(dy, "dy")
     dev = dy.device
